@@ -86,11 +86,13 @@ typedef enum {
     TL_ERR_LAUNCH = 6,   /* the HIP launch failed; see tl_last_error()         */
     TL_ERR_DTYPE = 7,    /* unknown output dtype                               */
     TL_ERR_WORKSPACE = 8, /* workspace missing or smaller than the call needs  */
-    TL_ERR_DATA = 9      /* invalid packed bytes found (only with TL_DEBUG=1)  */
+    TL_ERR_DATA = 9,     /* invalid packed bytes found (only with TL_DEBUG=1)  */
+    TL_ERR_VALUE = 10    /* a number argument is out of range (see each call)  */
 } tl_status;
 
 enum { TL_FMT_TRIT5 = 0, TL_FMT_SLOT2 = 1, TL_FMT_BIT1 = 2 };
-enum { TL_F32 = 0, TL_F16 = 1 };
+/* element types; the ternary calls take the first two only */
+enum { TL_F32 = 0, TL_F16 = 1, TL_BF16 = 2, TL_I8 = 3 };
 
 #define TL_BLOCK 1024      /* Hadamard block width                 */
 #define TL_GROUP 128       /* weights per scale                    */
@@ -311,6 +313,108 @@ TL_API tl_status tl_gemm_bf16(const uint8_t* packed, const uint16_t* scales, int
  * bitwise reproducible; codes then go to tl_pack. */
 TL_API tl_status tl_quantize(const float* w, const int8_t* signs, int64_t N, int64_t K,
                              int8_t* codes, uint16_t* scales, hipStream_t stream);
+
+/* ---- around the ternary linears: the norm in front of them, and matrices
+ * held in 4 bits where ternary codes do not suit (the embedding and the head
+ * are rounded apart from the large linears: page "OpenBonsai", section "How
+ * it works", step 2) ---- */
+
+/* Residual addition, root-mean-square norm and gain of M rows, and on demand
+ * the signed rotation that the ternary linear behind the norm needs (the
+ * Persian page, paragraph 3), in one pass:
+ *   h = x + residual, rounded to x_dtype (h = x without a residual),
+ *   y[m, k] = h[m, k] / sqrt(mean_k h[m, k]^2 + eps) * gain[k],
+ *   out = y, or R(y) (tl_hadamard_rotate's map) when signs is given.
+ * x, residual (NULL: none), sum_out: [M, K] and gain: [K], all of x_dtype
+ * (TL_F32, TL_F16 or TL_BF16).  sum_out receives h (NULL: not stored; without
+ * a residual it must be NULL: TL_ERR_NULL).  signs: int8 [K] (negative = -1)
+ * or NULL.  out: [M, K] of out_dtype.
+ *   TL_F32, TL_F16, TL_BF16: computed in fp32, rounded once to nearest even;
+ *     out_scales must be NULL (TL_ERR_DTYPE).
+ *   TL_I8: for each 128 consecutive values of a row with a = max |value|,
+ *     out_scales (fp32 [M, K/128]) = a / 127 and the code is the integer
+ *     nearest to 127 * value / a, ties to even (0 where a = 0); out =
+ *     code * scale is what tl_q4_gemv reads.  Without the rotation the codes
+ *     follow exactly from h and gain (decided in 64 bits at ties and near
+ *     them).  A group that holds an infinity or a NaN gets codes 0 and the
+ *     scale NaN.
+ * Sums are fp32: a row whose h^2 overflow fp32 (|h| above about 1.8e19) gives
+ * 0.  Bitwise reproducible from call to call.
+ * Requires 1 <= M <= 2^24, 8 <= K <= TL_MAX_K, K % 8 == 0 (K % 1024 == 0 with
+ * signs, K % 128 == 0 with TL_I8), M * K <= 2^36; eps a positive normal fp32
+ * number (TL_ERR_VALUE); every pointer 16-byte aligned, out_scales 4-byte.  sum_out may equal x
+ * or residual (in place) but must not otherwise overlap them, and sum_out,
+ * out and out_scales must overlap neither each other nor another input. */
+TL_API tl_status tl_rms_norm(const void* x, const void* residual, const void* gain,
+                             const int8_t* signs, int64_t M, int64_t K, int32_t x_dtype, float eps,
+                             void* sum_out, void* out, int32_t out_dtype, float* out_scales,
+                             hipStream_t stream);
+
+/* 4-bit weights ("q4"): codes in -8 .. 7 as 4-bit two's complement, one
+ * binary16 scale per `group` (32, 64 or 128) consecutive weights of a row;
+ * weight (n, k) = code * scales[n, k / group].  Each row holds K/2 bytes: of
+ * the 8 weights k0 .. k7 of a little-endian 32-bit word, the even ones lie in
+ * its low half and the odd ones in its high half, k(2i) at bits 4i .. 4i + 3
+ * and k(2i + 1) at bits 16 + 4i .. 19 + 4i (shifting the word by 4i puts two
+ * neighbouring weights at the bottom of its two halves).  Every byte is a
+ * valid encoding.  scales: [N, K/group].  4.125 bits per weight at 128. */
+
+/* Bytes of the packed codes of an N x K q4 weight; -1 when N < 1, K < 128 or
+ * K % 128 != 0.  Host only. */
+TL_API int64_t tl_q4_packed_bytes(int64_t N, int64_t K);
+
+/* Round weight rows to q4, after the signed rotation of the rows when signs
+ * is given (the weights of a linear whose activations are rotated):
+ *   a = max |w| over the group, scale = binary16(a / 7) (at most 65504),
+ *   code = the integer nearest to w / scale, ties to even, held to -8 .. 7
+ *   (0 where the scale is 0).
+ * A group that holds an infinity or a NaN gets codes 0 and the scale NaN.
+ * w: [N, K] of w_dtype (TL_F32, TL_F16 or TL_BF16); signs: int8 [K] (negative
+ * = -1) or NULL; packed: tl_q4_packed_bytes(N, K) bytes; scales: binary16
+ * [N, K/group].  Without the rotation codes and scales follow exactly from w;
+ * with it the rotation is fp32.  Bitwise reproducible.  Requires
+ * 1 <= N <= 2^24, 128 <= K <= TL_MAX_K, K % 128 == 0 (K % 1024 == 0 with
+ * signs), N * K <= 2^36, group 32, 64 or 128 (TL_ERR_FORMAT); every pointer
+ * 16-byte aligned; packed and scales overlap nothing else. */
+TL_API tl_status tl_q4_quantize(const void* w, const int8_t* signs, int64_t N, int64_t K,
+                                int32_t w_dtype, int32_t group, uint8_t* packed, uint16_t* scales,
+                                hipStream_t stream);
+
+/* The values of q4 weights: w[n, k] = code * scale, rounded to nearest even in
+ * w_dtype (exact in TL_F32).  Shape, group and alignment rules as
+ * tl_q4_quantize; w: [N, K] of w_dtype, overlapping neither input. */
+TL_API tl_status tl_q4_dequantize(const uint8_t* packed, const uint16_t* scales, int64_t N,
+                                  int64_t K, int32_t group, void* w, int32_t w_dtype,
+                                  hipStream_t stream);
+
+/* Bytes of device workspace tl_q4_gemv needs for this shape (0: none; none is
+ * ever needed at M <= 16).  Host only; it depends on the compute-unit count
+ * of the current device.  -1 when the shape is not accepted. */
+TL_API int64_t tl_q4_gemv_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* Product with q4 weights (decode shapes):
+ *   y[m, n] = sum_k x[m, k] * code[n, k] * scales[n, k / group]
+ * x: [M, K] of x_dtype: TL_F16, TL_BF16, or TL_I8 with x_scales (fp32
+ * [M, K/128], tl_rms_norm's; value = code * x_scales[m, k / 128]; -128 is a
+ * valid code); x_scales must be NULL for the other types (TL_ERR_DTYPE).  y:
+ * [M, N] of y_dtype (TL_F32, TL_F16 or TL_BF16, rounded once to nearest even).
+ * Products of codes and activations are exact and summed in fp32 (binary16,
+ * bfloat16) or exactly (8 bits) within a group, groups in fp32.  bfloat16
+ * activations are taken exactly except those below 2^-28 of the largest of
+ * their 128, which count as 0; where one of the 128 is an infinity or a NaN,
+ * the token's outputs are NaN.  A token's result is the same bits whatever
+ * the other tokens hold, and from call to call.
+ * Requires 1 <= M, N <= 2^24, 128 <= K <= TL_MAX_K, K % 128 == 0, M * K, N * K
+ * and M * N <= 2^36, group 32, 64 or 128 (TL_ERR_FORMAT).  Tuned for M <= 64;
+ * any M is accepted.  workspace: tl_q4_gemv_workspace_bytes(M, N, K) bytes
+ * (may be NULL when that is 0; TL_ERR_WORKSPACE); its contents on entry do
+ * not matter, and calls that may run at the same time need separate ones.
+ * Every pointer 16-byte aligned, x_scales 4-byte; y and workspace overlap
+ * nothing else. */
+TL_API tl_status tl_q4_gemv(const uint8_t* packed, const uint16_t* scales, int32_t group,
+                            const void* x, int32_t x_dtype, const float* x_scales, int64_t M,
+                            int64_t N, int64_t K, void* y, int32_t y_dtype, void* workspace,
+                            int64_t workspace_bytes, hipStream_t stream);
 
 /* Static name of a status code ("TL_OK", ...). */
 TL_API const char* tl_status_str(tl_status status);

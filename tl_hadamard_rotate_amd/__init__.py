@@ -22,12 +22,14 @@ FMT_SLOT2 = 1
 FMT_BIT1 = 2
 TL_F32 = 0
 TL_F16 = 1
+TL_BF16 = 2
+TL_I8 = 3
 BLOCK = 1024
 GROUP = 128
 
 _STATUS = {0: "TL_OK", 1: "TL_ERR_NULL", 2: "TL_ERR_SHAPE", 3: "TL_ERR_FORMAT",
            4: "TL_ERR_ALIGN", 5: "TL_ERR_ALIAS", 6: "TL_ERR_LAUNCH", 7: "TL_ERR_DTYPE",
-           8: "TL_ERR_WORKSPACE", 9: "TL_ERR_DATA"}
+           8: "TL_ERR_WORKSPACE", 9: "TL_ERR_DATA", 10: "TL_ERR_VALUE"}
 
 _lib = None
 
@@ -50,7 +52,7 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"{LIB_PATH} is missing: build it with "
                                "`python -m tl_hadamard_rotate_amd.build`")
         L = ctypes.CDLL(LIB_PATH)
-        p, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+        p, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
         sig = {
             "tl_packed_bytes": (i64, [i64, i64, i32]),
             "tl_pack": (i32, [p, i64, i64, i32, p, p, p]),
@@ -69,6 +71,12 @@ def lib() -> ctypes.CDLL:
             "tl_chain_sync_bytes": (i64, [i32]),
             "tl_chain_encode": (i32, [p, i32, p, i64]),
             "tl_linear_chain": (i32, [p, i32, p, p]),
+            "tl_rms_norm": (i32, [p, p, p, p, i64, i64, i32, f32, p, p, i32, p, p]),
+            "tl_q4_packed_bytes": (i64, [i64, i64]),
+            "tl_q4_quantize": (i32, [p, p, i64, i64, i32, i32, p, p, p]),
+            "tl_q4_dequantize": (i32, [p, p, i64, i64, i32, p, i32, p]),
+            "tl_q4_gemv_workspace_bytes": (i64, [i64, i64, i64]),
+            "tl_q4_gemv": (i32, [p, p, i32, p, i32, p, i64, i64, i64, p, i32, p, i64, p]),
             "tl_status_str": (ctypes.c_char_p, [i32]),
             "tl_last_error": (ctypes.c_char_p, []),
         }
@@ -308,6 +316,241 @@ def linear(packed, scales, fmt, x, signs, out_dtype=torch.float32, out=None,
     _check("tl_linear", lib().tl_linear(_ptr(packed), _ptr(scales), fmt, _ptr(x), _ptr(signs), m,
                                         n, k, _ptr(x_rot), _ptr(out), yd, wp, wb, _stream(x)))
     return out
+
+
+_REAL = {torch.float32: TL_F32, torch.float16: TL_F16, torch.bfloat16: TL_BF16}
+
+
+def _need_like(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device) -> None:
+    """A contiguous device tensor of this type and shape, on this device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _need_real(t: torch.Tensor, name: str) -> int:
+    """The TL_ type of a contiguous 2-D device tensor of real numbers."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _REAL:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    if not t.is_cuda or t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 2-D device tensor")
+    return _REAL[t.dtype]
+
+
+def _call(name: str, device: torch.device, *args) -> None:
+    """One library call on the device's current stream, with that device
+    current (a stream and the look-ups of a launch belong to a device)."""
+    fn = getattr(_lib or lib(), name)
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, stream)
+    if st != 0:
+        _check(name, st)
+
+
+def _rms_norm(x, gain, eps, residual, signs, sum_out, out, out_dtype, out_scales):
+    dt = _need_real(x, "x")
+    device, shape = x.device, x.shape
+    m, k = shape
+    _need_like(gain, "gain", x.dtype, (k,), device)
+    if residual is not None:
+        _need_like(residual, "residual", x.dtype, shape, device)
+        if sum_out is None:
+            sum_out = torch.empty_like(x)
+        else:
+            _need_like(sum_out, "sum_out", x.dtype, shape, device)
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    if signs is not None:
+        _need_like(signs, "signs", torch.int8, (k,), device)
+    _call("tl_rms_norm", device, x.data_ptr(), None if residual is None else residual.data_ptr(),
+          gain.data_ptr(), None if signs is None else signs.data_ptr(), m, k, dt, eps,
+          None if sum_out is None else sum_out.data_ptr(), out.data_ptr(), out_dtype,
+          None if out_scales is None else out_scales.data_ptr())
+    return sum_out
+
+
+def rms_norm(x, gain, eps, residual=None, signs=None, out_dtype=torch.float16, sum_out=None,
+             out=None):
+    """Root-mean-square norm of the rows of x [M, K] (float32, float16 or
+    bfloat16), with the addition of ``residual`` in front and, with ``signs``,
+    the signed rotation of the ternary linear behind it: ``out`` is then its
+    x_rot (see tl_rms_norm).  Returns out, or (out, sum) with a residual; the
+    sum x + residual goes to ``sum_out``, which may be x or residual itself."""
+    yd = _REAL.get(out_dtype)
+    if yd is None:
+        raise TypeError("out_dtype must be float32, float16 or bfloat16 (8 bits: rms_norm_i8)")
+    _need_real(x, "x")
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
+    else:
+        _need_like(out, "out", out_dtype, x.shape, x.device)
+    s = _rms_norm(x, gain, eps, residual, signs, sum_out, out, yd, None)
+    return out if s is None else (out, s)
+
+
+def rms_norm_i8(x, gain, eps, residual=None, signs=None, sum_out=None, out=None, scales=None):
+    """``rms_norm`` with 8-bit outputs for ``q4_gemv``: returns (codes int8
+    [M, K], scales float32 [M, K/128]), and the sum behind them with a
+    residual; value = code * scale of its 128."""
+    _need_real(x, "x")
+    m, k = x.shape
+    if k % GROUP:
+        raise ValueError("K must be a multiple of 128")
+    if out is None:
+        out = torch.empty((m, k), dtype=torch.int8, device=x.device)
+    else:
+        _need_like(out, "out", torch.int8, (m, k), x.device)
+    if scales is None:
+        scales = torch.empty((m, k // GROUP), dtype=torch.float32, device=x.device)
+    else:
+        _need_like(scales, "scales", torch.float32, (m, k // GROUP), x.device)
+    s = _rms_norm(x, gain, eps, residual, signs, sum_out, out, TL_I8, scales)
+    return (out, scales) if s is None else (out, scales, s)
+
+
+def q4_packed_bytes(n: int, k: int) -> int:
+    return int(lib().tl_q4_packed_bytes(n, k))
+
+
+def q4_quantize(w, group=GROUP, signs=None, packed=None, scales=None):
+    """Weight rows w [N, K] to 4-bit codes with a binary16 scale per ``group``
+    (32, 64 or 128) weights, after the signed rotation of the rows when
+    ``signs`` is given: returns (packed uint8 [N, K/2], scales float16
+    [N, K/group]); the layout is in include/tl.h."""
+    dt = _need_real(w, "w")
+    n, k = w.shape
+    if group not in (32, 64, 128) or k % GROUP:
+        raise ValueError("group must be 32, 64 or 128 and K a multiple of 128")
+    if signs is not None:
+        _need_like(signs, "signs", torch.int8, (k,), w.device)
+    if packed is None:
+        packed = torch.empty((n, k // 2), dtype=torch.uint8, device=w.device)
+    else:
+        _need_like(packed, "packed", torch.uint8, (n, k // 2), w.device)
+    if scales is None:
+        scales = torch.empty((n, k // group), dtype=torch.float16, device=w.device)
+    else:
+        _need_like(scales, "scales", torch.float16, (n, k // group), w.device)
+    _call("tl_q4_quantize", w.device, w.data_ptr(), None if signs is None else signs.data_ptr(), n, k,
+          dt, group, packed.data_ptr(), scales.data_ptr())
+    return packed, scales
+
+
+def _q4_shape(packed, scales):
+    """(N, K, group) of packed 4-bit weights and their scales."""
+    if not isinstance(packed, torch.Tensor) or not isinstance(scales, torch.Tensor):
+        raise TypeError("packed and scales must be torch.Tensors")
+    if packed.dtype != torch.uint8 or scales.dtype != torch.float16:
+        raise TypeError("packed must be uint8 and scales float16")
+    if not packed.is_cuda or scales.device != packed.device:
+        raise ValueError("packed and scales must be device tensors, on the same device")
+    if packed.dim() != 2 or scales.dim() != 2 or not packed.is_contiguous() or \
+            not scales.is_contiguous():
+        raise ValueError("packed and scales must be contiguous with 2 dims")
+    n, half = packed.shape
+    groups = scales.shape[1]
+    k = 2 * half
+    if scales.shape[0] != n or k % GROUP or not groups or k // groups not in (32, 64, 128) or k % groups:
+        raise ValueError(f"packed {tuple(packed.shape)} and scales {tuple(scales.shape)} must be "
+                         "[N, K/2] and [N, K/group], group 32, 64 or 128, K a multiple of 128")
+    return n, k, k // groups
+
+
+def q4_dequantize(packed, scales, out_dtype=torch.float16, out=None) -> torch.Tensor:
+    """The weights [N, K] that 4-bit codes and scales stand for."""
+    n, k, group = _q4_shape(packed, scales)
+    dt = _REAL.get(out_dtype)
+    if dt is None:
+        raise TypeError("out_dtype must be float32, float16 or bfloat16")
+    if out is None:
+        out = torch.empty((n, k), dtype=out_dtype, device=packed.device)
+    else:
+        _need_like(out, "out", out_dtype, (n, k), packed.device)
+    _call("tl_q4_dequantize", packed.device, packed.data_ptr(), scales.data_ptr(), n, k, group,
+          out.data_ptr(), dt)
+    return out
+
+
+def q4_gemv_workspace_bytes(m: int, n: int, k: int) -> int:
+    """Device workspace bytes tl_q4_gemv needs (0 at M <= 16)."""
+    b = int(lib().tl_q4_gemv_workspace_bytes(m, n, k))
+    if b < 0:
+        raise TLError("tl_q4_gemv_workspace_bytes", 2)
+    return b
+
+
+def q4_gemv(packed, scales, x, x_scales=None, out_dtype=torch.float32, out=None,
+            workspace=None) -> torch.Tensor:
+    """y[M, N] = x . dequant4(packed, scales)^T for few tokens (M <= 64): x
+    [M, K] float16 or bfloat16, or int8 with ``x_scales`` float32 [M, K/128]
+    (``rms_norm_i8``).  ``workspace`` (uint8, at least
+    ``q4_gemv_workspace_bytes``) is taken from torch's allocator when not given."""
+    n, k, group = _q4_shape(packed, scales)
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    device = packed.device
+    if x.device != device or x.dim() != 2 or x.shape[1] != k or not x.is_contiguous():
+        raise ValueError(f"x must be a contiguous [M, {k}] tensor on {device}")
+    m = x.shape[0]
+    if x.dtype == torch.int8:
+        xd = TL_I8
+        if x_scales is None:
+            raise ValueError("int8 activations need x_scales")
+        _need_like(x_scales, "x_scales", torch.float32, (m, k // GROUP), device)
+    else:
+        xd = _REAL.get(x.dtype)
+        if xd is None or xd == TL_F32:
+            raise TypeError(f"x must be float16, bfloat16 or int8, got {x.dtype}")
+        if x_scales is not None:
+            raise ValueError("x_scales go with int8 activations")
+    yd = _REAL.get(out_dtype)
+    if yd is None:
+        raise TypeError("out_dtype must be float32, float16 or bfloat16")
+    if out is None:
+        out = torch.empty((m, n), dtype=out_dtype, device=device)
+    else:
+        _need_like(out, "out", out_dtype, (m, n), device)
+    wb = 0
+    if workspace is not None:
+        wb = workspace.numel()
+        _need_like(workspace, "workspace", torch.uint8, (wb,), device)
+    elif m > 16:
+        with torch.cuda.device(device):
+            wb = q4_gemv_workspace_bytes(m, n, k)
+        workspace = torch.empty(wb, dtype=torch.uint8, device=device) if wb else None
+    _call("tl_q4_gemv", device, packed.data_ptr(), scales.data_ptr(), group, x.data_ptr(), xd,
+          None if x_scales is None else x_scales.data_ptr(), m, n, k, out.data_ptr(), yd,
+          None if workspace is None else workspace.data_ptr(), wb)
+    return out
+
+
+class Q4Linear:
+    """A linear layer with 4-bit weights and group scales, for the matrices
+    beside the ternary ones.  With ``signs`` the weights carry the folded
+    rotation (``q4_quantize`` with the same signs) and ``forward`` rotates its
+    float16 input first, as ``TernaryLinear`` does; int8 input with scales
+    (``rms_norm_i8``) has been rotated there."""
+
+    def __init__(self, packed, scales, signs=None):
+        self.packed, self.scales, self.signs = packed, scales, signs
+
+    def forward(self, x: torch.Tensor, x_scales=None, out_dtype=torch.float32) -> torch.Tensor:
+        if self.signs is not None and x.dtype != torch.int8:
+            x = hadamard_rotate(x, self.signs)
+        return q4_gemv(self.packed, self.scales, x, x_scales, out_dtype)
+
+    __call__ = forward
 
 
 class TernaryLinear:

@@ -1,0 +1,122 @@
+// Element types of the norm and the 4-bit calls: 8 consecutive elements to
+// and from fp32, and the signed rotation of a 1024-block held by one wave.
+#pragma once
+
+#include "tl_internal.h"
+
+namespace tl {
+namespace elem {
+
+struct F32 {
+    static constexpr int kType = TL_F32, kBytes = 4;
+};
+struct F16 {
+    static constexpr int kType = TL_F16, kBytes = 2;
+};
+struct BF16 {
+    static constexpr int kType = TL_BF16, kBytes = 2;
+};
+
+__device__ __forceinline__ uint32_t f16_bits(float f) {
+    return uint32_t(__builtin_bit_cast(uint16_t, _Float16(f)));
+}
+
+// fp32 -> bfloat16, nearest even; a NaN stays one
+__device__ __forceinline__ uint32_t bf16_bits(float f) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, f);
+    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (u >> 16) | 0x40u;
+    return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+}
+
+template <typename T>
+__device__ __forceinline__ float round_to(float f) {
+    if (T::kType == TL_F16) return float(_Float16(f));
+    if (T::kType == TL_BF16) return __builtin_bit_cast(float, bf16_bits(f) << 16);
+    return f;
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
+    if (T::kType == TL_F32) {
+        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+        const float4 a = q[0], b = q[1];
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+        const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (T::kType == TL_F16) {
+                v[2 * j] = float(__builtin_bit_cast(_Float16, uint16_t(w[j])));
+                v[2 * j + 1] = float(__builtin_bit_cast(_Float16, uint16_t(w[j] >> 16)));
+            } else {
+                v[2 * j] = __builtin_bit_cast(float, w[j] << 16);
+                v[2 * j + 1] = __builtin_bit_cast(float, w[j] & 0xFFFF0000u);
+            }
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) {
+    if (T::kType == TL_F32) {
+        float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+        q[0] = float4{v[0], v[1], v[2], v[3]};
+        q[1] = float4{v[4], v[5], v[6], v[7]};
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] = T::kType == TL_F16 ? f16_bits(v[2 * j]) | f16_bits(v[2 * j + 1]) << 16
+                                      : bf16_bits(v[2 * j]) | bf16_bits(v[2 * j + 1]) << 16;
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = uint4{w[0], w[1], w[2], w[3]};
+    }
+}
+
+// v of lane l ^ m: DPP quad permutes for m = 1, 2, a swap of the wave's
+// halves for m = 32, a lane permute otherwise
+__device__ __forceinline__ float lane_xor(float v, int m, int l) {
+    const int b = __builtin_bit_cast(int, v);
+    if (m == 1) return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(b, 0xB1, 0xF, 0xF, false));
+    if (m == 2) return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(b, 0x4E, 0xF, 0xF, false));
+    if (m == 32) {
+        const auto sw = __builtin_amdgcn_permlane32_swap(uint32_t(b), uint32_t(b), false, false);
+        return __builtin_bit_cast(float, l < 32 ? sw[1] : sw[0]);
+    }
+    return __shfl_xor(v, m, 64);
+}
+
+// The unscaled transform H (s * v) of a 1024-block, lane l holding elements
+// 16l .. 16l + 15 and the signs in `sg`: index bits 0-3 are butterflied in
+// registers, bits 4-9 (the lane bits) with cross-lane exchanges; fp32 in a
+// fixed order, 10 levels of sums.  The caller multiplies by 1/32 (exact).
+__device__ __forceinline__ void rotate16(float (&v)[16], const uint4 sg, int l) {
+    const uint32_t sw[4] = {sg.x, sg.y, sg.z, sg.w};
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const uint32_t neg = (sw[j >> 2] << (24 - 8 * (j & 3))) & 0x80000000u;
+        v[j] = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v[j]) ^ neg);
+    }
+#pragma unroll
+    for (int h = 1; h < 16; h <<= 1)
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (!(j & h)) {
+                const float a = v[j], b = v[j + h];
+                v[j] = a + b;
+                v[j + h] = a - b;
+            }
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+        const float sgn = (l & m) ? -1.0f : 1.0f;
+        float p[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) p[j] = lane_xor(v[j], m, l);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = __builtin_fmaf(v[j], sgn, p[j]);
+    }
+}
+
+}  // namespace elem
+}  // namespace tl

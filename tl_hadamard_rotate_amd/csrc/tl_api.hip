@@ -3,6 +3,7 @@
 // leaves every output untouched.
 #include <stdint.h>
 
+#include <cmath>
 #include <cstdlib>
 #include <initializer_list>
 #include <mutex>
@@ -20,6 +21,8 @@ constexpr int64_t kMaxElems = int64_t(1) << 36;    // M*K, N*K and M*N
 constexpr int32_t kMaxChain = 65536;               // linears in one chain
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
@@ -77,6 +80,22 @@ tl_status check_workspace(int64_t need, const void* ws, int64_t ws_bytes,
     for (const auto& b : bufs)
         if (b.first && overlap(ws, need, b.first, b.second)) return TL_ERR_ALIAS;
     return TL_OK;
+}
+
+// the calls around the ternary linears: element types, 4-bit weights
+bool real_dtype(int32_t t) { return t == TL_F32 || t == TL_F16 || t == TL_BF16; }
+
+int64_t dtype_bytes(int32_t t) { return t == TL_F32 ? 4 : t == TL_I8 ? 1 : 2; }
+
+bool q4_shape_ok(int64_t n, int64_t k) {
+    return n >= 1 && n <= kMaxRows && k >= TL_GROUP && k % TL_GROUP == 0 && k <= TL_MAX_K &&
+           n * k <= kMaxElems;
+}
+
+bool q4_group_ok(int32_t group) { return group == 32 || group == 64 || group == 128; }
+
+bool q4_product_shape_ok(int64_t m, int64_t n, int64_t k) {
+    return q4_shape_ok(n, k) && m >= 1 && m <= kMaxRows && m * k <= kMaxElems && m * n <= kMaxElems;
 }
 
 // TL_DEBUG=1: count the packed bytes that are not valid encodings before a
@@ -331,6 +350,101 @@ tl_status tl_quantize(const float* w, const int8_t* signs, int64_t N, int64_t K,
     return launched(tl::launch_quantize(w, signs, N, K, codes, scales, stream));
 }
 
+tl_status tl_rms_norm(const void* x, const void* residual, const void* gain, const int8_t* signs,
+                      int64_t M, int64_t K, int32_t x_dtype, float eps, void* sum_out, void* out,
+                      int32_t out_dtype, float* out_scales, hipStream_t stream) {
+    if (!x || !gain || !out || (sum_out && !residual)) return TL_ERR_NULL;
+    if (!real_dtype(x_dtype) || !(real_dtype(out_dtype) || out_dtype == TL_I8)) return TL_ERR_DTYPE;
+    if (out_dtype == TL_I8 && !out_scales) return TL_ERR_NULL;
+    if (out_dtype != TL_I8 && out_scales) return TL_ERR_DTYPE;
+    const int64_t step = signs ? TL_BLOCK : out_dtype == TL_I8 ? TL_GROUP : 8;
+    if (!(M >= 1 && M <= kMaxRows && K >= step && K % step == 0 && K <= TL_MAX_K && M * K <= kMaxElems))
+        return TL_ERR_SHAPE;
+    if (!std::isnormal(eps) || eps < 0.0f) return TL_ERR_VALUE;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(gain) || !aligned16(signs) ||
+        !aligned16(sum_out) || !aligned16(out) || !aligned4(out_scales))
+        return TL_ERR_ALIGN;
+    const int64_t e = dtype_bytes(x_dtype), xb = M * K * e, ob = M * K * dtype_bytes(out_dtype);
+    const int64_t sb = M * (K / TL_GROUP) * 4;
+    // the outputs against the inputs and each other; sum_out may be x or residual
+    const std::pair<const void*, int64_t> ins[] = {{x, xb}, {residual, xb}, {gain, K * e}, {signs, K}};
+    for (const auto& in : ins) {
+        if (!in.first) continue;
+        if (overlap(out, ob, in.first, in.second)) return TL_ERR_ALIAS;
+        if (out_scales && overlap(out_scales, sb, in.first, in.second)) return TL_ERR_ALIAS;
+        const bool in_place = sum_out == in.first && (in.first == x || in.first == residual) &&
+                              in.second == xb;
+        if (sum_out && !in_place && overlap(sum_out, xb, in.first, in.second)) return TL_ERR_ALIAS;
+    }
+    if (sum_out && overlap(sum_out, xb, out, ob)) return TL_ERR_ALIAS;
+    if (out_scales && (overlap(out_scales, sb, out, ob) ||
+                       (sum_out && overlap(out_scales, sb, sum_out, xb))))
+        return TL_ERR_ALIAS;
+    return launched(tl::launch_rms_norm(x, residual, gain, signs, M, K, x_dtype, eps, sum_out, out,
+                                        out_dtype, out_scales, stream));
+}
+
+int64_t tl_q4_packed_bytes(int64_t N, int64_t K) {
+    return N < 1 || K < TL_GROUP || K % TL_GROUP != 0 ? -1 : N * (K / 2);
+}
+
+tl_status tl_q4_quantize(const void* w, const int8_t* signs, int64_t N, int64_t K, int32_t w_dtype,
+                         int32_t group, uint8_t* packed, uint16_t* scales, hipStream_t stream) {
+    if (!w || !packed || !scales) return TL_ERR_NULL;
+    if (!q4_shape_ok(N, K) || (signs && K % TL_BLOCK != 0)) return TL_ERR_SHAPE;
+    if (!q4_group_ok(group)) return TL_ERR_FORMAT;
+    if (!real_dtype(w_dtype)) return TL_ERR_DTYPE;
+    if (!aligned16(w) || !aligned16(signs) || !aligned16(packed) || !aligned16(scales))
+        return TL_ERR_ALIGN;
+    const int64_t wb = N * K * dtype_bytes(w_dtype), pb = N * (K / 2), sb = N * (K / group) * 2;
+    if (overlap(packed, pb, w, wb) || overlap(scales, sb, w, wb) || overlap(packed, pb, scales, sb) ||
+        (signs && (overlap(packed, pb, signs, K) || overlap(scales, sb, signs, K))))
+        return TL_ERR_ALIAS;
+    return launched(
+        tl::launch_q4_quantize(w, signs, N, K, w_dtype, group, packed, scales, stream));
+}
+
+tl_status tl_q4_dequantize(const uint8_t* packed, const uint16_t* scales, int64_t N, int64_t K,
+                           int32_t group, void* w, int32_t w_dtype, hipStream_t stream) {
+    if (!w || !packed || !scales) return TL_ERR_NULL;
+    if (!q4_shape_ok(N, K)) return TL_ERR_SHAPE;
+    if (!q4_group_ok(group)) return TL_ERR_FORMAT;
+    if (!real_dtype(w_dtype)) return TL_ERR_DTYPE;
+    if (!aligned16(w) || !aligned16(packed) || !aligned16(scales)) return TL_ERR_ALIGN;
+    const int64_t wb = N * K * dtype_bytes(w_dtype);
+    if (overlap(w, wb, packed, N * (K / 2)) || overlap(w, wb, scales, N * (K / group) * 2))
+        return TL_ERR_ALIAS;
+    return launched(tl::launch_q4_dequantize(packed, scales, N, K, group, w, w_dtype, stream));
+}
+
+int64_t tl_q4_gemv_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    return q4_product_shape_ok(M, N, K) ? tl::q4_gemv_workspace_bytes(M, N, K) : -1;
+}
+
+tl_status tl_q4_gemv(const uint8_t* packed, const uint16_t* scales, int32_t group, const void* x,
+                     int32_t x_dtype, const float* x_scales, int64_t M, int64_t N, int64_t K, void* y,
+                     int32_t y_dtype, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+    if (!packed || !scales || !x || !y || (x_dtype == TL_I8 && !x_scales)) return TL_ERR_NULL;
+    if (!q4_product_shape_ok(M, N, K)) return TL_ERR_SHAPE;
+    if (!q4_group_ok(group)) return TL_ERR_FORMAT;
+    if (x_dtype != TL_F16 && x_dtype != TL_BF16 && x_dtype != TL_I8) return TL_ERR_DTYPE;
+    if (!real_dtype(y_dtype) || (x_dtype != TL_I8 && x_scales)) return TL_ERR_DTYPE;
+    if (!aligned16(packed) || !aligned16(scales) || !aligned16(x) || !aligned4(x_scales) ||
+        !aligned16(y))
+        return TL_ERR_ALIGN;
+    const int64_t pb = N * (K / 2), sb = N * (K / group) * 2, xb = M * K * dtype_bytes(x_dtype);
+    const int64_t xsb = M * (K / TL_GROUP) * 4, yb = M * N * dtype_bytes(y_dtype);
+    if (overlap(y, yb, packed, pb) || overlap(y, yb, scales, sb) || overlap(y, yb, x, xb) ||
+        (x_scales && overlap(y, yb, x_scales, xsb)))
+        return TL_ERR_ALIAS;
+    const tl_status st =
+        check_workspace(tl::q4_gemv_workspace_bytes(M, N, K), workspace, workspace_bytes,
+                        {{packed, pb}, {scales, sb}, {x, xb}, {x_scales, xsb}, {y, yb}});
+    if (st != TL_OK) return st;
+    return launched(tl::launch_q4_gemv(packed, scales, group, x, x_dtype, x_scales, M, N, K, y,
+                                       y_dtype, workspace, stream));
+}
+
 const char* tl_status_str(tl_status status) {
     switch (status) {
         case TL_OK: return "TL_OK";
@@ -343,6 +457,7 @@ const char* tl_status_str(tl_status status) {
         case TL_ERR_DTYPE: return "TL_ERR_DTYPE";
         case TL_ERR_WORKSPACE: return "TL_ERR_WORKSPACE";
         case TL_ERR_DATA: return "TL_ERR_DATA";
+        case TL_ERR_VALUE: return "TL_ERR_VALUE";
     }
     return "TL_ERR_UNKNOWN";
 }

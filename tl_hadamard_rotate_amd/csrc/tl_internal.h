@@ -132,5 +132,20 @@ hipError_t launch_chain(const void* plan, int32_t count, uint32_t* sync, hipStre
 // Device address and size of the current device's copy of the file-scope
 // workspace of tl_gemm_noalloc (looked up once per device; thread-safe).
 hipError_t noalloc_scratch(void** out, int64_t* bytes);
+// Residual addition, RMS norm, gain and the optional rotation of rows
+// (tl_rms_norm); types are the TL_ enum, null pointers as there
+hipError_t launch_rms_norm(const void* x, const void* residual, const void* gain, const int8_t* signs,
+                           int64_t m, int64_t k, int x_dtype, float eps, void* sum_out, void* out,
+                           int out_dtype, float* out_scales, hipStream_t stream);
+// 4-bit weights: rounding of rows (with the rotation when signs is given),
+// their values, and the product with few tokens
+hipError_t launch_q4_quantize(const void* w, const int8_t* signs, int64_t n, int64_t k, int w_dtype,
+                              int group, uint8_t* packed, uint16_t* scales, hipStream_t stream);
+hipError_t launch_q4_dequantize(const uint8_t* packed, const uint16_t* scales, int64_t n, int64_t k,
+                                int group, void* w, int w_dtype, hipStream_t stream);
+int64_t q4_gemv_workspace_bytes(int64_t m, int64_t n, int64_t k);
+hipError_t launch_q4_gemv(const uint8_t* packed, const uint16_t* scales, int group, const void* x,
+                          int x_dtype, const float* x_scales, int64_t m, int64_t n, int64_t k, void* y,
+                          int y_dtype, void* ws, hipStream_t stream);
 
 }  // namespace tl
