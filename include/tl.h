@@ -387,9 +387,11 @@ TL_API tl_status tl_q4_dequantize(const uint8_t* packed, const uint16_t* scales,
                                   int64_t K, int32_t group, void* w, int32_t w_dtype,
                                   hipStream_t stream);
 
-/* Bytes of device workspace tl_q4_gemv needs for this shape (0: none; none is
- * ever needed at M <= 16).  Host only; it depends on the compute-unit count
- * of the current device.  -1 when the shape is not accepted. */
+/* Bytes of device workspace tl_q4_gemv needs for this shape (0: none), enough
+ * for every type and group size: fp32 sums of up to as many parts of K as
+ * activations fit in LDS at a time.  None is needed while M * K <= 16384.
+ * Host only; it depends on the compute-unit count of the current device.  -1
+ * when the shape is not accepted. */
 TL_API int64_t tl_q4_gemv_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /* Product with q4 weights (decode shapes):

@@ -105,12 +105,12 @@ def test_q4_gemv_refusals():
 
 def test_q4_gemv_workspace():
     L = tl.lib()
-    for m in (1, 7, 16):
-        for n, k in ((1024, 5120), (5120, 17408), (131072, 5120), (1, 128)):
+    for m, k in ((1, 128), (1, 5120), (1, 16384), (3, 5120), (16, 1024), (64, 256), (128, 128)):
+        for n in (1, 1024, 131072):
             assert L.tl_q4_gemv_workspace_bytes(m, n, k) == 0
     for bad in ((0, 64, 1024), (4, 0, 1024), (4, 64, 100), (4, 64, 0), (1 << 24, 64, 8192)):
         assert L.tl_q4_gemv_workspace_bytes(*bad) == -1
-    for m in (17, 64, 300):
+    for m in (8, 17, 64, 300):
         for n, k in ((1024, 5120), (5120, 17408), (17, 17408)):
             need = L.tl_q4_gemv_workspace_bytes(m, n, k)
             assert need >= 0

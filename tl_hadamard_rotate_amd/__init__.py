@@ -483,7 +483,7 @@ def q4_dequantize(packed, scales, out_dtype=torch.float16, out=None) -> torch.Te
 
 
 def q4_gemv_workspace_bytes(m: int, n: int, k: int) -> int:
-    """Device workspace bytes tl_q4_gemv needs (0 at M <= 16)."""
+    """Device workspace bytes tl_q4_gemv needs (0 while m * k <= 16384)."""
     b = int(lib().tl_q4_gemv_workspace_bytes(m, n, k))
     if b < 0:
         raise TLError("tl_q4_gemv_workspace_bytes", 2)
@@ -525,7 +525,7 @@ def q4_gemv(packed, scales, x, x_scales=None, out_dtype=torch.float32, out=None,
     if workspace is not None:
         wb = workspace.numel()
         _need_like(workspace, "workspace", torch.uint8, (wb,), device)
-    elif m > 16:
+    elif m * k > 16384:
         with torch.cuda.device(device):
             wb = q4_gemv_workspace_bytes(m, n, k)
         workspace = torch.empty(wb, dtype=torch.uint8, device=device) if wb else None

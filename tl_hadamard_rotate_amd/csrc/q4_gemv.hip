@@ -5,18 +5,21 @@
 // v_mfma_f32_16x16x32_f16 (8 bits: v_mfma_i32_16x16x64_i8, 16x16x32 for groups
 // of 32) with 16 tokens as A rows and 16 weight rows as B columns.  Lane
 // (q, c) = (lane / 16, lane % 16) loads the 16 bytes of row c that hold octets
-// 4q .. 4q + 3 of a 128-weight chunk; two swaps across the quarters of the wave
-// (v_permlane16_swap, v_permlane32_swap) hand it the octets q, q + 4, q + 8,
-// q + 12 instead, so that each MFMA covers 32 (64) consecutive weights, which
-// lie in one scale group, and reads the activations of 16 tokens in runs of 64
-// bytes.  The sums of a group leave the matrix cores in fp32 (exact int32 for
-// 8 bits) and are multiplied by the group's scale in fp32.
+// 4q .. 4q + 3 of a 128-weight chunk.  Which weights a matrix instruction sums
+// is free as long as they share a scale and both operands agree: in groups of
+// 128 the four octets go in as loaded, in groups of 64 (32) one (two) swaps
+// across the quarters of the wave bring the octets of a group together.  The
+// sums of a group leave the matrix cores in fp32 (exact int32 for 8 bits) and
+// are multiplied by the group's scale in fp32.
 //
-// Decode: a nibble n of two's complement is code + 8 = n ^ 8.  For binary16,
-// (w & 0x000F000F) ^ 0x64086408 is the pair 1024 + (code + 8) and (w & 0x00F000F0)
-// ^ 0x64806480 the pair 1024 + 16 (code + 8); one packed add or fma makes them
-// the codes, exactly.  For 8 bits, w & 0xF0F0F0F0 and (w << 4) & 0xF0F0F0F0 are
-// four signed bytes 16 * code each; the 1/16 goes into the scale.
+// Decode.  A nibble n of two's complement is code + 8 = n ^ 8.  For 16-bit
+// activations, (w & 0x000F000F) ^ 0x64086408 is the binary16 pair 1024 + (code
+// + 8) and (w & 0x00F000F0) ^ 0x64806480 the pair 1024 + 16 (code + 8); one
+// packed add or fma makes them the codes, exactly.  (Feeding code + 8 as a
+// subnormal pattern and taking the 8 off the sums saves those, but then rows
+// of small codes carry the rounding errors of 8 * sum x.)  For 8 bits, w &
+// 0xF0F0F0F0 and (w << 4) & 0xF0F0F0F0 are four signed bytes 16 * code each;
+// the 1/16 goes into the scale.
 //
 // bfloat16 activations become binary16 under a power of two per token and
 // chunk, chosen so that the largest of the chunk lies in [2^14, 2^15): 8
@@ -24,16 +27,16 @@
 // 2^-28 of the largest; smaller ones are off by at most 2^-29 of it.  The
 // power of two is applied to the sums, as the scales of 8-bit activations are.
 //
-// Work split: a workgroup owns a tile of 16 R TW weight rows; its TW KS waves
-// are TW sets of 16 R rows, each split along K into KS runs of chunks whose
-// partial sums are added through LDS in a fixed order.  A wave keeps D chunks
-// of weights on the way.  Activations and scales go through LDS: read from
-// memory as the matrix cores want them, the scales (2 bytes from each of 16
-// rows) took longer than the weights, and the activations of 16 tokens (64
-// bytes from each row, a power of two apart, so from few L2 channels) as long
-// as the weights.  Activations that fit in LDS are loaded once and stay while
-// the workgroup goes through its tiles; others (PH) come in phases, P chunks
-// of each of the KS runs at a time.
+// Work split.  K is cut into `parts` of L chunks such that the activations of
+// a part fit in LDS; a workgroup stages one part once and each of its waves
+// then goes through tiles of 16 R weight rows on its own, without a barrier,
+// D chunks of weights on the way.  Where rows are few, KS waves share a tile,
+// each a run of the part's chunks, and add their sums through LDS.  With
+// several parts the sums go to the workspace and a second kernel adds them.
+// All sums are taken in a fixed order.  A tile's scales, one run of memory or
+// a piece of each row, go through the wave's own LDS, SEG chunks at a time:
+// read as they are used, 2 bytes from each of 16 rows, they took longer than
+// the weights.
 #include "elem.h"
 #include "tl_internal.h"
 
@@ -49,7 +52,7 @@ typedef float float4v __attribute__((ext_vector_type(4)));
 typedef int int4v __attribute__((ext_vector_type(4)));
 typedef unsigned int uint4v __attribute__((ext_vector_type(4)));
 
-constexpr int kThreads = 512;   // at most
+constexpr int kWaves = 8;    // of a workgroup
 
 // a's upper half-wave exchanged with b's lower one; odd rows of 16 of a with
 // even ones of b
@@ -77,13 +80,18 @@ __device__ __forceinline__ half8v decode_f16(uint32_t w) {
     return half8v{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// largest of the 16 lanes of a row (as bfloat16 magnitudes)
+// value of lane ^ 1, lane ^ 2, the other four of 8, the other 8 of 16
+template <int STEP>
+__device__ __forceinline__ uint32_t row16(uint32_t a) {
+    constexpr int kCtrl[4] = {0xB1, 0x4E, 0x141, 0x140};
+    return uint32_t(__builtin_amdgcn_mov_dpp(int(a), kCtrl[STEP], 0xF, 0xF, false));
+}
 __device__ __forceinline__ uint32_t row16_max(uint32_t a) {
     const auto step = [&](uint32_t o) { a = o > a ? o : a; };
-    step(uint32_t(__builtin_amdgcn_mov_dpp(int(a), 0xB1, 0xF, 0xF, false)));    // lane ^ 1
-    step(uint32_t(__builtin_amdgcn_mov_dpp(int(a), 0x4E, 0xF, 0xF, false)));    // lane ^ 2
-    step(uint32_t(__builtin_amdgcn_mov_dpp(int(a), 0x141, 0xF, 0xF, false)));   // the other four of 8
-    step(uint32_t(__builtin_amdgcn_mov_dpp(int(a), 0x140, 0xF, 0xF, false)));   // the other 8 of 16
+    step(row16<0>(a));
+    step(row16<1>(a));
+    step(row16<2>(a));
+    step(row16<3>(a));
     return a;
 }
 
@@ -116,40 +124,57 @@ __device__ __forceinline__ void order_i8(uint4v& v) {
                __builtin_amdgcn_perm(d, c, 0x05010400u), __builtin_amdgcn_perm(d, c, 0x07030602u)};
 }
 
+// Octets of the chunk that lane quarter q and (16 bits, or groups of 32) word
+// j, (8 bits) pair of words j, meet in: first_octet(q) + octet_step(j)
+template <int G>
+__device__ __forceinline__ int first_octet(int q) {
+    return G == 128 ? 4 * q : G == 64 ? 4 * (q & 1) + 2 * (q >> 1) : q;
+}
+template <int G>
+constexpr int octet_step(int j, bool pair) {
+    if (pair) return G == 128 ? 2 * j : 8 * j;
+    return G == 128 ? j : G == 64 ? 8 * (j >> 1) + (j & 1) : 4 * j;
+}
+
+template <int XT>
+constexpr int chunk_bytes() { return XT == TL_I8 ? 128 : 256; }
+// fp32 factors a chunk has per token beside its activations (bfloat16, 8 bits)
+template <int XT>
+constexpr int chunk_floats() { return XT == TL_F16 ? 0 : 1; }
+
 // One chunk's sums added to acc[r][t]: lane (q, c) holds weight row 16 r + c
-// and tokens 16 t + 4 q .. + 3.  In LDS: xa[t] the lane's token's activations
-// of the chunk, sc the chunk's scales of row c (row 16 r + c is r * row_step
-// elements further), fa the factors of tokens 4 q .. of the chunk (bfloat16, 8
-// bits).
-template <int XT, int G, int R, int MT>
-__device__ __forceinline__ void consume(const uint4 (&wr)[R], const uint8_t* const (&xa)[MT], const uint16_t* sc,
-                                        int row_step, const float* fa, int q, float4v (&acc)[R][MT]) {
+// and tokens 16 t + 4 q .. + V - 1.  In LDS: xa[t] the lane's token's
+// activations, fa[t] the chunk's factors of tokens 16 t + 4 q .. + 3, sc its
+// scales of row c (row 16 r + c is r * row_step elements further).
+template <int XT, int G, int R, int MT, int V>
+__device__ __forceinline__ void consume(const uint4v (&wr)[R], const uint8_t* const (&xa)[MT], const uint16_t* sc,
+                                        int row_step, const float* const (&fa)[MT], float (&acc)[R][MT][V]) {
     constexpr int NS = 128 / G;               // scales of the chunk
-    constexpr int NX = XT == TL_I8 && G != 32 ? 2 : 4;   // matrix instructions along K
+    constexpr bool kPair = XT == TL_I8 && G != 32;
+    constexpr int NX = kPair ? 2 : 4;         // matrix instructions along K
     uint32_t w[R][4];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        w[r][0] = wr[r].x, w[r][1] = wr[r].y, w[r][2] = wr[r].z, w[r][3] = wr[r].w;
-        if constexpr (NX == 4) {              // octets q, q + 4, q + 8, q + 12
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[r][i] = wr[r][i];
+        if constexpr (G != 128) {
             swap32(w[r][0], w[r][2]);
             swap32(w[r][1], w[r][3]);
+        }
+        if constexpr (G == 32) {
             swap16(w[r][0], w[r][1]);
             swap16(w[r][2], w[r][3]);
-        } else {                              // octet pairs q, q + 4
-            swap16(w[r][0], w[r][2]);
-            swap16(w[r][1], w[r][3]);
-            swap32(w[r][0], w[r][2]);
-            swap32(w[r][1], w[r][3]);
         }
     }
     float4v f[MT];
     if constexpr (XT != TL_F16)
 #pragma unroll
-        for (int t = 0; t < MT; ++t) f[t] = *reinterpret_cast<const float4v*>(fa + 16 * t);
+        for (int t = 0; t < MT; ++t)
+            f[t] = *reinterpret_cast<const float4v*>(fa[t]);
     float s[R][NS];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        uint32_t sb[2];
+        uint32_t sb[2] = {};
         if constexpr (NS == 1) sb[0] = sc[r * row_step];
         else if constexpr (NS == 2) sb[0] = *reinterpret_cast<const uint32_t*>(sc + r * row_step);
         else {
@@ -167,10 +192,12 @@ __device__ __forceinline__ void consume(const uint4 (&wr)[R], const uint8_t* con
     for (int j = 0; j < NX; ++j) {
         const bool first = j % (NX / NS) == 0, last = (j + 1) % (NX / NS) == 0;
         const int g = j / (NX / NS);
+        constexpr int kOctet = XT == TL_I8 ? 8 : 16;   // bytes
+        const int at = kOctet * octet_step<G>(j, kPair);
         if constexpr (XT != TL_I8) {
             half8v a[MT];
 #pragma unroll
-            for (int t = 0; t < MT; ++t) a[t] = *reinterpret_cast<const half8v*>(xa[t] + 64 * j);
+            for (int t = 0; t < MT; ++t) a[t] = *reinterpret_cast<const half8v*>(xa[t] + at);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const half8v b = decode_f16(w[r][j]);
@@ -178,10 +205,10 @@ __device__ __forceinline__ void consume(const uint4 (&wr)[R], const uint8_t* con
                 for (int t = 0; t < MT; ++t)
                     d[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[t], b, first ? float4v{} : d[r][t], 0, 0, 0);
             }
-        } else if constexpr (G == 32) {
+        } else if constexpr (!kPair) {
             int64_t a[MT];
 #pragma unroll
-            for (int t = 0; t < MT; ++t) a[t] = *reinterpret_cast<const int64_t*>(xa[t] + 32 * j);
+            for (int t = 0; t < MT; ++t) a[t] = *reinterpret_cast<const int64_t*>(xa[t] + at);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const uint32_t lo = (w[r][j] << 4) & 0xF0F0F0F0u, hi = w[r][j] & 0xF0F0F0F0u;
@@ -193,7 +220,7 @@ __device__ __forceinline__ void consume(const uint4 (&wr)[R], const uint8_t* con
         } else {
             int4v a[MT];
 #pragma unroll
-            for (int t = 0; t < MT; ++t) a[t] = *reinterpret_cast<const int4v*>(xa[t] + 64 * j);
+            for (int t = 0; t < MT; ++t) a[t] = *reinterpret_cast<const int4v*>(xa[t] + at);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const uint32_t u = w[r][2 * j], v = w[r][2 * j + 1];
@@ -210,7 +237,7 @@ __device__ __forceinline__ void consume(const uint4 (&wr)[R], const uint8_t* con
 #pragma unroll
                 for (int t = 0; t < MT; ++t)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < V; ++i) {
                         float v;
                         if constexpr (XT == TL_I8) v = float(di[r][t][i]);
                         else v = d[r][t][i];
@@ -225,11 +252,13 @@ struct Args {
     const uint8_t* x;
     const float* xs;
     void* y;
+    float* sums;     // parts > 1: fp32 [part][m][n]
     int64_t n, k;
     int m, y_dtype;
-    // the launch's split: KS runs of C chunks, P of each in a phase; tiles of
-    // rows, how many a workgroup takes, of how many the scales are in LDS
-    int ks, c, p, tiles, per_wg, s_tiles;
+    // parts of L chunks; KS waves share a tile, LW = ceil(L / KS) chunks each;
+    // tiles of 16 R rows, row groups (workgroups of a part); chunks whose
+    // scales a wave has in LDS at a time, and their bytes
+    int parts, l, ks, lw, tiles, groups, seg, s_bytes;
 };
 
 __device__ __forceinline__ void store_y(void* y, int64_t at, float v, int y_dtype) {
@@ -237,99 +266,122 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, float v, int y_dtyp
     else static_cast<uint16_t*>(y)[at] = uint16_t(y_dtype == TL_F16 ? f16_bits(v) : bf16_bits(v));
 }
 
-template <int XT, int G, int R, int MT, int D, bool PH>
-__global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void q4_gemv_kernel(const Args p) {
+template <int XT, int G, int R, int MT, int D, int V>
+__global__ __launch_bounds__(64 * kWaves, MT == 1 ? 4 : 2) void q4_gemv_kernel(const Args p) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    constexpr int kXB = XT == TL_I8 ? 1 : 2;
-    constexpr int kPieces = 8 * kXB;          // 16-byte pieces of a token's chunk
-    constexpr int kLanePiece = XT == TL_I8 && G == 32 ? 8 : 16;   // bytes of x a lane reads at a time
+    constexpr int kCB = chunk_bytes<XT>();
+    constexpr int kPieces = kCB / 16;         // 16-byte pieces of a token's chunk
+    constexpr int kF = chunk_floats<XT>();
     constexpr int NS = 128 / G;
     const int tid = threadIdx.x, threads = int(blockDim.x);
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int waves = threads >> 6;
     const int q = lane >> 4, c = lane & 15;
     const int chunks = int(p.k / 128);
     const int row_bytes = int(p.k / 2);
-    const int ks = wave % p.ks, tw = wave / p.ks, tws = (threads >> 6) / p.ks;
-    const int tile_rows = 16 * R * tws;
+    const int part = int(blockIdx.x) % p.parts, group = int(blockIdx.x) / p.parts;
+    const int ks = wave % p.ks, tw = wave / p.ks, tws = waves / p.ks;
     const int64_t m0 = int64_t(blockIdx.y) * (16 * MT);
     const int tokens = int(p.m - m0 < 16 * MT ? p.m - m0 : 16 * MT);
-    const int slots = PH ? p.ks * p.p : chunks;   // chunks of activations in LDS
-    const int tile0 = int(blockIdx.x) * p.per_wg;
-    const int tile1 = tile0 + p.per_wg < p.tiles ? tile0 + p.per_wg : p.tiles;
+    // the part's chunks [c0, c0 + len), this wave's [w0, w0 + mine) of them
+    const int c0 = part * p.l;
+    const int len = chunks - c0 < p.l ? chunks - c0 : p.l;
+    const int w0 = ks * p.lw;
+    const int left = len - w0;
+    const int mine = left < 0 ? 0 : left < p.lw ? left : p.lw;
 
-    // LDS: activations [token][slot], factors [slot][16 MT], two sets of
-    // partial sums [ks][tw][t][r][row][token], scales [row][chunk]
-    const int xstride = slots * (128 * kXB) + 16;   // 16: rows on different banks
-    const int red_set = (threads >> 6) * (MT * R * 256);
+    // LDS: activations [token][chunk], factors [chunk][TS], TS the tokens
+    // rounded up to fours, the waves' scales [row][chunk]; at the end partial sums (KS > 1)
+    const int xstride = p.l * kCB + 16;       // 16: rows on different banks
+    const int ts = (tokens + 3) / 4 * 4;
     uint8_t* const lx = smem;
     float* const lf = reinterpret_cast<float*>(lx + tokens * xstride);
-    float* const red = lf + (XT == TL_F16 ? 0 : slots * 16 * MT);
-    uint16_t* const lsc = reinterpret_cast<uint16_t*>(red + (p.ks > 1 ? 2 * red_set : 0));
+    uint16_t* const ls = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(lf + p.l * (kF * ts)) +
+                                                     wave * p.s_bytes);
+    float* const red = reinterpret_cast<float*>(smem);
 
-    // this wave's chunks are ks * C + [0, mine)
-    const int left = chunks - ks * p.c;
-    const int mine = left < 0 ? 0 : left < p.c ? left : p.c;
+    // this wave's tiles: tile, tile + stride, ...
+    const int stride = p.groups * tws;
+    int tile = group * tws + tw;
 
     // Weights on the way: chunk i of a tile in ring[i % D].  voff: the lane's
-    // rows of a tile (rows that do not exist repeat the last one; their sums
+    // rows of the tile (rows that do not exist repeat the last one; their sums
     // are not stored).
-    uint4 ring[D][R];
+    uint4v ring[D][R];
     uint32_t voff[R], vnext[R];
-    const uint8_t *base, *nbase = nullptr;
-    const auto tile_count = [&](int tile) {
-        const int64_t rest = p.n - int64_t(tile) * tile_rows;
-        return int(rest < tile_rows ? rest : tile_rows);
-    };
-    const auto enter = [&](int tile, uint32_t (&v)[R]) {
-        const int last = tile_count(tile) - 1;
+    const auto enter = [&](int t, uint32_t (&v)[R]) {
+        const int64_t n0 = int64_t(t) * (16 * R);
+        const int last = int(p.n - n0 < 16 * R ? p.n - n0 : 16 * R) - 1;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int row = 16 * (R * tw + r) + c;
+            const int row = 16 * r + c;
             v[r] = uint32_t(row < last ? row : last) * uint32_t(row_bytes) + 16u * uint32_t(q);
         }
-        return p.packed + (int64_t(tile) * tile_rows * row_bytes + int64_t(ks) * p.c * 64);
+        return p.packed + (n0 * row_bytes + int64_t(c0 + w0) * 64);
     };
-    const auto fetch = [&](const uint8_t* b, const uint32_t (&v)[R], uint4 (&w)[R]) {
+    const auto fetch = [&](const uint8_t* b, const uint32_t (&v)[R], uint4v (&w)[R]) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) w[r] = *reinterpret_cast<const uint4*>(b + v[r]);
+        for (int r = 0; r < R; ++r) w[r] = *reinterpret_cast<const uint4v*>(b + v[r]);
     };
-    base = enter(tile0, voff);
+    // scales of chunks [i0, i0 + SEG) of this wave's of a tile into its LDS,
+    // [row][chunk]: one run of memory when they are all of the rows
+    const auto stage_s = [&](int t, int i0) {
+        const int64_t n0 = int64_t(t) * (16 * R);
+        const int rows = int(p.n - n0 < 16 * R ? p.n - n0 : 16 * R);
+        const int span = mine - i0 < p.seg ? mine - i0 : p.seg;
+        const uint16_t* const src = p.scales + (n0 * chunks + c0 + w0 + i0) * NS;
+        const int row_e = span * NS, count = rows * row_e;
+        if (span == chunks) {
+            for (int i = 8 * lane; i < count; i += 512) {
+                if (i + 8 <= count) *reinterpret_cast<uint4v*>(ls + i) = *reinterpret_cast<const uint4v*>(src + i);
+                else
+                    for (int j = i; j < count; ++j) ls[j] = src[j];
+            }
+        } else if (span > 0) {
+            // (row, chunk) units of a lane, the row advanced without a division
+            int row = lane / span, i = lane - row * span;
+            while (row < rows) {
+                const uint16_t* const from = src + (int64_t(row) * chunks + i) * NS;
+                uint16_t* const to = ls + row * row_e + i * NS;
+                if constexpr (NS == 1) *to = *from;
+                else if constexpr (NS == 2) *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(from);
+                else *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(from);
+                i += 64;
+                while (i >= span) {
+                    i -= span;
+                    ++row;
+                }
+            }
+        }
+    };
+    const bool work = tile < p.tiles;
+    const uint8_t* base = p.packed;
+    if (work) {
+        base = enter(tile, voff);
 #pragma unroll
-    for (int d = 0; d < D; ++d)
-        if (d < mine) fetch(base + 64 * d, voff, ring[d]);
+        for (int d = 0; d < D; ++d)
+            if (d < mine) fetch(base + 64 * d, voff, ring[d]);
+    }
 
-    // activations of phase ph to LDS
-    const auto stage_x = [&](int ph) {
+    // the part's activations to LDS
+    {
         constexpr int U = 4;
-        const uint8_t* const xt = p.x + m0 * p.k * kXB;
-        const float* const xst = XT == TL_I8 ? p.xs + m0 * chunks : nullptr;
-        const int per_token = slots * kPieces;
+        const uint8_t* const xt = p.x + (m0 * p.k + int64_t(c0) * 128) * (kCB / 128);
+        const float* const xst = XT == TL_I8 ? p.xs + m0 * chunks + c0 : nullptr;
+        const int per_token = len * kPieces;
         int t = tid / per_token, e = tid - t * per_token;
         while (t < tokens) {
             uint4v v[U] = {};
-            int dst[U];     // byte of the piece in LDS, -1: none
-            int fd[U];      // its factor's place, -1: another lane's
+            int tok[U], at[U];
             float f[U] = {};
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                dst[u] = fd[u] = -1;
+                tok[u] = t;
+                at[u] = e;
                 if (t < tokens) {
-                    const int slot = e / kPieces;
-                    int g = slot;
-                    if (PH) {
-                        const int run = slot / p.p, i = ph * p.p + (slot - run * p.p);
-                        g = i < p.c ? run * p.c + i : chunks;
-                    }
-                    if (g < chunks) {
-                        dst[u] = t * xstride + 16 * e;
-                        v[u] = *reinterpret_cast<const uint4v*>(xt + (int64_t(t) * p.k + int64_t(g) * 128) * kXB +
-                                                               16 * (e % kPieces));
-                        if (XT != TL_F16 && e % kPieces == 0) {
-                            fd[u] = slot * (16 * MT) + t;
-                            if (XT == TL_I8) f[u] = xst[int64_t(t) * chunks + g];
-                        }
-                    }
+                    v[u] = *reinterpret_cast<const uint4v*>(xt + int64_t(t) * p.k * (kCB / 128) + 16 * e);
+                    if (XT == TL_I8 && e % kPieces == 0) f[u] = xst[int64_t(t) * chunks + e / kPieces];
                     e += threads;
                     while (e >= per_token) {
                         e -= per_token;
@@ -341,227 +393,241 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void q4_gemv_kernel(cons
             for (int u = 0; u < U; ++u) {
                 // (a chunk's lanes are a row of 16 or half of one, present or
                 // absent together)
-                if (dst[u] >= 0) {
-                    if constexpr (XT == TL_BF16) f[u] = convert_bf16(v[u]);
-                    if constexpr (XT == TL_I8) order_i8(v[u]);
-                    *reinterpret_cast<uint4v*>(lx + dst[u]) = v[u];
-                    if (XT != TL_F16 && fd[u] >= 0) lf[fd[u]] = f[u];
-                }
+                if (tok[u] >= tokens) continue;
+                if constexpr (XT == TL_BF16) f[u] = convert_bf16(v[u]);
+                if constexpr (XT == TL_I8) order_i8(v[u]);
+                *reinterpret_cast<uint4v*>(lx + tok[u] * xstride + 16 * at[u]) = v[u];
+                if (kF && at[u] % kPieces == 0) lf[at[u] / kPieces * ts + tok[u]] = f[u];
             }
         }
-    };
-    // scales: of s_tiles tiles from `tile` on, one run of memory; PH: of a tile's
-    // chunks of phase ph
-    const auto stage_s = [&](int tile, int ph) {
-        const int64_t n0 = int64_t(tile) * tile_rows;
-        const uint16_t* const src = p.scales + n0 * (chunks * NS);
-        if constexpr (PH) {
-            const int units = tile_count(tile) * slots;
-            for (int u = tid; u < units; u += threads) {
-                const int row = u / slots, slot = u - row * slots, run = slot / p.p;
-                const int i = ph * p.p + (slot - run * p.p), g = run * p.c + i;
-                if (i >= p.c || g >= chunks) continue;
-                const uint16_t* const from = src + (int64_t(row) * chunks + g) * NS;
-                uint16_t* const to = lsc + u * NS;
-                if constexpr (NS == 1) *to = *from;
-                else if constexpr (NS == 2) *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(from);
-                else *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(from);
-            }
-        } else {
-            const int64_t have = (p.n - n0) * (chunks * NS);
-            const int want = p.s_tiles * tile_rows * chunks * NS;
-            const int count = int(have < want ? have : want);
-            for (int i = 8 * tid; i < count; i += 8 * threads) {
-                if (i + 8 <= count) *reinterpret_cast<uint4*>(lsc + i) = *reinterpret_cast<const uint4*>(src + i);
-                else
-                    for (int j = i; j < count; ++j) lsc[j] = src[j];
-            }
-        }
-    };
-    stage_s(tile0, 0);
-    stage_x(0);
+    }
+    if (work) stage_s(tile, 0);
     __syncthreads();
 
     const uint8_t* xa[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
         const int tok = 16 * t + c < tokens ? 16 * t + c : tokens - 1;   // absent tokens repeat the last
-        xa[t] = lx + tok * xstride + kLanePiece * q;
+        xa[t] = lx + tok * xstride + first_octet<G>(q) * (XT == TL_I8 ? 8 : 16) + w0 * kCB;
     }
-    int s_tile = 0, set = 0;
-    for (int tile = tile0; tile < tile1; ++tile) {
-        float4v acc[R][MT] = {};
-        const int64_t n0 = int64_t(tile) * tile_rows;
-        const int rows = tile_count(tile);
-        if (tile + 1 < tile1) nbase = enter(tile + 1, vnext);
-        const int srow = slots * NS;    // elements of a row of scales in LDS
-        const uint16_t* const sc = lsc + (s_tile * tile_rows + 16 * R * tw + c) * srow;
-        int ph = 0;
-        do {
-            const int beg = PH ? ph * p.p : 0;
-            const int end = PH && beg + p.p < mine ? beg + p.p : mine;
-            for (int i0 = beg; i0 < end; i0 += D)
+    const float* fa[MT];
 #pragma unroll
-                for (int d = 0; d < D; ++d) {
-                    const int i = i0 + d;
-                    if (i >= end) break;
-                    const int slot = PH ? ks * p.p + (i - beg) : ks * p.c + i;
-                    const uint8_t* xc[MT];
-#pragma unroll
-                    for (int t = 0; t < MT; ++t) xc[t] = xa[t] + slot * (128 * kXB);
-                    consume<XT, G, R, MT>(ring[d], xc, sc + slot * NS, 16 * srow, lf + slot * (16 * MT) + 4 * q, q, acc);
-                    // the chunk that uses this place next, of this tile or the next
-                    if (i + D < mine) fetch(base + 64 * (i + D), voff, ring[d]);
-                    else if (tile + 1 < tile1) fetch(nbase + 64 * d, vnext, ring[d]);
-                }
-            if constexpr (PH) {
-                ++ph;
-                const bool more = ph * p.p < p.c;
-                if (more || tile + 1 < tile1) {
-                    __syncthreads();
-                    stage_s(more ? tile : tile + 1, more ? ph : 0);
-                    stage_x(more ? ph : 0);
-                    if (more) __syncthreads();   // else the one below
-                }
+    for (int t = 0; t < MT; ++t)   // (factors of absent tokens: any)
+        fa[t] = lf + w0 * (kF * ts) + (16 * t + 4 * q < ts ? 16 * t + 4 * q : ts - 4);
+    for (; tile < p.tiles; tile += stride) {
+        float acc[R][MT][V] = {};
+        const int64_t n0 = int64_t(tile) * (16 * R);
+        const int rows = int(p.n - n0 < 16 * R ? p.n - n0 : 16 * R);
+        const bool more = tile + stride < p.tiles;
+        const uint8_t* nbase = base;
+        if (more) nbase = enter(tile + stride, vnext);
+        int seg0 = 0;
+        for (int i0 = 0; i0 < mine; i0 += D) {
+            if (i0 == seg0 + p.seg) {
+                // (the wave's LDS operations run in order: its reads of the
+                // old scales are done, its reads of the new ones follow)
+                seg0 = i0;
+                __builtin_amdgcn_wave_barrier();
+                stage_s(tile, seg0);
+                __builtin_amdgcn_wave_barrier();
             }
-        } while (PH && ph * p.p < p.c);
+            const int row_e = (mine - seg0 < p.seg ? mine - seg0 : p.seg) * NS;
+            const uint16_t* const sc = ls + c * row_e - seg0 * NS;
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                const int i = i0 + d;
+                if (i >= mine) break;
+                const uint8_t* xc[MT];
+#pragma unroll
+                for (int t = 0; t < MT; ++t) xc[t] = xa[t] + i * kCB;
+                const float* fc[MT];
+#pragma unroll
+                for (int t = 0; t < MT; ++t) fc[t] = fa[t] + i * (kF * ts);
+                consume<XT, G, R, MT, V>(ring[d], xc, sc + i * NS, 16 * row_e, fc, acc);
+                // the chunk that uses this place next, of this tile or the next
+                if (i + D < mine) fetch(base + 64 * (i + D), voff, ring[d]);
+                else if (more) fetch(nbase + 64 * d, vnext, ring[d]);
+            }
+        }
         base = nbase;
 #pragma unroll
         for (int r = 0; r < R; ++r) voff[r] = vnext[r];
-
         if (p.ks > 1) {
+            // (one tile a wave then)
+            __syncthreads();
 #pragma unroll
             for (int t = 0; t < MT; ++t)
 #pragma unroll
                 for (int r = 0; r < R; ++r)
-                    *reinterpret_cast<float4v*>(red + set * red_set + ((wave * MT + t) * R + r) * 256 + c * 16 + 4 * q) =
-                        acc[r][t];
-        } else {
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int t = 0; t < MT; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int row = 16 * (R * tw + r) + c, tok = 16 * t + 4 * q + e;
-                        if (row < rows && tok < tokens)
-                            store_y(p.y, (m0 + tok) * p.n + n0 + row, acc[r][t][e], p.y_dtype);
-                    }
+                    for (int i = 0; i < V; ++i)
+                        red[((wave * MT + t) * R + r) * 256 + (4 * q + i) * 16 + c] = acc[r][t][i];
+            break;
         }
-        if (!PH && ++s_tile == p.s_tiles && tile + 1 < tile1) {
-            __syncthreads();
-            stage_s(tile + 1, 0);
-            s_tile = 0;
+        if (more) {
+            __builtin_amdgcn_wave_barrier();
+            stage_s(tile + stride, 0);
+            __builtin_amdgcn_wave_barrier();
         }
-        // (one barrier a tile: the other set of partial sums is written next,
-        // and read by nobody once all have come here again)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int row = 16 * r + c, tok = 16 * t + 4 * q + i;
+                    if (row >= rows || tok >= tokens) continue;
+                    const int64_t at = (m0 + tok) * p.n + n0 + row;
+                    if (p.parts > 1) p.sums[int64_t(part) * p.m * p.n + at] = acc[r][t][i];
+                    else store_y(p.y, at, acc[r][t][i], p.y_dtype);
+                }
+    }
+    if (p.ks > 1) {
+        // waves without a tile meet the others at both barriers
+        if (!work) __syncthreads();
         __syncthreads();
-        if (p.ks > 1) {
-            for (int o = tid; o < rows * tokens; o += threads) {
-                const int tok = o / rows, row = o - tok * rows;
-                const int w0 = row / (16 * R), rr = row - w0 * (16 * R);
-                const float* src = red + set * red_set + (w0 * p.ks * MT * R + ((tok >> 4) * R + (rr >> 4))) * 256 +
-                                   (rr & 15) * 16 + (tok & 15);
-                float v = 0.0f;
-                for (int w = 0; w < p.ks; ++w) v += src[w * (MT * R * 256)];
-                store_y(p.y, (m0 + tok) * p.n + n0 + row, v, p.y_dtype);
-            }
-            set ^= 1;
+        const int64_t n0 = int64_t(group) * tws * (16 * R);
+        const int rows = int(p.n - n0 < tws * 16 * R ? p.n - n0 : tws * 16 * R);
+        for (int o = tid; o < rows * tokens; o += threads) {
+            const int tok = o / rows, row = o - tok * rows;
+            const int w1 = row / (16 * R), rr = row - w1 * (16 * R);
+            const float* src = red + ((w1 * p.ks * MT + (tok >> 4)) * R + (rr >> 4)) * 256 + (tok & 15) * 16 + (rr & 15);
+            float v = 0.0f;
+            for (int w = 0; w < p.ks; ++w) v += src[w * (MT * R * 256)];
+            const int64_t at = (m0 + tok) * p.n + n0 + row;
+            if (p.parts > 1) p.sums[int64_t(part) * p.m * p.n + at] = v;
+            else store_y(p.y, at, v, p.y_dtype);
         }
     }
 }
 
-constexpr int64_t kLdsCu = 160 * 1024;
-constexpr int64_t kOneX = 84 * 1024;     // activations that stay in LDS
-constexpr int64_t kScaleLds = 24 * 1024; // scales of several tiles
-
-// Waves: KS runs of K (8, so that a workgroup reads long pieces of few rows),
-// the rest sets of rows.  Activations in phases (PH) where they, or a tile's
-// scales, do not fit in LDS.
-template <int XT, int G, int R, int MT, int D, bool PH>
-hipError_t launch(Args a, hipStream_t stream) {
-    const auto kernel = q4_gemv_kernel<XT, G, R, MT, D, PH>;
-    constexpr int kChunkX = XT == TL_I8 ? 128 : 256, NS = 128 / G;
-    const int64_t chunks = a.k / 128;
-    const int waves = PH || chunks >= 8 ? 8 : int(chunks);
-    const int64_t tokens = a.m < 16 * MT ? a.m : 16 * MT;
-    int64_t tile_rows = 0, fixed = 0, lds = 0;
-    const auto size = [&](int64_t slots) {   // LDS without scales
-        return tokens * (slots * kChunkX + 16) + (XT == TL_F16 ? 0 : slots * 64 * MT) +
-               (a.ks > 1 ? 2 * waves * MT * R * 1024 : 0);
-    };
-    for (a.ks = waves;; a.ks /= 2) {
-        tile_rows = 16 * R * (waves / a.ks);
-        a.c = int((chunks + a.ks - 1) / a.ks);
-        a.p = a.c;
-        if (!PH) {
-            fixed = size(chunks);
-            break;
-        }
-        // the longest phase (a multiple of D, at most all) that lets two
-        // workgroups run on a compute unit
-        const auto phase = [&](int64_t pp) { return size(a.ks * pp) + tile_rows * a.ks * pp * NS * 2; };
-        a.p = (a.c + D - 1) / D * D;
-        while (a.p > D && phase(a.p) > kLdsCu / 2) a.p -= D;
-        fixed = size(int64_t(a.ks) * a.p);
-        if (phase(a.p) <= kLdsCu / 2 || a.ks == 1) break;
+// y = the parts' sums added in order
+__global__ __launch_bounds__(256) void q4_join_kernel(const float* __restrict__ sums, int parts, int64_t count,
+                                                      void* __restrict__ y, int y_dtype) {
+    const int64_t step = int64_t(gridDim.x) * 256;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < count; i += step) {
+        float v = sums[i];
+        for (int s = 1; s < parts; ++s) v += sums[s * count + i];
+        store_y(y, i, v, y_dtype);
     }
-    a.tiles = int((a.n + tile_rows - 1) / tile_rows);
-    const int64_t s_tile = tile_rows * (PH ? int64_t(a.ks) * a.p : chunks) * NS * 2;
-    // as many workgroups as run at once, each with a run of tiles
-    const auto split = [&](int64_t per_cu) {
-        const int64_t most = per_cu * cu_count();
-        a.per_wg = int((a.tiles + most - 1) / most);
-        const int64_t room = kLdsCu / per_cu - fixed;
-        const int64_t fit = (room < kScaleLds ? room : kScaleLds) / s_tile;
-        a.s_tiles = PH || fit < 1 ? 1 : fit < a.per_wg ? int(fit) : a.per_wg;
-        lds = fixed + a.s_tiles * s_tile;
-    };
-    split(2);
-    if (lds > kLdsCu / 2) split(1);
-    if (lds > kLdsCu) return hipErrorInvalidValue;
-    const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), int(kLdsCu));
+}
+
+constexpr int64_t kLds = 80 * 1024;   // two workgroups on a compute unit
+constexpr int kScaleLds = 2560;       // scales of a wave: K = 5120 of 32 rows in groups of 128
+
+struct Plan {
+    int r, mt, l, parts, ks, d, seg;
+    int64_t s_bytes, lds;
+};
+
+// LDS bytes of a workgroup with parts of l chunks, and of a wave's scales
+template <int XT, int G>
+void size_lds(Plan& p, int64_t tokens) {
+    const int lw = (p.l + p.ks - 1) / p.ks, chunk = 16 * p.r * (128 / G) * 2;
+    p.seg = lw;
+    if (lw * chunk > kScaleLds) p.seg = kScaleLds / chunk / p.d * p.d;   // whole turns of the ring
+    p.s_bytes = (p.seg * chunk + 15) / 16 * 16;
+    p.lds = tokens * (int64_t(p.l) * chunk_bytes<XT>() + 16) + int64_t(p.l) * chunk_floats<XT>() * ((tokens + 3) / 4 * 16) +
+            kWaves * p.s_bytes;
+    const int64_t red = p.ks > 1 ? int64_t(kWaves) * p.mt * p.r * 1024 : 0;
+    if (p.lds < red) p.lds = red;
+}
+
+// chunks of weights a wave has on the way
+constexpr int ring_depth(int r, int mt) { return mt > 1 ? 4 : r == 2 ? 4 : 6; }
+
+template <int XT, int G>
+Plan q4_plan(int64_t m, int64_t n, int64_t k) {
+    const int64_t chunks = k / 128, slots = int64_t(cu_count()) * 2 * kWaves;
+    Plan p;
+    p.mt = m <= 16 ? 1 : m <= 32 ? 2 : m <= 48 ? 3 : 4;
+    const int64_t tokens = m < 16 * p.mt ? m : 16 * p.mt;
+    p.r = n >= 32 * slots && p.mt == 1 ? 2 : 1;
+    p.d = ring_depth(p.r, p.mt);
+    const int64_t tiles = (n + 16 * p.r - 1) / (16 * p.r);
+    // as many waves on a tile as run at once, as few parts as LDS allows
+    for (p.ks = kWaves;; p.ks /= 2) {
+        for (p.parts = 1;; ++p.parts) {
+            p.l = int((chunks + p.parts - 1) / p.parts);
+            size_lds<XT, G>(p, tokens);
+            if (p.l == 1 || p.lds <= kLds) break;
+        }
+        p.parts = int((chunks + p.l - 1) / p.l);
+        if (p.ks == 1 || (tiles * p.parts * p.ks <= slots && p.l >= p.ks)) return p;
+    }
+}
+
+template <int XT, int G, int R, int MT, int V>
+hipError_t launch(Args a, const Plan& p, hipStream_t stream) {
+    const auto kernel = q4_gemv_kernel<XT, G, R, MT, ring_depth(R, MT), V>;
+    a.parts = p.parts;
+    a.l = p.l;
+    a.ks = p.ks;
+    a.lw = (p.l + p.ks - 1) / p.ks;
+    a.tiles = int((a.n + 16 * R - 1) / (16 * R));
+    const int tws = kWaves / p.ks;
+    a.groups = (a.tiles + tws - 1) / tws;
+    const int most = 2 * cu_count() / p.parts > 0 ? 2 * cu_count() / p.parts : 1;
+    if (p.ks == 1 && a.groups > most) a.groups = most;
+    a.seg = p.seg;
+    a.s_bytes = int(p.s_bytes);
+    const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), 160 * 1024);
     if (e != hipSuccess) return e;
-    const dim3 grid(unsigned((a.tiles + a.per_wg - 1) / a.per_wg), unsigned((a.m + 16 * MT - 1) / (16 * MT)));
-    hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), unsigned(lds), stream, a);
+    const dim3 grid(unsigned(a.groups * a.parts), unsigned((a.m + 16 * MT - 1) / (16 * MT)));
+    hipLaunchKernelGGL(kernel, grid, dim3(64 * kWaves), unsigned(p.lds), stream, a);
+    if (p.parts > 1) {
+        const int64_t count = int64_t(a.m) * a.n, g = (count + 255) / 256;
+        hipLaunchKernelGGL(q4_join_kernel, dim3(unsigned(g < 8192 ? g : 8192)), dim3(256), 0, stream, a.sums, a.parts,
+                           count, a.y, a.y_dtype);
+    }
     return hipGetLastError();
 }
 
-template <int XT, int G, int R>
-hipError_t launch_mt(const Args& a, hipStream_t stream) {
-    if (a.m > 48) return launch<XT, G, G == 32 ? 1 : R, 4, 2, true>(a, stream);   // (registers)
-    if (a.m > 32) return launch<XT, G, R, 3, 2, true>(a, stream);
-    if (a.m > 16) return launch<XT, G, R, 2, 2, true>(a, stream);
-    const int64_t chunks = a.k / 128;
-    if (a.m * chunks * (XT == TL_I8 ? 128 : 256) > kOneX || 16 * R * chunks * (256 / G) > kScaleLds)
-        return launch<XT, G, R, 1, 2, true>(a, stream);
-    return launch<XT, G, R, 1, 4, false>(a, stream);
-}
-
 template <int XT, int G>
-hipError_t launch_rows(const Args& a, hipStream_t stream) {
-    return a.n >= 32 * int64_t(cu_count()) ? launch_mt<XT, G, 2>(a, stream) : launch_mt<XT, G, 1>(a, stream);
+hipError_t launch_rows(const Args& a, int64_t m, hipStream_t stream) {
+    const Plan p = q4_plan<XT, G>(m, a.n, a.k);
+    if (a.m == 1) return p.r == 2 ? launch<XT, G, 2, 1, 1>(a, p, stream) : launch<XT, G, 1, 1, 1>(a, p, stream);
+    switch (p.mt) {
+        case 1: return p.r == 2 ? launch<XT, G, 2, 1, 4>(a, p, stream) : launch<XT, G, 1, 1, 4>(a, p, stream);
+        case 2: return launch<XT, G, 1, 2, 4>(a, p, stream);
+        case 3: return launch<XT, G, 1, 3, 4>(a, p, stream);
+        default: return launch<XT, G, 1, 4, 4>(a, p, stream);
+    }
 }
 
 }  // namespace
 
-int64_t q4_gemv_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
+int64_t q4_gemv_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+    // the most parts any type of activations and group size takes
+    int64_t parts = 1;
+    const auto most = [&](const Plan& p) { parts = p.parts > parts ? p.parts : parts; };
+    most(q4_plan<TL_F16, 32>(m, n, k));
+    most(q4_plan<TL_F16, 64>(m, n, k));
+    most(q4_plan<TL_F16, 128>(m, n, k));
+    most(q4_plan<TL_BF16, 32>(m, n, k));
+    most(q4_plan<TL_BF16, 64>(m, n, k));
+    most(q4_plan<TL_BF16, 128>(m, n, k));
+    most(q4_plan<TL_I8, 32>(m, n, k));
+    most(q4_plan<TL_I8, 64>(m, n, k));
+    most(q4_plan<TL_I8, 128>(m, n, k));
+    return parts > 1 ? parts * m * n * 4 : 0;
+}
 
 hipError_t launch_q4_gemv(const uint8_t* packed, const uint16_t* scales, int group, const void* x,
                           int x_dtype, const float* x_scales, int64_t m, int64_t n, int64_t k, void* y,
-                          int y_dtype, void*, hipStream_t stream) {
+                          int y_dtype, void* ws, hipStream_t stream) {
     // a grid's second dimension ends at 65535: at most 65535 * 16 tokens a launch
     constexpr int64_t kMaxTokens = 65535 * 16;
     const int64_t xb = x_dtype == TL_I8 ? 1 : 2, yb = y_dtype == TL_F32 ? 4 : 2;
     for (int64_t m0 = 0; m0 < m; m0 += kMaxTokens) {
         const int64_t mt = m - m0 < kMaxTokens ? m - m0 : kMaxTokens;
         const Args a = {packed, scales, static_cast<const uint8_t*>(x) + m0 * k * xb,
-                        x_scales ? x_scales + m0 * (k / 128) : nullptr,
-                        static_cast<uint8_t*>(y) + m0 * n * yb, n, k, int(mt), y_dtype, 0, 0, 0, 0, 0, 0};
-#define TL_Q4_GROUP(XT)                                             \
-    (group == 32   ? launch_rows<XT, 32>(a, stream)              \
-     : group == 64 ? launch_rows<XT, 64>(a, stream)              \
-                   : launch_rows<XT, 128>(a, stream))
+                        x_scales ? x_scales + m0 * (k / 128) : nullptr, static_cast<uint8_t*>(y) + m0 * n * yb,
+                        static_cast<float*>(ws), n, k, int(mt), y_dtype, 0, 0, 0, 0, 0, 0, 0, 0};
+#define TL_Q4_GROUP(XT)                                                \
+    (group == 32   ? launch_rows<XT, 32>(a, m, stream)                 \
+     : group == 64 ? launch_rows<XT, 64>(a, m, stream)                 \
+                   : launch_rows<XT, 128>(a, m, stream))
         const hipError_t e = x_dtype == TL_I8    ? TL_Q4_GROUP(TL_I8)
                              : x_dtype == TL_F16 ? TL_Q4_GROUP(TL_F16)
                                                  : TL_Q4_GROUP(TL_BF16);
