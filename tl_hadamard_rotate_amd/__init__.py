@@ -10,6 +10,7 @@ raises at first use.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -490,6 +491,13 @@ def q4_gemv_workspace_bytes(m: int, n: int, k: int) -> int:
     return b
 
 
+@functools.lru_cache(maxsize=4096)
+def _q4_workspace(device: torch.device, m: int, n: int, k: int) -> int:
+    """q4_gemv_workspace_bytes of a shape, asked once a device."""
+    with torch.cuda.device(device):
+        return q4_gemv_workspace_bytes(m, n, k)
+
+
 def q4_gemv(packed, scales, x, x_scales=None, out_dtype=torch.float32, out=None,
             workspace=None) -> torch.Tensor:
     """y[M, N] = x . dequant4(packed, scales)^T for few tokens (M <= 64): x
@@ -526,8 +534,7 @@ def q4_gemv(packed, scales, x, x_scales=None, out_dtype=torch.float32, out=None,
         wb = workspace.numel()
         _need_like(workspace, "workspace", torch.uint8, (wb,), device)
     elif m * k > 16384:
-        with torch.cuda.device(device):
-            wb = q4_gemv_workspace_bytes(m, n, k)
+        wb = _q4_workspace(device, m, n, k)
         workspace = torch.empty(wb, dtype=torch.uint8, device=device) if wb else None
     _call("tl_q4_gemv", device, packed.data_ptr(), scales.data_ptr(), group, x.data_ptr(), xd,
           None if x_scales is None else x_scales.data_ptr(), m, n, k, out.data_ptr(), yd,

@@ -30,13 +30,18 @@
 // Work split.  K is cut into `parts` of L chunks such that the activations of
 // a part fit in LDS; a workgroup stages one part once and each of its waves
 // then goes through tiles of 16 R weight rows on its own, without a barrier,
-// D chunks of weights on the way.  Where rows are few, KS waves share a tile,
+// D chunks at a time: their weights are requested together and used in order
+// (a ring refilled chunk by chunk behind conditions made the compiler wait for
+// every load in flight before each use).  Where rows are few, KS waves share a tile,
 // each a run of the part's chunks, and add their sums through LDS.  With
 // several parts the sums go to the workspace and a second kernel adds them.
 // All sums are taken in a fixed order.  A tile's scales, one run of memory or
 // a piece of each row, go through the wave's own LDS, SEG chunks at a time:
 // read as they are used, 2 bytes from each of 16 rows, they took longer than
-// the weights.
+// the weights.  Both come by loads that write LDS directly (through registers
+// they waited for one another), in places of 16 (4) bytes a lane in order; the
+// pieces of a token's activations are exchanged by 3 bits of its number, so
+// that 8 tokens at one place lie on different banks.
 #include "elem.h"
 #include "tl_internal.h"
 
@@ -124,6 +129,16 @@ __device__ __forceinline__ void order_i8(uint4v& v) {
                __builtin_amdgcn_perm(d, c, 0x05010400u), __builtin_amdgcn_perm(d, c, 0x07030602u)};
 }
 
+// a load of B bytes a lane that writes LDS itself, lane i at l + max(B, 4) * i
+template <int B>
+__device__ __forceinline__ void load_lds(const void* g, void* l) {
+    const auto from = (const __attribute__((address_space(1))) void*)g;
+    const auto to = (__attribute__((address_space(3))) void*)l;
+    if constexpr (B == 16) __builtin_amdgcn_global_load_lds(from, to, 16, 0, 0);
+    else if constexpr (B == 4) __builtin_amdgcn_global_load_lds(from, to, 4, 0, 0);
+    else __builtin_amdgcn_global_load_lds(from, to, 2, 0, 0);
+}
+
 // Octets of the chunk that lane quarter q and (16 bits, or groups of 32) word
 // j, (8 bits) pair of words j, meet in: first_octet(q) + octet_step(j)
 template <int G>
@@ -144,11 +159,12 @@ constexpr int chunk_floats() { return XT == TL_F16 ? 0 : 1; }
 
 // One chunk's sums added to acc[r][t]: lane (q, c) holds weight row 16 r + c
 // and tokens 16 t + 4 q .. + V - 1.  In LDS: xa[t] the lane's token's
-// activations, fa[t] the chunk's factors of tokens 16 t + 4 q .. + 3, sc its
-// scales of row c (row 16 r + c is r * row_step elements further).
+// activations (xsw[t] in the offset: where the lane starts, exchanged by the
+// token's bits), fa[t] the chunk's factors of tokens 16 t + 4 q .. + 3, sc its
+// scales of row c (row 16 r + c is r * row_step bytes further).
 template <int XT, int G, int R, int MT, int V>
-__device__ __forceinline__ void consume(const uint4v (&wr)[R], const uint8_t* const (&xa)[MT], const uint16_t* sc,
-                                        int row_step, const float* const (&fa)[MT], float (&acc)[R][MT][V]) {
+__device__ __forceinline__ void consume(const uint4v (&wr)[R], const uint8_t* const (&xa)[MT],
+                                        const int (&xsw)[MT], const uint8_t* sc, int row_step, const float* const (&fa)[MT], float (&acc)[R][MT][V]) {
     constexpr int NS = 128 / G;               // scales of the chunk
     constexpr bool kPair = XT == TL_I8 && G != 32;
     constexpr int NX = kPair ? 2 : 4;         // matrix instructions along K
@@ -175,7 +191,7 @@ __device__ __forceinline__ void consume(const uint4v (&wr)[R], const uint8_t* co
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         uint32_t sb[2] = {};
-        if constexpr (NS == 1) sb[0] = sc[r * row_step];
+        if constexpr (NS == 1) sb[0] = *reinterpret_cast<const uint16_t*>(sc + r * row_step);
         else if constexpr (NS == 2) sb[0] = *reinterpret_cast<const uint32_t*>(sc + r * row_step);
         else {
             const uint2 u = *reinterpret_cast<const uint2*>(sc + r * row_step);
@@ -197,7 +213,7 @@ __device__ __forceinline__ void consume(const uint4v (&wr)[R], const uint8_t* co
         if constexpr (XT != TL_I8) {
             half8v a[MT];
 #pragma unroll
-            for (int t = 0; t < MT; ++t) a[t] = *reinterpret_cast<const half8v*>(xa[t] + at);
+            for (int t = 0; t < MT; ++t) a[t] = *reinterpret_cast<const half8v*>(xa[t] + (at ^ xsw[t]));
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const half8v b = decode_f16(w[r][j]);
@@ -208,7 +224,12 @@ __device__ __forceinline__ void consume(const uint4v (&wr)[R], const uint8_t* co
         } else if constexpr (!kPair) {
             int64_t a[MT];
 #pragma unroll
-            for (int t = 0; t < MT; ++t) a[t] = *reinterpret_cast<const int64_t*>(xa[t] + at);
+            for (int t = 0; t < MT; ++t) {
+                const uint2 v = *reinterpret_cast<const uint2*>(xa[t] + (at ^ xsw[t]));
+                const uint32_t lo = __builtin_amdgcn_perm(v.y, v.x, 0x05010400u);
+                const uint32_t hi = __builtin_amdgcn_perm(v.y, v.x, 0x07030602u);
+                a[t] = int64_t(uint64_t(hi) << 32 | lo);
+            }
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const uint32_t lo = (w[r][j] << 4) & 0xF0F0F0F0u, hi = w[r][j] & 0xF0F0F0F0u;
@@ -220,7 +241,11 @@ __device__ __forceinline__ void consume(const uint4v (&wr)[R], const uint8_t* co
         } else {
             int4v a[MT];
 #pragma unroll
-            for (int t = 0; t < MT; ++t) a[t] = *reinterpret_cast<const int4v*>(xa[t] + at);
+            for (int t = 0; t < MT; ++t) {
+                uint4v v = *reinterpret_cast<const uint4v*>(xa[t] + (at ^ xsw[t]));
+                order_i8(v);
+                a[t] = __builtin_bit_cast(int4v, v);
+            }
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const uint32_t u = w[r][2 * j], v = w[r][2 * j + 1];
@@ -293,122 +318,112 @@ __global__ __launch_bounds__(64 * kWaves, MT == 1 ? 4 : 2) void q4_gemv_kernel(c
 
     // LDS: activations [token][chunk], factors [chunk][TS], TS the tokens
     // rounded up to fours, the waves' scales [row][chunk]; at the end partial sums (KS > 1)
-    const int xstride = p.l * kCB + 16;       // 16: rows on different banks
+    const int xstride = len * kCB;
     const int ts = (tokens + 3) / 4 * 4;
     uint8_t* const lx = smem;
-    float* const lf = reinterpret_cast<float*>(lx + tokens * xstride);
-    uint16_t* const ls = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(lf + p.l * (kF * ts)) +
-                                                     wave * p.s_bytes);
+    float* const lf = reinterpret_cast<float*>(lx + tokens * p.l * kCB);
+    uint8_t* const ls = reinterpret_cast<uint8_t*>(lf + p.l * (kF * ts)) + wave * p.s_bytes;
     float* const red = reinterpret_cast<float*>(smem);
 
     // this wave's tiles: tile, tile + stride, ...
     const int stride = p.groups * tws;
     int tile = group * tws + tw;
 
-    // Weights on the way: chunk i of a tile in ring[i % D].  voff: the lane's
-    // rows of the tile (rows that do not exist repeat the last one; their sums
-    // are not stored).
-    uint4v ring[D][R];
-    uint32_t voff[R], vnext[R];
-    const auto enter = [&](int t, uint32_t (&v)[R]) {
+    // Weights on the way: D chunks of a tile.  voff: the lane's rows of the
+    // tile (rows that do not exist repeat the last one; their sums are not
+    // stored).
+    uint4v buf[D][R];
+    uint32_t voff[R];
+    const auto enter = [&](int t) {
         const int64_t n0 = int64_t(t) * (16 * R);
         const int last = int(p.n - n0 < 16 * R ? p.n - n0 : 16 * R) - 1;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int row = 16 * r + c;
-            v[r] = uint32_t(row < last ? row : last) * uint32_t(row_bytes) + 16u * uint32_t(q);
+            voff[r] = uint32_t(row < last ? row : last) * uint32_t(row_bytes) + 16u * uint32_t(q);
         }
         return p.packed + (n0 * row_bytes + int64_t(c0 + w0) * 64);
     };
-    const auto fetch = [&](const uint8_t* b, const uint32_t (&v)[R], uint4v (&w)[R]) {
+    // chunks i0 .. i0 + D - 1 (past the end the last one again)
+    const auto fetch = [&](const uint8_t* b, int i0) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) w[r] = *reinterpret_cast<const uint4v*>(b + v[r]);
+        for (int d = 0; d < D; ++d) {
+            const uint8_t* const from = b + 64 * (i0 + d < mine ? i0 + d : mine - 1);
+#pragma unroll
+            for (int r = 0; r < R; ++r) buf[d][r] = *reinterpret_cast<const uint4v*>(from + voff[r]);
+        }
     };
-    // scales of chunks [i0, i0 + SEG) of this wave's of a tile into its LDS,
-    // [row][chunk]: one run of memory when they are all of the rows
-    const auto stage_s = [&](int t, int i0) {
+    // Scales of chunks [i0, i0 + SEG) of this wave's of a tile into its LDS,
+    // [row][chunk]: one run of memory when they are all of the rows, else
+    // places of 4 bytes (a scale, or two)
+    constexpr int kPlaces = NS > 2 ? NS / 2 : 1;
+    const auto load_s = [&](int t, int i0) {
         const int64_t n0 = int64_t(t) * (16 * R);
         const int rows = int(p.n - n0 < 16 * R ? p.n - n0 : 16 * R);
         const int span = mine - i0 < p.seg ? mine - i0 : p.seg;
         const uint16_t* const src = p.scales + (n0 * chunks + c0 + w0 + i0) * NS;
-        const int row_e = span * NS, count = rows * row_e;
         if (span == chunks) {
-            for (int i = 8 * lane; i < count; i += 512) {
-                if (i + 8 <= count) *reinterpret_cast<uint4v*>(ls + i) = *reinterpret_cast<const uint4v*>(src + i);
-                else
-                    for (int j = i; j < count; ++j) ls[j] = src[j];
-            }
-        } else if (span > 0) {
-            // (row, chunk) units of a lane, the row advanced without a division
-            int row = lane / span, i = lane - row * span;
-            while (row < rows) {
-                const uint16_t* const from = src + (int64_t(row) * chunks + i) * NS;
-                uint16_t* const to = ls + row * row_e + i * NS;
-                if constexpr (NS == 1) *to = *from;
-                else if constexpr (NS == 2) *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(from);
-                else *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(from);
-                i += 64;
-                while (i >= span) {
-                    i -= span;
-                    ++row;
-                }
+            const int count = rows * span * NS;
+            for (int i = 0; i < count / 8; i += 64)
+                if (i + lane < count / 8) load_lds<16>(src + 8 * (i + lane), ls + 16 * i);
+            const int tail = count / 8 * 8 + lane;   // the end of the scales
+            if (tail < count) reinterpret_cast<uint16_t*>(ls)[tail] = src[tail];
+        } else {
+            const int per_row = span * kPlaces, count = rows * per_row;
+            const float inv = 1.0f / float(per_row);
+            for (int i = 0; i < count; i += 64) {
+                const int u = i + lane, row = int((float(u) + 0.5f) * inv);   // exact: u < 2^16
+                if (u < count)
+                    load_lds<NS == 1 ? 2 : 4>(src + int64_t(row) * (chunks * NS) + (u - row * per_row) * (NS == 1 ? 1 : 2),
+                                              ls + 4 * i);
             }
         }
     };
-    const bool work = tile < p.tiles;
+    const bool work = tile < p.tiles && mine > 0;
     const uint8_t* base = p.packed;
-    if (work) {
-        base = enter(tile, voff);
-#pragma unroll
-        for (int d = 0; d < D; ++d)
-            if (d < mine) fetch(base + 64 * d, voff, ring[d]);
-    }
 
-    // the part's activations to LDS
+    // the part's activations (and their scales) to LDS
     {
-        constexpr int U = 4;
         const uint8_t* const xt = p.x + (m0 * p.k + int64_t(c0) * 128) * (kCB / 128);
-        const float* const xst = XT == TL_I8 ? p.xs + m0 * chunks + c0 : nullptr;
-        const int per_token = len * kPieces;
-        int t = tid / per_token, e = tid - t * per_token;
-        while (t < tokens) {
-            uint4v v[U] = {};
-            int tok[U], at[U];
-            float f[U] = {};
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                tok[u] = t;
-                at[u] = e;
-                if (t < tokens) {
-                    v[u] = *reinterpret_cast<const uint4v*>(xt + int64_t(t) * p.k * (kCB / 128) + 16 * e);
-                    if (XT == TL_I8 && e % kPieces == 0) f[u] = xst[int64_t(t) * chunks + e / kPieces];
-                    e += threads;
-                    while (e >= per_token) {
-                        e -= per_token;
-                        ++t;
-                    }
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                // (a chunk's lanes are a row of 16 or half of one, present or
-                // absent together)
-                if (tok[u] >= tokens) continue;
-                if constexpr (XT == TL_BF16) f[u] = convert_bf16(v[u]);
-                if constexpr (XT == TL_I8) order_i8(v[u]);
-                *reinterpret_cast<uint4v*>(lx + tok[u] * xstride + 16 * at[u]) = v[u];
-                if (kF && at[u] % kPieces == 0) lf[at[u] / kPieces * ts + tok[u]] = f[u];
-            }
+        const int per_token = len * kPieces, count = tokens * per_token;
+        const float inv = 1.0f / float(per_token);
+        for (int i = 64 * wave; i < count; i += threads) {
+            const int u = i + lane, t = int((float(u) + 0.5f) * inv);   // exact: u < 2^16
+            if (u < count)
+                load_lds<16>(xt + int64_t(t) * p.k * (kCB / 128) + 16 * ((u - t * per_token) ^ (t & 7)), lx + 16 * i);
         }
+        if constexpr (XT == TL_I8)
+            for (int i = 64 * wave; i < len * ts; i += threads) {
+                const int u = i + lane, slot = u / ts, t = u - slot * ts;
+                if (slot < len && t < tokens) load_lds<4>(p.xs + (m0 + t) * chunks + c0 + slot, lf + i);
+            }
     }
-    if (work) stage_s(tile, 0);
+    if (work) {
+        load_s(tile, 0);
+        base = enter(tile);
+        fetch(base, 0);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
+    if constexpr (XT == TL_BF16) {
+        const int count = tokens * len * kPieces;   // whole rows of 16 lanes: a chunk
+        for (int i = tid; i < count; i += threads) {
+            uint4v v = *reinterpret_cast<const uint4v*>(lx + 16 * i);
+            const float f = convert_bf16(v);
+            *reinterpret_cast<uint4v*>(lx + 16 * i) = v;
+            const int t = i / (len * kPieces), e = i - t * (len * kPieces);
+            if (e % kPieces == 0) lf[e / kPieces * ts + t] = f;
+        }
+        __syncthreads();
+    }
 
     const uint8_t* xa[MT];
+    int xsw[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
         const int tok = 16 * t + c < tokens ? 16 * t + c : tokens - 1;   // absent tokens repeat the last
-        xa[t] = lx + tok * xstride + first_octet<G>(q) * (XT == TL_I8 ? 8 : 16) + w0 * kCB;
+        xa[t] = lx + tok * xstride + w0 * kCB;
+        xsw[t] = (first_octet<G>(q) * (XT == TL_I8 ? 8 : 16)) ^ (16 * (tok & 7));
     }
     const float* fa[MT];
 #pragma unroll
@@ -419,20 +434,16 @@ __global__ __launch_bounds__(64 * kWaves, MT == 1 ? 4 : 2) void q4_gemv_kernel(c
         const int64_t n0 = int64_t(tile) * (16 * R);
         const int rows = int(p.n - n0 < 16 * R ? p.n - n0 : 16 * R);
         const bool more = tile + stride < p.tiles;
-        const uint8_t* nbase = base;
-        if (more) nbase = enter(tile + stride, vnext);
         int seg0 = 0;
-        for (int i0 = 0; i0 < mine; i0 += D) {
+        for (int i0 = 0; i0 < mine;) {
             if (i0 == seg0 + p.seg) {
-                // (the wave's LDS operations run in order: its reads of the
-                // old scales are done, its reads of the new ones follow)
                 seg0 = i0;
-                __builtin_amdgcn_wave_barrier();
-                stage_s(tile, seg0);
-                __builtin_amdgcn_wave_barrier();
+                load_s(tile, seg0);
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             }
-            const int row_e = (mine - seg0 < p.seg ? mine - seg0 : p.seg) * NS;
-            const uint16_t* const sc = ls + c * row_e - seg0 * NS;
+            const int span = mine - seg0 < p.seg ? mine - seg0 : p.seg;
+            const int s_step = span == chunks ? 2 * NS : 4 * kPlaces, row_step = span * s_step;   // bytes
+            const uint8_t* const sc = ls + c * row_step - seg0 * s_step;
 #pragma unroll
             for (int d = 0; d < D; ++d) {
                 const int i = i0 + d;
@@ -443,15 +454,11 @@ __global__ __launch_bounds__(64 * kWaves, MT == 1 ? 4 : 2) void q4_gemv_kernel(c
                 const float* fc[MT];
 #pragma unroll
                 for (int t = 0; t < MT; ++t) fc[t] = fa[t] + i * (kF * ts);
-                consume<XT, G, R, MT, V>(ring[d], xc, sc + i * NS, 16 * row_e, fc, acc);
-                // the chunk that uses this place next, of this tile or the next
-                if (i + D < mine) fetch(base + 64 * (i + D), voff, ring[d]);
-                else if (more) fetch(nbase + 64 * d, vnext, ring[d]);
+                consume<XT, G, R, MT, V>(buf[d], xc, xsw, sc + i * s_step, 16 * row_step, fc, acc);
             }
+            i0 += D;
+            if (i0 < mine) fetch(base, i0);
         }
-        base = nbase;
-#pragma unroll
-        for (int r = 0; r < R; ++r) voff[r] = vnext[r];
         if (p.ks > 1) {
             // (one tile a wave then)
             __syncthreads();
@@ -463,11 +470,6 @@ __global__ __launch_bounds__(64 * kWaves, MT == 1 ? 4 : 2) void q4_gemv_kernel(c
                     for (int i = 0; i < V; ++i)
                         red[((wave * MT + t) * R + r) * 256 + (4 * q + i) * 16 + c] = acc[r][t][i];
             break;
-        }
-        if (more) {
-            __builtin_amdgcn_wave_barrier();
-            stage_s(tile + stride, 0);
-            __builtin_amdgcn_wave_barrier();
         }
 #pragma unroll
         for (int r = 0; r < R; ++r)
@@ -481,10 +483,19 @@ __global__ __launch_bounds__(64 * kWaves, MT == 1 ? 4 : 2) void q4_gemv_kernel(c
                     if (p.parts > 1) p.sums[int64_t(part) * p.m * p.n + at] = acc[r][t][i];
                     else store_y(p.y, at, acc[r][t][i], p.y_dtype);
                 }
+        if (more) {
+            // the next tile's scales (the old ones have been read), then its
+            // weights; all but the latter are awaited
+            load_s(tile + stride, 0);
+            asm volatile("" ::: "memory");
+            base = enter(tile + stride);
+            fetch(base, 0);
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(D * R) : "memory");
+        }
     }
     if (p.ks > 1) {
         // waves without a tile meet the others at both barriers
-        if (!work) __syncthreads();
+        if (tile >= p.tiles) __syncthreads();
         __syncthreads();
         const int64_t n0 = int64_t(group) * tws * (16 * R);
         const int rows = int(p.n - n0 < tws * 16 * R ? p.n - n0 : tws * 16 * R);
@@ -512,49 +523,73 @@ __global__ __launch_bounds__(256) void q4_join_kernel(const float* __restrict__ 
     }
 }
 
-constexpr int64_t kLds = 80 * 1024;   // two workgroups on a compute unit
+constexpr int64_t kLdsCu = 160 * 1024;
 constexpr int kScaleLds = 2560;       // scales of a wave: K = 5120 of 32 rows in groups of 128
 
+// How a call is split; the same for the workspace and the launch.
 struct Plan {
     int r, mt, l, parts, ks, d, seg;
     int64_t s_bytes, lds;
 };
 
+// chunks of weights a wave has on the way
+constexpr int ring_depth(int r, int mt) { return r == 2 ? 2 : mt == 1 ? 4 : 5; }
+
 // LDS bytes of a workgroup with parts of l chunks, and of a wave's scales
 template <int XT, int G>
 void size_lds(Plan& p, int64_t tokens) {
-    const int lw = (p.l + p.ks - 1) / p.ks, chunk = 16 * p.r * (128 / G) * 2;
+    const int lw = (p.l + p.ks - 1) / p.ks;
+    int chunk = 16 * p.r * (G == 128 ? 4 : 256 / G);        // bytes of a chunk's scales
+    if (p.parts == 1 && p.ks == 1 && lw * chunk / (G == 128 ? 2 : 1) <= kScaleLds) chunk = 16 * p.r * (256 / G);
     p.seg = lw;
-    if (lw * chunk > kScaleLds) p.seg = kScaleLds / chunk / p.d * p.d;   // whole turns of the ring
+    if (lw * chunk > kScaleLds) p.seg = kScaleLds / chunk / p.d * p.d;   // whole steps
     p.s_bytes = (p.seg * chunk + 15) / 16 * 16;
-    p.lds = tokens * (int64_t(p.l) * chunk_bytes<XT>() + 16) + int64_t(p.l) * chunk_floats<XT>() * ((tokens + 3) / 4 * 16) +
+    p.lds = tokens * int64_t(p.l) * chunk_bytes<XT>() + int64_t(p.l) * chunk_floats<XT>() * ((tokens + 3) / 4 * 16) +
             kWaves * p.s_bytes;
     const int64_t red = p.ks > 1 ? int64_t(kWaves) * p.mt * p.r * 1024 : 0;
     if (p.lds < red) p.lds = red;
 }
 
-// chunks of weights a wave has on the way
-constexpr int ring_depth(int r, int mt) { return mt > 1 ? 4 : r == 2 ? 4 : 6; }
-
+// The split with the least estimated time.  What it weighs was measured at N x
+// K from 1024 x 5120 to 131072 x 5120: weights arrive at 5.3 bytes per ps
+// once about 0.7 of the waves that fit are busy (0.4 of that with few), more
+// waves than fit cost a tenth; staged activations at 12; a second kernel costs
+// 2 us and its sums 6 bytes per ps.
 template <int XT, int G>
 Plan q4_plan(int64_t m, int64_t n, int64_t k) {
-    const int64_t chunks = k / 128, slots = int64_t(cu_count()) * 2 * kWaves;
-    Plan p;
+    const int64_t chunks = k / 128, cus = cu_count();
+    Plan p, best = {};
+    double least = 0;
     p.mt = m <= 16 ? 1 : m <= 32 ? 2 : m <= 48 ? 3 : 4;
-    const int64_t tokens = m < 16 * p.mt ? m : 16 * p.mt;
-    p.r = n >= 32 * slots && p.mt == 1 ? 2 : 1;
+    const int64_t tokens = m < 16 * p.mt ? m : 16 * p.mt, slices = (m + 16 * p.mt - 1) / (16 * p.mt);
+    p.r = p.mt > 1 && n >= 64 * cus ? 2 : 1;
     p.d = ring_depth(p.r, p.mt);
-    const int64_t tiles = (n + 16 * p.r - 1) / (16 * p.r);
-    // as many waves on a tile as run at once, as few parts as LDS allows
-    for (p.ks = kWaves;; p.ks /= 2) {
-        for (p.parts = 1;; ++p.parts) {
+    // one token tile: two workgroups on a compute unit; more: one
+    const int64_t per_cu = p.mt == 1 ? 2 : 1, room = kLdsCu / per_cu;
+    const int64_t tiles = (n + 16 * p.r - 1) / (16 * p.r), slots = cus * per_cu * kWaves;
+    for (p.ks = kWaves; p.ks >= 1; p.ks /= 2) {
+        int tried = 0;
+        for (p.parts = 1; p.parts <= chunks && tried < 5; ++p.parts) {
             p.l = int((chunks + p.parts - 1) / p.parts);
             size_lds<XT, G>(p, tokens);
-            if (p.l == 1 || p.lds <= kLds) break;
+            if (p.lds > room || (chunks + p.l - 1) / p.l != p.parts) continue;
+            ++tried;
+            if (p.ks > 1 && p.l < p.ks) continue;
+            const double waves = double(tiles) * p.parts * p.ks * slices;
+            const double busy = waves < 0.7 * slots ? waves / (0.7 * slots) : 1.0;
+            const double over = p.ks > 1 && waves > 1.125 * slots ? 1.1 : 1.0;
+            double groups = double((tiles + kWaves / p.ks - 1) / (kWaves / p.ks)) * p.parts;
+            if (p.ks == 1 && groups > double(cus * per_cu)) groups = double(cus * per_cu);
+            double us = double(n) * k / 2 * slices / 5.3e6 * over / (0.4 + 0.6 * busy) +
+                        groups * slices * double(tokens) * p.l * chunk_bytes<XT>() / 12e6;
+            if (p.parts > 1) us += 2.0 + double(p.parts) * m * n * 8 / 6e6;
+            if (least == 0 || us < least) {
+                least = us;
+                best = p;
+            }
         }
-        p.parts = int((chunks + p.l - 1) / p.l);
-        if (p.ks == 1 || (tiles * p.parts * p.ks <= slots && p.l >= p.ks)) return p;
     }
+    return best;
 }
 
 template <int XT, int G, int R, int MT, int V>
@@ -567,7 +602,8 @@ hipError_t launch(Args a, const Plan& p, hipStream_t stream) {
     a.tiles = int((a.n + 16 * R - 1) / (16 * R));
     const int tws = kWaves / p.ks;
     a.groups = (a.tiles + tws - 1) / tws;
-    const int most = 2 * cu_count() / p.parts > 0 ? 2 * cu_count() / p.parts : 1;
+    const int per_cu = MT == 1 ? 2 : 1;
+    const int most = per_cu * cu_count() / p.parts > 0 ? per_cu * cu_count() / p.parts : 1;
     if (p.ks == 1 && a.groups > most) a.groups = most;
     a.seg = p.seg;
     a.s_bytes = int(p.s_bytes);
@@ -586,12 +622,12 @@ hipError_t launch(Args a, const Plan& p, hipStream_t stream) {
 template <int XT, int G>
 hipError_t launch_rows(const Args& a, int64_t m, hipStream_t stream) {
     const Plan p = q4_plan<XT, G>(m, a.n, a.k);
-    if (a.m == 1) return p.r == 2 ? launch<XT, G, 2, 1, 1>(a, p, stream) : launch<XT, G, 1, 1, 1>(a, p, stream);
+    if (a.m == 1) return launch<XT, G, 1, 1, 1>(a, p, stream);
     switch (p.mt) {
-        case 1: return p.r == 2 ? launch<XT, G, 2, 1, 4>(a, p, stream) : launch<XT, G, 1, 1, 4>(a, p, stream);
-        case 2: return launch<XT, G, 1, 2, 4>(a, p, stream);
-        case 3: return launch<XT, G, 1, 3, 4>(a, p, stream);
-        default: return launch<XT, G, 1, 4, 4>(a, p, stream);
+        case 1: return launch<XT, G, 1, 1, 4>(a, p, stream);
+        case 2: return p.r == 2 ? launch<XT, G, 2, 2, 4>(a, p, stream) : launch<XT, G, 1, 2, 4>(a, p, stream);
+        case 3: return p.r == 2 ? launch<XT, G, 2, 3, 4>(a, p, stream) : launch<XT, G, 1, 3, 4>(a, p, stream);
+        default: return p.r == 2 ? launch<XT, G, 2, 4, 4>(a, p, stream) : launch<XT, G, 1, 4, 4>(a, p, stream);
     }
 }
 
