@@ -338,46 +338,57 @@ def _need_real(t: torch.Tensor, name: str) -> int:
     """The TL_ type of a contiguous 2-D device tensor of real numbers."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in _REAL:
+    dt = _REAL.get(t.dtype)
+    if dt is None:
         raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
     if not t.is_cuda or t.dim() != 2 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous 2-D device tensor")
-    return _REAL[t.dtype]
+    return dt
+
+
+def _out_type(dtype: torch.dtype) -> int:
+    dt = _REAL.get(dtype)
+    if dt is None:
+        raise TypeError(f"out_dtype must be float32, float16 or bfloat16, got {dtype}")
+    return dt
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _call(name: str, device: torch.device, *args) -> None:
     """One library call on the device's current stream, with that device
     current (a stream and the look-ups of a launch belong to a device)."""
     fn = getattr(_lib or lib(), name)
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, stream)
+    index = device.index
+    if index == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, stream)
+        with torch.cuda.device(index):
+            st = fn(*args, _raw_stream(index))
     if st != 0:
         _check(name, st)
 
 
-def _rms_norm(x, gain, eps, residual, signs, sum_out, out, out_dtype, out_scales):
-    dt = _need_real(x, "x")
-    device, shape = x.device, x.shape
+def _rms_norm(x, dt, gain, eps, residual, signs, sum_out, out, out_dtype, out_scales):
+    device, dtype, shape = x.device, x.dtype, x.shape
     m, k = shape
-    _need_like(gain, "gain", x.dtype, (k,), device)
+    _need_like(gain, "gain", dtype, (k,), device)
+    rp = sp = gp = None
     if residual is not None:
-        _need_like(residual, "residual", x.dtype, shape, device)
+        _need_like(residual, "residual", dtype, shape, device)
         if sum_out is None:
             sum_out = torch.empty_like(x)
         else:
-            _need_like(sum_out, "sum_out", x.dtype, shape, device)
+            _need_like(sum_out, "sum_out", dtype, shape, device)
+        rp, sp = residual.data_ptr(), sum_out.data_ptr()
     elif sum_out is not None:
         raise ValueError("sum_out needs a residual")
     if signs is not None:
         _need_like(signs, "signs", torch.int8, (k,), device)
-    _call("tl_rms_norm", device, x.data_ptr(), None if residual is None else residual.data_ptr(),
-          gain.data_ptr(), None if signs is None else signs.data_ptr(), m, k, dt, eps,
-          None if sum_out is None else sum_out.data_ptr(), out.data_ptr(), out_dtype,
-          None if out_scales is None else out_scales.data_ptr())
+        gp = signs.data_ptr()
+    _call("tl_rms_norm", device, x.data_ptr(), rp, gain.data_ptr(), gp, m, k, dt, eps, sp,
+          out.data_ptr(), out_dtype, None if out_scales is None else out_scales.data_ptr())
     return sum_out
 
 
@@ -388,15 +399,13 @@ def rms_norm(x, gain, eps, residual=None, signs=None, out_dtype=torch.float16, s
     the signed rotation of the ternary linear behind it: ``out`` is then its
     x_rot (see tl_rms_norm).  Returns out, or (out, sum) with a residual; the
     sum x + residual goes to ``sum_out``, which may be x or residual itself."""
-    yd = _REAL.get(out_dtype)
-    if yd is None:
-        raise TypeError("out_dtype must be float32, float16 or bfloat16 (8 bits: rms_norm_i8)")
-    _need_real(x, "x")
+    yd = _out_type(out_dtype)
+    dt = _need_real(x, "x")
     if out is None:
         out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
     else:
         _need_like(out, "out", out_dtype, x.shape, x.device)
-    s = _rms_norm(x, gain, eps, residual, signs, sum_out, out, yd, None)
+    s = _rms_norm(x, dt, gain, eps, residual, signs, sum_out, out, yd, None)
     return out if s is None else (out, s)
 
 
@@ -404,7 +413,7 @@ def rms_norm_i8(x, gain, eps, residual=None, signs=None, sum_out=None, out=None,
     """``rms_norm`` with 8-bit outputs for ``q4_gemv``: returns (codes int8
     [M, K], scales float32 [M, K/128]), and the sum behind them with a
     residual; value = code * scale of its 128."""
-    _need_real(x, "x")
+    dt = _need_real(x, "x")
     m, k = x.shape
     if k % GROUP:
         raise ValueError("K must be a multiple of 128")
@@ -416,7 +425,7 @@ def rms_norm_i8(x, gain, eps, residual=None, signs=None, sum_out=None, out=None,
         scales = torch.empty((m, k // GROUP), dtype=torch.float32, device=x.device)
     else:
         _need_like(scales, "scales", torch.float32, (m, k // GROUP), x.device)
-    s = _rms_norm(x, gain, eps, residual, signs, sum_out, out, TL_I8, scales)
+    s = _rms_norm(x, dt, gain, eps, residual, signs, sum_out, out, TL_I8, scales)
     return (out, scales) if s is None else (out, scales, s)
 
 
@@ -471,9 +480,7 @@ def _q4_shape(packed, scales):
 def q4_dequantize(packed, scales, out_dtype=torch.float16, out=None) -> torch.Tensor:
     """The weights [N, K] that 4-bit codes and scales stand for."""
     n, k, group = _q4_shape(packed, scales)
-    dt = _REAL.get(out_dtype)
-    if dt is None:
-        raise TypeError("out_dtype must be float32, float16 or bfloat16")
+    dt = _out_type(out_dtype)
     if out is None:
         out = torch.empty((n, k), dtype=out_dtype, device=packed.device)
     else:
@@ -522,9 +529,7 @@ def q4_gemv(packed, scales, x, x_scales=None, out_dtype=torch.float32, out=None,
             raise TypeError(f"x must be float16, bfloat16 or int8, got {x.dtype}")
         if x_scales is not None:
             raise ValueError("x_scales go with int8 activations")
-    yd = _REAL.get(out_dtype)
-    if yd is None:
-        raise TypeError("out_dtype must be float32, float16 or bfloat16")
+    yd = _out_type(out_dtype)
     if out is None:
         out = torch.empty((m, n), dtype=out_dtype, device=device)
     else:

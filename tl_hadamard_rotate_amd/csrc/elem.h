@@ -74,12 +74,17 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) 
     }
 }
 
-// v of lane l ^ m: DPP quad permutes for m = 1, 2, a swap of the wave's
-// halves for m = 32, a lane permute otherwise
+// v of lane l ^ m: DPP quad permutes for m = 1, 2, a rotation of a row of 16
+// for m = 8, swaps of rows and halves for m = 16, 32, a lane permute for m = 4
 __device__ __forceinline__ float lane_xor(float v, int m, int l) {
     const int b = __builtin_bit_cast(int, v);
     if (m == 1) return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(b, 0xB1, 0xF, 0xF, false));
     if (m == 2) return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(b, 0x4E, 0xF, 0xF, false));
+    if (m == 8) return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(b, 0x128, 0xF, 0xF, false));
+    if (m == 16) {
+        const auto sw = __builtin_amdgcn_permlane16_swap(uint32_t(b), uint32_t(b), false, false);
+        return __builtin_bit_cast(float, (l & 16) ? sw[0] : sw[1]);
+    }
     if (m == 32) {
         const auto sw = __builtin_amdgcn_permlane32_swap(uint32_t(b), uint32_t(b), false, false);
         return __builtin_bit_cast(float, l < 32 ? sw[1] : sw[0]);
@@ -87,10 +92,12 @@ __device__ __forceinline__ float lane_xor(float v, int m, int l) {
     return __shfl_xor(v, m, 64);
 }
 
-// The unscaled transform H (s * v) of a 1024-block, lane l holding elements
-// 16l .. 16l + 15 and the signs in `sg`: index bits 0-3 are butterflied in
-// registers, bits 4-9 (the lane bits) with cross-lane exchanges; fp32 in a
-// fixed order, 10 levels of sums.  The caller multiplies by 1/32 (exact).
+// The unscaled transform H (s * v) of a 1024-block whose index bits lie in 4
+// register and 6 lane bits, in any order (the matrix only asks which bits two
+// indices share): the register bits are butterflied in registers, the lane
+// bits with cross-lane exchanges; fp32 in a fixed order, 10 levels of sums.
+// sg: the elements' sign bytes in register order.  The caller multiplies by
+// 1/32 (exact).
 __device__ __forceinline__ void rotate16(float (&v)[16], const uint4 sg, int l) {
     const uint32_t sw[4] = {sg.x, sg.y, sg.z, sg.w};
 #pragma unroll

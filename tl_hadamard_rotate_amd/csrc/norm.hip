@@ -12,9 +12,14 @@
 // bits (24 by 24 bits), and the codes are decided there: a quotient of 16-bit
 // types (22 bits by 22) lies on a tie only if the true one does.
 //
-// One workgroup per row, in two passes over it: the sum of squares (h goes to
-// sum_out), then the values.  A lane handles the same elements in both, so the
-// second pass may read h back from sum_out, which may be x or the residual.
+// One workgroup per row.  A wave holds one or two 1024-blocks in registers,
+// lane l elements 8l .. 8l + 7 and 512 + 8l .. of each, so that every load is 1
+// KB of memory (the rotation's index bits are then 4 register and 6 lane bits):
+// each input is read once and each output written once, and the rotation runs
+// while the waves' sums of squares are on their way through LDS.  Rows past
+// kLongRow are gone through twice: the sum of squares (h goes to sum_out), then
+// the values; a lane handles the same elements in both passes, so the second
+// may read h back from sum_out, which may be x or the residual.
 #include <type_traits>
 
 #include "elem.h"
@@ -27,141 +32,275 @@ using namespace elem;
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
+constexpr int kLongRow = 24576;     // elements; 12 waves of two blocks: longer rows do not fit in registers
 constexpr int kMaxGrid = 1 << 20;   // workgroups of a launch; rows beyond it are looped over
 
 struct I8 {
     static constexpr int kType = TL_I8, kBytes = 1;
 };
 
-// largest |p| of the lanes' group, NaN above infinity above numbers
+// largest |p| of the 16 lanes that hold 128 values, NaN above infinity above
+// numbers
 template <typename P>
-__device__ __forceinline__ P group_max(P a, int lanes) {
-    for (int m = 1; m < lanes; m <<= 1) {
+__device__ __forceinline__ P group_max(P a) {
+    for (int m = 1; m < 16; m <<= 1) {
         const P o = __shfl_xor(a, m, 64);
         a = o > a || o != o ? o : a;
     }
     return a;
 }
 
-// E consecutive p of a lane (lanes l ^ 1 .. hold the rest of the group of 128)
-// to codes and the group's scale
-template <typename P, int E>
-__device__ __forceinline__ void store_i8(const P (&p)[E], float inv, int64_t i, int64_t row_groups0, int64_t k0,
-                                         bool on, int8_t* out, float* out_scales) {
+// 8 consecutive p of a lane (its row of 16 lanes holds the group of 128) to
+// codes at out and, by the group's first lane, its scale
+template <typename P>
+__device__ __forceinline__ void store_i8(const P (&p)[8], float inv, bool on, int l, int8_t* out, float* out_scale) {
     P a = 0;
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
+    for (int j = 0; j < 8; ++j) {
         const P b = p[j] < 0 ? -p[j] : p[j];
         a = b > a || b != b ? b : a;
     }
-    a = group_max(a, 128 / E);
+    a = group_max(a);
     if (!on) return;
-    const bool finite = a <= P(3.4028234663852886e38);
-    uint32_t w[E / 4] = {};
+    const float af = float(a);
+    const bool finite = af <= 3.4028234663852886e38f;
+    // in fp32 off a tie by less than 127 * 3 * 2^-24; nearer than 1e-4 to one
+    // (or where 127 / a is no number) the quotient is taken in 64 bits
+    const bool slow = !(af > 1e-30f);
+    const float r = 127.0f / af;
+    uint32_t w[2] = {};
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-        const int c = finite && a > 0 ? int(__builtin_rint(127.0 * double(p[j]) / double(a))) : 0;
+    for (int j = 0; j < 8; ++j) {
+        const float t = float(p[j]) * r;
+        float q = __builtin_rintf(t);
+        if (finite && (slow || __builtin_fabsf(__builtin_fabsf(t - q) - 0.5f) < 1e-4f))
+            q = a > 0 ? float(__builtin_rint(127.0 * double(p[j]) / double(a))) : 0.0f;
+        const int c = finite ? int(q) : 0;
         w[j >> 2] |= (uint32_t(c) & 0xFFu) << (8 * (j & 3));
     }
-    uint32_t* dst = reinterpret_cast<uint32_t*>(out + i);
+    *reinterpret_cast<uint2*>(out) = uint2{w[0], w[1]};
+    if ((l & 15) == 0) *out_scale = finite ? af * inv * (1.0f / 127.0f) : __builtin_nanf("");
+}
+
+// p of a lane's 8 consecutive elements written, `scale` the row's factor
+template <typename O, typename P>
+__device__ __forceinline__ void store_out(const P (&p)[8], float scale, bool on, int l, int64_t at, int64_t group,
+                                          void* out, float* out_scales) {
+    if constexpr (O::kType == TL_I8) {
+        store_i8<P>(p, scale, on, l, static_cast<int8_t*>(out) + at, out_scales + group);
+    } else if (on) {
+        float v[8];
 #pragma unroll
-    for (int j = 0; j < E / 4; ++j) dst[j] = w[j];
-    if (k0 % 128 == 0)
-        out_scales[row_groups0 + k0 / 128] =
-            finite ? float(a) * inv * (1.0f / 127.0f) : __builtin_nanf("");
+        for (int j = 0; j < 8; ++j) v[j] = float(p[j]) * scale;
+        store8<O>(out, at, v);
+    }
+}
+
+// sum over the wave, the same in every lane
+__device__ __forceinline__ float wave_sum(float v, int l) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) v += lane_xor(v, m, l);
+    return v;
+}
+
+template <typename O, bool ROT>
+using PType = typename std::conditional<O::kType == TL_I8 && !ROT, double, float>::type;
+
+// NB 1024-blocks a wave, as many waves as the row needs
+template <typename T, typename O, bool ROT, int NB>
+__global__ __launch_bounds__(NB == 1 ? 1024 : 768) void rms_norm_kernel(const void* x, const void* residual,
+                                                                         const void* gain, const int8_t* signs,
+                                                                         int64_t m, int64_t k, float eps,
+                                                                         void* sum_out, void* out,
+                                                                         float* out_scales) {
+    using P = PType<O, ROT>;
+    __shared__ float part[2][16];
+    const int l = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = int(blockDim.x >> 6);
+    const float inv_k = 1.0f / float(k);
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < m; row += gridDim.x, turn ^= 1) {
+        const int64_t base = row * k;
+        float h[NB][2][8], g[NB][2][8];
+        uint4 sg[NB];
+        float ss = 0.0f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int64_t i = 1024 * (wave + int64_t(b) * waves) + 512 * e + 8 * l;
+                if (i < k) load8<T>(x, base + i, h[b][e]);
+                else
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) h[b][e][j] = 0.0f;
+            }
+        if (residual) {
+            float r[NB][2][8];
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int64_t i = 1024 * (wave + int64_t(b) * waves) + 512 * e + 8 * l;
+                    if (i < k) load8<T>(residual, base + i, r[b][e]);
+                    else
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) r[b][e][j] = 0.0f;
+                }
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) h[b][e][j] = round_to<T>(h[b][e][j] + r[b][e][j]);
+                }
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int64_t i = 1024 * (wave + int64_t(b) * waves) + 512 * e + 8 * l;
+                if (i < k) load8<T>(gain, i, g[b][e]);
+                else
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) g[b][e][j] = 0.0f;
+                if (ROT) {
+                    const uint2 s = i < k ? *reinterpret_cast<const uint2*>(signs + i) : uint2{0, 0};
+                    if (e == 0) sg[b].x = s.x, sg[b].y = s.y;
+                    else sg[b].z = s.x, sg[b].w = s.y;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(h[b][e][j], h[b][e][j], ss);
+            }
+        ss = wave_sum(ss, l);
+        if (l == 0) part[turn][wave] = ss;
+        if (sum_out)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int64_t i = 1024 * (wave + int64_t(b) * waves) + 512 * e + 8 * l;
+                    if (i < k) store8<T>(sum_out, base + i, h[b][e]);
+                }
+        if constexpr (ROT)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                float v[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = h[b][j >> 3][j & 7] * g[b][j >> 3][j & 7];
+                rotate16(v, sg[b], l);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) h[b][j >> 3][j & 7] = v[j];
+            }
+        __syncthreads();   // (the other set of sums is written next)
+        ss = 0.0f;
+        for (int w = 0; w < waves; ++w) ss += part[turn][w];
+        float scale = 1.0f / sqrtf(ss * inv_k + eps);
+        if (ROT) scale *= 0.03125f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int64_t i = 1024 * (wave + int64_t(b) * waves) + 512 * e + 8 * l;
+                P p[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) p[j] = ROT ? P(h[b][e][j]) : P(h[b][e][j]) * P(g[b][e][j]);
+                store_out<O, P>(p, scale, i < k, l, base + i, (base + i) / 128, out, out_scales);
+            }
+    }
 }
 
 template <typename T, typename O, bool ROT>
-__global__ __launch_bounds__(kThreads) void rms_norm_kernel(const void* x, const void* residual,
-                                                            const void* gain, const int8_t* signs,
-                                                            int64_t m, int64_t k, float eps,
-                                                            void* sum_out, void* out,
-                                                            float* out_scales) {
-    constexpr int E = ROT ? 16 : 8;   // consecutive elements of a lane
+__global__ __launch_bounds__(kThreads) void rms_norm_long_kernel(const void* x, const void* residual,
+                                                                 const void* gain, const int8_t* signs,
+                                                                 int64_t m, int64_t k, float eps,
+                                                                 void* sum_out, void* out,
+                                                                 float* out_scales) {
+    using P = PType<O, ROT>;
     __shared__ float part[kWaves];
     const int l = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int64_t row = blockIdx.x; row < m; row += gridDim.x) {
         const int64_t base = row * k;
+        const auto element = [&](int64_t b, int e) { return 1024 * (b + wave) + 512 * e + 8 * l; };
+        const auto load_h = [&](int64_t i, const void* from, bool add, float (&v)[8]) {
+            load8<T>(from, base + i, v);
+            if (add) {
+                float r[8];
+                load8<T>(residual, base + i, r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = round_to<T>(v[j] + r[j]);
+            }
+        };
         float ss = 0.0f;
-        for (int64_t i = int64_t(threadIdx.x) * E; i < k; i += kThreads * E)
+        for (int64_t b = 0; 1024 * b < k; b += kWaves)
 #pragma unroll
-            for (int e = 0; e < E; e += 8) {
+            for (int e = 0; e < 2; ++e) {
+                const int64_t i = element(b, e);
+                if (i >= k) continue;
                 float v[8];
-                load8<T>(x, base + i + e, v);
-                if (residual) {
-                    float r[8];
-                    load8<T>(residual, base + i + e, r);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = round_to<T>(v[j] + r[j]);
-                    if (sum_out) store8<T>(sum_out, base + i + e, v);
-                }
+                load_h(i, x, residual != nullptr, v);
+                if (sum_out) store8<T>(sum_out, base + i, v);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(v[j], v[j], ss);
             }
-        for (int s = 1; s < 64; s <<= 1) ss += __shfl_xor(ss, s, 64);
+        ss = wave_sum(ss, l);
         if (l == 0) part[wave] = ss;
         __syncthreads();
         ss = (part[0] + part[1]) + (part[2] + part[3]);
         __syncthreads();
-        const float inv = 1.0f / sqrtf(ss / float(k) + eps);
-
+        float scale = 1.0f / sqrtf(ss / float(k) + eps);
+        if (ROT) scale *= 0.03125f;
         // whole waves take part in the exchanges, whether their elements exist or not
-        const int64_t steps = (k + kThreads * E - 1) / (kThreads * E);
-        for (int64_t st = 0; st < steps; ++st) {
-            const int64_t i = (st * kThreads + threadIdx.x) * E;
-            const bool on = i < k;
-            using P = typename std::conditional<O::kType == TL_I8 && !ROT, double, float>::type;
-            P p[E];
+        for (int64_t b = 0; 1024 * b < k; b += kWaves) {
+            float h[2][8] = {}, g[2][8] = {};
+            uint2 sg[2] = {};
 #pragma unroll
-            for (int j = 0; j < E; ++j) p[j] = 0;
-            if (on)
-#pragma unroll
-                for (int e = 0; e < E; e += 8) {
-                    float v[8], g[8];
-                    load8<T>(sum_out ? sum_out : x, base + i + e, v);
-                    if (residual && !sum_out) {
-                        float r[8];
-                        load8<T>(residual, base + i + e, r);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) v[j] = round_to<T>(v[j] + r[j]);
-                    }
-                    load8<T>(gain, i + e, g);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) p[e + j] = P(v[j]) * P(g[j]);
-                }
-            float scale = inv;
-            if constexpr (ROT) {
-                uint4 sg = uint4{0, 0, 0, 0};
-                if (on) sg = *reinterpret_cast<const uint4*>(signs + i);
-                rotate16(p, sg, l);
-                scale *= 0.03125f;
+            for (int e = 0; e < 2; ++e) {
+                const int64_t i = element(b, e);
+                if (i >= k) continue;
+                load_h(i, sum_out ? sum_out : x, residual && !sum_out, h[e]);
+                load8<T>(gain, i, g[e]);
+                if (ROT) sg[e] = *reinterpret_cast<const uint2*>(signs + i);
             }
-            if constexpr (O::kType == TL_I8) {
-                store_i8<P, E>(p, scale, base + i, row * (k / 128), i, on, static_cast<int8_t*>(out),
-                               out_scales);
-            } else if (on) {
+            if constexpr (ROT) {
+                float v[16];
 #pragma unroll
-                for (int e = 0; e < E; e += 8) {
-                    float v[8];
+                for (int j = 0; j < 16; ++j) v[j] = h[j >> 3][j & 7] * g[j >> 3][j & 7];
+                rotate16(v, uint4{sg[0].x, sg[0].y, sg[1].x, sg[1].y}, l);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = float(p[e + j]) * scale;
-                    store8<O>(out, base + i + e, v);
-                }
+                for (int j = 0; j < 16; ++j) h[j >> 3][j & 7] = v[j];
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int64_t i = element(b, e);
+                P p[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) p[j] = ROT ? P(h[e][j]) : P(h[e][j]) * P(g[e][j]);
+                store_out<O, P>(p, scale, i < k, l, base + i, (base + i) / 128, out, out_scales);
             }
         }
     }
 }
 
+template <typename T, typename O, bool ROT>
+void launch_row(const void* x, const void* residual, const void* gain, const int8_t* signs, int64_t m,
+                int64_t k, float eps, void* sum_out, void* out, float* out_scales, hipStream_t stream) {
+    const dim3 grid(unsigned(m < kMaxGrid ? m : kMaxGrid));
+    const int blocks = int((k + 1023) / 1024);
+    if (blocks <= 16)
+        hipLaunchKernelGGL((rms_norm_kernel<T, O, ROT, 1>), grid, dim3(64 * blocks), 0, stream, x, residual, gain,
+                           signs, m, k, eps, sum_out, out, out_scales);
+    else if (k <= kLongRow)
+        hipLaunchKernelGGL((rms_norm_kernel<T, O, ROT, 2>), grid, dim3(64 * ((blocks + 1) / 2)), 0, stream, x,
+                           residual, gain, signs, m, k, eps, sum_out, out, out_scales);
+    else
+        hipLaunchKernelGGL((rms_norm_long_kernel<T, O, ROT>), grid, dim3(kThreads), 0, stream, x, residual, gain,
+                           signs, m, k, eps, sum_out, out, out_scales);
+}
+
 template <typename T, typename O>
 void launch(const void* x, const void* residual, const void* gain, const int8_t* signs, int64_t m,
             int64_t k, float eps, void* sum_out, void* out, float* out_scales, hipStream_t stream) {
-    const dim3 grid(unsigned(m < kMaxGrid ? m : kMaxGrid));
-    if (signs)
-        hipLaunchKernelGGL((rms_norm_kernel<T, O, true>), grid, dim3(kThreads), 0, stream, x, residual,
-                           gain, signs, m, k, eps, sum_out, out, out_scales);
-    else
-        hipLaunchKernelGGL((rms_norm_kernel<T, O, false>), grid, dim3(kThreads), 0, stream, x, residual,
-                           gain, signs, m, k, eps, sum_out, out, out_scales);
+    if (signs) launch_row<T, O, true>(x, residual, gain, signs, m, k, eps, sum_out, out, out_scales, stream);
+    else launch_row<T, O, false>(x, residual, gain, signs, m, k, eps, sum_out, out, out_scales, stream);
 }
 
 template <typename T>

@@ -524,6 +524,7 @@ __global__ __launch_bounds__(256) void q4_join_kernel(const float* __restrict__ 
 }
 
 constexpr int64_t kLdsCu = 160 * 1024;
+constexpr int64_t kOnePart = 16384;   // M * K that is never cut into parts: its activations fit in LDS
 constexpr int kScaleLds = 2560;       // scales of a wave: K = 5120 of 32 rows in groups of 128
 
 // How a call is split; the same for the workspace and the launch.
@@ -570,6 +571,7 @@ Plan q4_plan(int64_t m, int64_t n, int64_t k) {
     for (p.ks = kWaves; p.ks >= 1; p.ks /= 2) {
         int tried = 0;
         for (p.parts = 1; p.parts <= chunks && tried < 5; ++p.parts) {
+            if (p.parts > 1 && m * k <= kOnePart) break;
             p.l = int((chunks + p.parts - 1) / p.parts);
             size_lds<XT, G>(p, tokens);
             if (p.lds > room || (chunks + p.l - 1) / p.l != p.parts) continue;
@@ -633,20 +635,24 @@ hipError_t launch_rows(const Args& a, int64_t m, hipStream_t stream) {
 
 }  // namespace
 
+int64_t q4_gemv_need(int64_t m, int64_t n, int64_t k, int x_dtype, int group) {
+    if (m * k <= kOnePart) return 0;
+    const auto bytes = [&](const Plan& p) { return p.parts > 1 ? p.parts * m * n * 4 : int64_t(0); };
+#define TL_Q4_NEED(XT)                                      \
+    bytes(group == 32   ? q4_plan<XT, 32>(m, n, k)          \
+          : group == 64 ? q4_plan<XT, 64>(m, n, k)          \
+                        : q4_plan<XT, 128>(m, n, k))
+    return x_dtype == TL_I8 ? TL_Q4_NEED(TL_I8) : x_dtype == TL_F16 ? TL_Q4_NEED(TL_F16) : TL_Q4_NEED(TL_BF16);
+}
+
 int64_t q4_gemv_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-    // the most parts any type of activations and group size takes
-    int64_t parts = 1;
-    const auto most = [&](const Plan& p) { parts = p.parts > parts ? p.parts : parts; };
-    most(q4_plan<TL_F16, 32>(m, n, k));
-    most(q4_plan<TL_F16, 64>(m, n, k));
-    most(q4_plan<TL_F16, 128>(m, n, k));
-    most(q4_plan<TL_BF16, 32>(m, n, k));
-    most(q4_plan<TL_BF16, 64>(m, n, k));
-    most(q4_plan<TL_BF16, 128>(m, n, k));
-    most(q4_plan<TL_I8, 32>(m, n, k));
-    most(q4_plan<TL_I8, 64>(m, n, k));
-    most(q4_plan<TL_I8, 128>(m, n, k));
-    return parts > 1 ? parts * m * n * 4 : 0;
+    int64_t most = 0;
+    for (const int x_dtype : {TL_F16, TL_BF16, TL_I8})
+        for (const int group : {32, 64, 128}) {
+            const int64_t b = q4_gemv_need(m, n, k, x_dtype, group);
+            most = b > most ? b : most;
+        }
+    return most;
 }
 
 hipError_t launch_q4_gemv(const uint8_t* packed, const uint16_t* scales, int group, const void* x,

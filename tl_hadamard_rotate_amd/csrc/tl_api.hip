@@ -438,7 +438,7 @@ tl_status tl_q4_gemv(const uint8_t* packed, const uint16_t* scales, int32_t grou
         (x_scales && overlap(y, yb, x_scales, xsb)))
         return TL_ERR_ALIAS;
     const tl_status st =
-        check_workspace(tl::q4_gemv_workspace_bytes(M, N, K), workspace, workspace_bytes,
+        check_workspace(tl::q4_gemv_need(M, N, K, x_dtype, group), workspace, workspace_bytes,
                         {{packed, pb}, {scales, sb}, {x, xb}, {x_scales, xsb}, {y, yb}});
     if (st != TL_OK) return st;
     return launched(tl::launch_q4_gemv(packed, scales, group, x, x_dtype, x_scales, M, N, K, y,

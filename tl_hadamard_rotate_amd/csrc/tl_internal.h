@@ -143,7 +143,9 @@ hipError_t launch_q4_quantize(const void* w, const int8_t* signs, int64_t n, int
                               int group, uint8_t* packed, uint16_t* scales, hipStream_t stream);
 hipError_t launch_q4_dequantize(const uint8_t* packed, const uint16_t* scales, int64_t n, int64_t k,
                                 int group, void* w, int w_dtype, hipStream_t stream);
+// workspace bytes of a product: for every type and group size, and for one
 int64_t q4_gemv_workspace_bytes(int64_t m, int64_t n, int64_t k);
+int64_t q4_gemv_need(int64_t m, int64_t n, int64_t k, int x_dtype, int group);
 hipError_t launch_q4_gemv(const uint8_t* packed, const uint16_t* scales, int group, const void* x,
                           int x_dtype, const float* x_scales, int64_t m, int64_t n, int64_t k, void* y,
                           int y_dtype, void* ws, hipStream_t stream);
