@@ -320,30 +320,38 @@ def linear(packed, scales, fmt, x, signs, out_dtype=torch.float32, out=None,
 
 
 _REAL = {torch.float32: TL_F32, torch.float16: TL_F16, torch.bfloat16: TL_BF16}
+_I8, _U8, _F16, _F32 = torch.int8, torch.uint8, torch.float16, torch.float32
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_get_device = torch._C._cuda_getDevice
+
+# The calls below take microseconds, so their checks are written out: each
+# tensor's type, shape, device and contiguity in one condition, and only a
+# tensor that fails it goes to the function that says why.
 
 
-def _need_like(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device) -> None:
-    """A contiguous device tensor of this type and shape, on this device."""
+def _refuse(t, name: str, dtype: torch.dtype, shape, index: int) -> None:
+    """Raise for a tensor that is not a contiguous one of this type and shape
+    on this device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    raise ValueError(f"{name} must be contiguous {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _need_real(t: torch.Tensor, name: str) -> int:
-    """The TL_ type of a contiguous 2-D device tensor of real numbers."""
+def _rows(t, name: str):
+    """(TL_ type, shape, device index) of a contiguous 2-D device tensor of real numbers."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     dt = _REAL.get(t.dtype)
     if dt is None:
         raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
-    if not t.is_cuda or t.dim() != 2 or not t.is_contiguous():
+    shape, index = t.shape, t.get_device()
+    if index < 0 or len(shape) != 2 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous 2-D device tensor")
-    return dt
+    return dt, shape, index
 
 
 def _out_type(dtype: torch.dtype) -> int:
@@ -353,42 +361,48 @@ def _out_type(dtype: torch.dtype) -> int:
     return dt
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _call(name: str, device: torch.device, *args) -> None:
+def _call(name: str, index: int, args: tuple) -> None:
     """One library call on the device's current stream, with that device
     current (a stream and the look-ups of a launch belong to a device)."""
     fn = getattr(_lib or lib(), name)
-    index = device.index
-    if index == torch.cuda.current_device():
+    if index == _get_device():
         st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
             st = fn(*args, _raw_stream(index))
-    if st != 0:
+    if st:
         _check(name, st)
 
 
-def _rms_norm(x, dt, gain, eps, residual, signs, sum_out, out, out_dtype, out_scales):
-    device, dtype, shape = x.device, x.dtype, x.shape
+def _rms_norm(x, dt, shape, index, gain, eps, residual, signs, sum_out, out, out_dtype, out_scales):
+    dtype = x.dtype
     m, k = shape
-    _need_like(gain, "gain", dtype, (k,), device)
+    row = (k,)
+    if not (isinstance(gain, torch.Tensor) and gain.dtype is dtype and gain.shape == row and
+            gain.get_device() == index and gain.is_contiguous()):
+        _refuse(gain, "gain", dtype, row, index)
     rp = sp = gp = None
     if residual is not None:
-        _need_like(residual, "residual", dtype, shape, device)
+        if not (isinstance(residual, torch.Tensor) and residual.dtype is dtype and
+                residual.shape == shape and residual.get_device() == index and
+                residual.is_contiguous()):
+            _refuse(residual, "residual", dtype, shape, index)
         if sum_out is None:
             sum_out = torch.empty_like(x)
-        else:
-            _need_like(sum_out, "sum_out", dtype, shape, device)
+        elif not (isinstance(sum_out, torch.Tensor) and sum_out.dtype is dtype and
+                  sum_out.shape == shape and sum_out.get_device() == index and
+                  sum_out.is_contiguous()):
+            _refuse(sum_out, "sum_out", dtype, shape, index)
         rp, sp = residual.data_ptr(), sum_out.data_ptr()
     elif sum_out is not None:
         raise ValueError("sum_out needs a residual")
     if signs is not None:
-        _need_like(signs, "signs", torch.int8, (k,), device)
+        if not (isinstance(signs, torch.Tensor) and signs.dtype is _I8 and signs.shape == row and
+                signs.get_device() == index and signs.is_contiguous()):
+            _refuse(signs, "signs", _I8, row, index)
         gp = signs.data_ptr()
-    _call("tl_rms_norm", device, x.data_ptr(), rp, gain.data_ptr(), gp, m, k, dt, eps, sp,
-          out.data_ptr(), out_dtype, None if out_scales is None else out_scales.data_ptr())
+    _call("tl_rms_norm", index, (x.data_ptr(), rp, gain.data_ptr(), gp, m, k, dt, eps, sp,
+                                 out.data_ptr(), out_dtype, out_scales))
     return sum_out
 
 
@@ -400,12 +414,13 @@ def rms_norm(x, gain, eps, residual=None, signs=None, out_dtype=torch.float16, s
     x_rot (see tl_rms_norm).  Returns out, or (out, sum) with a residual; the
     sum x + residual goes to ``sum_out``, which may be x or residual itself."""
     yd = _out_type(out_dtype)
-    dt = _need_real(x, "x")
+    dt, shape, index = _rows(x, "x")
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
-    else:
-        _need_like(out, "out", out_dtype, x.shape, x.device)
-    s = _rms_norm(x, dt, gain, eps, residual, signs, sum_out, out, yd, None)
+        out = torch.empty(shape, dtype=out_dtype, device=x.device)
+    elif not (isinstance(out, torch.Tensor) and out.dtype is out_dtype and out.shape == shape and
+              out.get_device() == index and out.is_contiguous()):
+        _refuse(out, "out", out_dtype, shape, index)
+    s = _rms_norm(x, dt, shape, index, gain, eps, residual, signs, sum_out, out, yd, None)
     return out if s is None else (out, s)
 
 
@@ -413,19 +428,23 @@ def rms_norm_i8(x, gain, eps, residual=None, signs=None, sum_out=None, out=None,
     """``rms_norm`` with 8-bit outputs for ``q4_gemv``: returns (codes int8
     [M, K], scales float32 [M, K/128]), and the sum behind them with a
     residual; value = code * scale of its 128."""
-    dt = _need_real(x, "x")
-    m, k = x.shape
+    dt, shape, index = _rows(x, "x")
+    m, k = shape
     if k % GROUP:
         raise ValueError("K must be a multiple of 128")
+    groups = (m, k // GROUP)
     if out is None:
-        out = torch.empty((m, k), dtype=torch.int8, device=x.device)
-    else:
-        _need_like(out, "out", torch.int8, (m, k), x.device)
+        out = torch.empty(shape, dtype=_I8, device=x.device)
+    elif not (isinstance(out, torch.Tensor) and out.dtype is _I8 and out.shape == shape and
+              out.get_device() == index and out.is_contiguous()):
+        _refuse(out, "out", _I8, shape, index)
     if scales is None:
-        scales = torch.empty((m, k // GROUP), dtype=torch.float32, device=x.device)
-    else:
-        _need_like(scales, "scales", torch.float32, (m, k // GROUP), x.device)
-    s = _rms_norm(x, dt, gain, eps, residual, signs, sum_out, out, TL_I8, scales)
+        scales = torch.empty(groups, dtype=_F32, device=x.device)
+    elif not (isinstance(scales, torch.Tensor) and scales.dtype is _F32 and
+              scales.shape == groups and scales.get_device() == index and scales.is_contiguous()):
+        _refuse(scales, "scales", _F32, groups, index)
+    s = _rms_norm(x, dt, shape, index, gain, eps, residual, signs, sum_out, out, TL_I8,
+                  scales.data_ptr())
     return (out, scales) if s is None else (out, scales, s)
 
 
@@ -438,55 +457,64 @@ def q4_quantize(w, group=GROUP, signs=None, packed=None, scales=None):
     (32, 64 or 128) weights, after the signed rotation of the rows when
     ``signs`` is given: returns (packed uint8 [N, K/2], scales float16
     [N, K/group]); the layout is in include/tl.h."""
-    dt = _need_real(w, "w")
-    n, k = w.shape
+    dt, (n, k), index = _rows(w, "w")
     if group not in (32, 64, 128) or k % GROUP:
         raise ValueError("group must be 32, 64 or 128 and K a multiple of 128")
+    gp = None
     if signs is not None:
-        _need_like(signs, "signs", torch.int8, (k,), w.device)
+        if not (isinstance(signs, torch.Tensor) and signs.dtype is _I8 and signs.shape == (k,) and
+                signs.get_device() == index and signs.is_contiguous()):
+            _refuse(signs, "signs", _I8, (k,), index)
+        gp = signs.data_ptr()
+    halves, groups = (n, k // 2), (n, k // group)
     if packed is None:
-        packed = torch.empty((n, k // 2), dtype=torch.uint8, device=w.device)
-    else:
-        _need_like(packed, "packed", torch.uint8, (n, k // 2), w.device)
+        packed = torch.empty(halves, dtype=_U8, device=w.device)
+    elif not (isinstance(packed, torch.Tensor) and packed.dtype is _U8 and
+              packed.shape == halves and packed.get_device() == index and packed.is_contiguous()):
+        _refuse(packed, "packed", _U8, halves, index)
     if scales is None:
-        scales = torch.empty((n, k // group), dtype=torch.float16, device=w.device)
-    else:
-        _need_like(scales, "scales", torch.float16, (n, k // group), w.device)
-    _call("tl_q4_quantize", w.device, w.data_ptr(), None if signs is None else signs.data_ptr(), n, k,
-          dt, group, packed.data_ptr(), scales.data_ptr())
+        scales = torch.empty(groups, dtype=_F16, device=w.device)
+    elif not (isinstance(scales, torch.Tensor) and scales.dtype is _F16 and
+              scales.shape == groups and scales.get_device() == index and scales.is_contiguous()):
+        _refuse(scales, "scales", _F16, groups, index)
+    _call("tl_q4_quantize", index, (w.data_ptr(), gp, n, k, dt, group, packed.data_ptr(),
+                                    scales.data_ptr()))
     return packed, scales
 
 
 def _q4_shape(packed, scales):
-    """(N, K, group) of packed 4-bit weights and their scales."""
-    if not isinstance(packed, torch.Tensor) or not isinstance(scales, torch.Tensor):
+    """(N, K, group, device index) of packed 4-bit weights and their scales."""
+    if not (isinstance(packed, torch.Tensor) and isinstance(scales, torch.Tensor)):
         raise TypeError("packed and scales must be torch.Tensors")
-    if packed.dtype != torch.uint8 or scales.dtype != torch.float16:
+    if packed.dtype is not _U8 or scales.dtype is not _F16:
         raise TypeError("packed must be uint8 and scales float16")
-    if not packed.is_cuda or scales.device != packed.device:
+    index = packed.get_device()
+    if index < 0 or scales.get_device() != index:
         raise ValueError("packed and scales must be device tensors, on the same device")
-    if packed.dim() != 2 or scales.dim() != 2 or not packed.is_contiguous() or \
-            not scales.is_contiguous():
+    ps, ss = packed.shape, scales.shape
+    if len(ps) != 2 or len(ss) != 2 or not packed.is_contiguous() or not scales.is_contiguous():
         raise ValueError("packed and scales must be contiguous with 2 dims")
-    n, half = packed.shape
-    groups = scales.shape[1]
+    n, half = ps
+    groups = ss[1]
     k = 2 * half
-    if scales.shape[0] != n or k % GROUP or not groups or k // groups not in (32, 64, 128) or k % groups:
-        raise ValueError(f"packed {tuple(packed.shape)} and scales {tuple(scales.shape)} must be "
+    group = k // groups if groups else 0
+    if ss[0] != n or k % GROUP or group not in (32, 64, 128) or group * groups != k:
+        raise ValueError(f"packed {tuple(ps)} and scales {tuple(ss)} must be "
                          "[N, K/2] and [N, K/group], group 32, 64 or 128, K a multiple of 128")
-    return n, k, k // groups
+    return n, k, group, index
 
 
 def q4_dequantize(packed, scales, out_dtype=torch.float16, out=None) -> torch.Tensor:
     """The weights [N, K] that 4-bit codes and scales stand for."""
-    n, k, group = _q4_shape(packed, scales)
+    n, k, group, index = _q4_shape(packed, scales)
     dt = _out_type(out_dtype)
     if out is None:
         out = torch.empty((n, k), dtype=out_dtype, device=packed.device)
-    else:
-        _need_like(out, "out", out_dtype, (n, k), packed.device)
-    _call("tl_q4_dequantize", packed.device, packed.data_ptr(), scales.data_ptr(), n, k, group,
-          out.data_ptr(), dt)
+    elif not (isinstance(out, torch.Tensor) and out.dtype is out_dtype and out.shape == (n, k) and
+              out.get_device() == index and out.is_contiguous()):
+        _refuse(out, "out", out_dtype, (n, k), index)
+    _call("tl_q4_dequantize", index, (packed.data_ptr(), scales.data_ptr(), n, k, group,
+                                      out.data_ptr(), dt))
     return out
 
 
@@ -499,9 +527,9 @@ def q4_gemv_workspace_bytes(m: int, n: int, k: int) -> int:
 
 
 @functools.lru_cache(maxsize=4096)
-def _q4_workspace(device: torch.device, m: int, n: int, k: int) -> int:
+def _q4_workspace(index: int, m: int, n: int, k: int) -> int:
     """q4_gemv_workspace_bytes of a shape, asked once a device."""
-    with torch.cuda.device(device):
+    with torch.cuda.device(index):
         return q4_gemv_workspace_bytes(m, n, k)
 
 
@@ -511,18 +539,24 @@ def q4_gemv(packed, scales, x, x_scales=None, out_dtype=torch.float32, out=None,
     [M, K] float16 or bfloat16, or int8 with ``x_scales`` float32 [M, K/128]
     (``rms_norm_i8``).  ``workspace`` (uint8, at least
     ``q4_gemv_workspace_bytes``) is taken from torch's allocator when not given."""
-    n, k, group = _q4_shape(packed, scales)
+    n, k, group, index = _q4_shape(packed, scales)
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
-    device = packed.device
-    if x.device != device or x.dim() != 2 or x.shape[1] != k or not x.is_contiguous():
-        raise ValueError(f"x must be a contiguous [M, {k}] tensor on {device}")
-    m = x.shape[0]
-    if x.dtype == torch.int8:
+    xs = x.shape
+    if len(xs) != 2 or xs[1] != k or x.get_device() != index or not x.is_contiguous():
+        raise ValueError(f"x must be a contiguous [M, {k}] tensor on {packed.device}")
+    m = xs[0]
+    sp = None
+    if x.dtype is _I8:
         xd = TL_I8
         if x_scales is None:
             raise ValueError("int8 activations need x_scales")
-        _need_like(x_scales, "x_scales", torch.float32, (m, k // GROUP), device)
+        groups = (m, k // GROUP)
+        if not (isinstance(x_scales, torch.Tensor) and x_scales.dtype is _F32 and
+                x_scales.shape == groups and x_scales.get_device() == index and
+                x_scales.is_contiguous()):
+            _refuse(x_scales, "x_scales", _F32, groups, index)
+        sp = x_scales.data_ptr()
     else:
         xd = _REAL.get(x.dtype)
         if xd is None or xd == TL_F32:
@@ -531,19 +565,24 @@ def q4_gemv(packed, scales, x, x_scales=None, out_dtype=torch.float32, out=None,
             raise ValueError("x_scales go with int8 activations")
     yd = _out_type(out_dtype)
     if out is None:
-        out = torch.empty((m, n), dtype=out_dtype, device=device)
-    else:
-        _need_like(out, "out", out_dtype, (m, n), device)
-    wb = 0
+        out = torch.empty((m, n), dtype=out_dtype, device=packed.device)
+    elif not (isinstance(out, torch.Tensor) and out.dtype is out_dtype and out.shape == (m, n) and
+              out.get_device() == index and out.is_contiguous()):
+        _refuse(out, "out", out_dtype, (m, n), index)
+    wp, wb = None, 0
     if workspace is not None:
-        wb = workspace.numel()
-        _need_like(workspace, "workspace", torch.uint8, (wb,), device)
+        if not (isinstance(workspace, torch.Tensor) and workspace.dtype is _U8 and
+                workspace.dim() == 1 and workspace.get_device() == index and
+                workspace.is_contiguous()):
+            _refuse(workspace, "workspace", _U8, ("bytes",), index)
+        wp, wb = workspace.data_ptr(), workspace.numel()
     elif m * k > 16384:
-        wb = _q4_workspace(device, m, n, k)
-        workspace = torch.empty(wb, dtype=torch.uint8, device=device) if wb else None
-    _call("tl_q4_gemv", device, packed.data_ptr(), scales.data_ptr(), group, x.data_ptr(), xd,
-          None if x_scales is None else x_scales.data_ptr(), m, n, k, out.data_ptr(), yd,
-          None if workspace is None else workspace.data_ptr(), wb)
+        wb = _q4_workspace(index, m, n, k)
+        if wb:
+            workspace = torch.empty(wb, dtype=_U8, device=packed.device)
+            wp = workspace.data_ptr()
+    _call("tl_q4_gemv", index, (packed.data_ptr(), scales.data_ptr(), group, x.data_ptr(), xd, sp, m,
+                                n, k, out.data_ptr(), yd, wp, wb))
     return out
 
 
