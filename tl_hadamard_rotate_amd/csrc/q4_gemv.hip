@@ -277,7 +277,7 @@ struct Args {
     const uint8_t* x;
     const float* xs;
     void* y;
-    float* sums;     // parts > 1: fp32 [part][m][n]
+    float* sums;     // parts > 1: fp32 [part][m][n], parts sums_stride(m * n) apart
     int64_t n, k;
     int m, y_dtype;
     // parts of L chunks; KS waves share a tile, LW = ceil(L / KS) chunks each;
@@ -285,6 +285,9 @@ struct Args {
     // scales a wave has in LDS at a time, and their bytes
     int parts, l, ks, lw, tiles, groups, seg, s_bytes;
 };
+
+// floats from one part's sums to the next's, which start on 16 bytes
+__host__ __device__ constexpr int64_t sums_stride(int64_t count) { return (count + 3) / 4 * 4; }
 
 __device__ __forceinline__ void store_y(void* y, int64_t at, float v, int y_dtype) {
     if (y_dtype == TL_F32) static_cast<float*>(y)[at] = v;
@@ -406,13 +409,15 @@ __global__ __launch_bounds__(64 * kWaves, MT == 1 ? 4 : 2) void q4_gemv_kernel(c
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if constexpr (XT == TL_BF16) {
-        const int count = tokens * len * kPieces;   // whole rows of 16 lanes: a chunk
-        for (int i = tid; i < count; i += threads) {
-            uint4v v = *reinterpret_cast<const uint4v*>(lx + 16 * i);
+        const int count = tokens * len;   // (token, chunk), a row of 16 lanes each
+        const float inv = 1.0f / float(len);
+        for (int i = tid >> 4; i < count; i += threads >> 4) {
+            uint4v* const at = reinterpret_cast<uint4v*>(lx) + 16 * i + c;
+            uint4v v = *at;
             const float f = convert_bf16(v);
-            *reinterpret_cast<uint4v*>(lx + 16 * i) = v;
-            const int t = i / (len * kPieces), e = i - t * (len * kPieces);
-            if (e % kPieces == 0) lf[e / kPieces * ts + t] = f;
+            *at = v;
+            const int t = int((float(i) + 0.5f) * inv);   // exact: i < 2^16
+            if (c == 0) lf[(i - t * len) * ts + t] = f;
         }
         __syncthreads();
     }
@@ -480,7 +485,7 @@ __global__ __launch_bounds__(64 * kWaves, MT == 1 ? 4 : 2) void q4_gemv_kernel(c
                     const int row = 16 * r + c, tok = 16 * t + 4 * q + i;
                     if (row >= rows || tok >= tokens) continue;
                     const int64_t at = (m0 + tok) * p.n + n0 + row;
-                    if (p.parts > 1) p.sums[int64_t(part) * p.m * p.n + at] = acc[r][t][i];
+                    if (p.parts > 1) p.sums[part * sums_stride(int64_t(p.m) * p.n) + at] = acc[r][t][i];
                     else store_y(p.y, at, acc[r][t][i], p.y_dtype);
                 }
         if (more) {
@@ -506,7 +511,7 @@ __global__ __launch_bounds__(64 * kWaves, MT == 1 ? 4 : 2) void q4_gemv_kernel(c
             float v = 0.0f;
             for (int w = 0; w < p.ks; ++w) v += src[w * (MT * R * 256)];
             const int64_t at = (m0 + tok) * p.n + n0 + row;
-            if (p.parts > 1) p.sums[int64_t(part) * p.m * p.n + at] = v;
+            if (p.parts > 1) p.sums[part * sums_stride(int64_t(p.m) * p.n) + at] = v;
             else store_y(p.y, at, v, p.y_dtype);
         }
     }
@@ -515,11 +520,21 @@ __global__ __launch_bounds__(64 * kWaves, MT == 1 ? 4 : 2) void q4_gemv_kernel(c
 // y = the parts' sums added in order
 __global__ __launch_bounds__(256) void q4_join_kernel(const float* __restrict__ sums, int parts, int64_t count,
                                                       void* __restrict__ y, int y_dtype) {
-    const int64_t step = int64_t(gridDim.x) * 256;
-    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < count; i += step) {
-        float v = sums[i];
-        for (int s = 1; s < parts; ++s) v += sums[s * count + i];
-        store_y(y, i, v, y_dtype);
+    const int64_t stride = sums_stride(count);
+    for (int64_t i = 4 * (int64_t(blockIdx.x) * 256 + threadIdx.x); i < count; i += int64_t(gridDim.x) * 1024) {
+        float4v v = *reinterpret_cast<const float4v*>(sums + i);
+#pragma unroll 4
+        for (int s = 1; s < parts; ++s) v += *reinterpret_cast<const float4v*>(sums + s * stride + i);
+        if (i + 4 > count) {
+            for (int j = 0; j < count - i; ++j) store_y(y, i + j, v[j], y_dtype);
+        } else if (y_dtype == TL_F32) {
+            *reinterpret_cast<float4v*>(static_cast<float*>(y) + i) = v;
+        } else {
+            uint32_t h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = y_dtype == TL_F16 ? f16_bits(v[j]) : bf16_bits(v[j]);
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + i) = uint2{h[0] | h[1] << 16, h[2] | h[3] << 16};
+        }
     }
 }
 
@@ -614,7 +629,7 @@ hipError_t launch(Args a, const Plan& p, hipStream_t stream) {
     const dim3 grid(unsigned(a.groups * a.parts), unsigned((a.m + 16 * MT - 1) / (16 * MT)));
     hipLaunchKernelGGL(kernel, grid, dim3(64 * kWaves), unsigned(p.lds), stream, a);
     if (p.parts > 1) {
-        const int64_t count = int64_t(a.m) * a.n, g = (count + 255) / 256;
+        const int64_t count = int64_t(a.m) * a.n, g = (count + 1023) / 1024;
         hipLaunchKernelGGL(q4_join_kernel, dim3(unsigned(g < 8192 ? g : 8192)), dim3(256), 0, stream, a.sums, a.parts,
                            count, a.y, a.y_dtype);
     }
@@ -637,7 +652,7 @@ hipError_t launch_rows(const Args& a, int64_t m, hipStream_t stream) {
 
 int64_t q4_gemv_need(int64_t m, int64_t n, int64_t k, int x_dtype, int group) {
     if (m * k <= kOnePart) return 0;
-    const auto bytes = [&](const Plan& p) { return p.parts > 1 ? p.parts * m * n * 4 : int64_t(0); };
+    const auto bytes = [&](const Plan& p) { return p.parts > 1 ? p.parts * sums_stride(m * n) * 4 : int64_t(0); };
 #define TL_Q4_NEED(XT)                                      \
     bytes(group == 32   ? q4_plan<XT, 32>(m, n, k)          \
           : group == 64 ? q4_plan<XT, 64>(m, n, k)          \
