@@ -58,19 +58,33 @@ __device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
     }
 }
 
-template <typename T>
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// KEEP: the value is read again soon, by the same kernel.  What a kernel only
+// writes is stored past the caches' replacement order, so that it does not push
+// out what is still to be read
+template <bool KEEP, typename V>
+__device__ __forceinline__ void put(V* p, V v) {
+    if (KEEP) *p = v;
+    else __builtin_nontemporal_store(v, p);
+}
+
+template <typename T, bool KEEP = false>
 __device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) {
+    uint32_t w[8];
     if (T::kType == TL_F32) {
-        float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-        q[0] = float4{v[0], v[1], v[2], v[3]};
-        q[1] = float4{v[4], v[5], v[6], v[7]};
+        u32x4* q = reinterpret_cast<u32x4*>(static_cast<float*>(p) + i);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = __builtin_bit_cast(uint32_t, v[j]);
+        put<KEEP>(q, u32x4{w[0], w[1], w[2], w[3]});
+        put<KEEP>(q + 1, u32x4{w[4], w[5], w[6], w[7]});
     } else {
-        uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             w[j] = T::kType == TL_F16 ? f16_bits(v[2 * j]) | f16_bits(v[2 * j + 1]) << 16
                                       : bf16_bits(v[2 * j]) | bf16_bits(v[2 * j + 1]) << 16;
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = uint4{w[0], w[1], w[2], w[3]};
+        put<KEEP>(reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i), u32x4{w[0], w[1], w[2], w[3]});
     }
 }
 

@@ -20,8 +20,6 @@
 // kLongRow are gone through twice: the sum of squares (h goes to sum_out), then
 // the values; a lane handles the same elements in both passes, so the second
 // may read h back from sum_out, which may be x or the residual.
-#include <type_traits>
-
 #include "elem.h"
 #include "tl_internal.h"
 
@@ -39,59 +37,85 @@ struct I8 {
     static constexpr int kType = TL_I8, kBytes = 1;
 };
 
-// largest |p| of the 16 lanes that hold 128 values, NaN above infinity above
-// numbers
+// largest value of the 16 lanes that hold 128 elements, NaN above infinity
+// above numbers
 template <typename P>
-__device__ __forceinline__ P group_max(P a) {
+__device__ __forceinline__ P group_max(P a, int l) {
+#pragma unroll
     for (int m = 1; m < 16; m <<= 1) {
-        const P o = __shfl_xor(a, m, 64);
+        P o;
+        if constexpr (sizeof(P) == 4) o = lane_xor(a, m, l);
+        else o = __shfl_xor(a, m, 64);
         a = o > a || o != o ? o : a;
     }
     return a;
 }
 
-// 8 consecutive p of a lane (its row of 16 lanes holds the group of 128) to
-// codes at out and, by the group's first lane, its scale
-template <typename P>
-__device__ __forceinline__ void store_i8(const P (&p)[8], float inv, bool on, int l, int8_t* out, float* out_scale) {
+// values of a lane as the output takes them: h * g, or h that was rotated
+template <typename P, bool ROT>
+__device__ __forceinline__ P value(float h, float g) {
+    return ROT ? P(h) : P(h) * P(g);
+}
+
+template <typename P, bool ROT>
+__device__ __forceinline__ P abs_max(const float (&h)[8], const float (&g)[8], int l) {
     P a = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const P b = p[j] < 0 ? -p[j] : p[j];
+        const P p = value<P, ROT>(h[j], g[j]);
+        const P b = p < 0 ? -p : p;
         a = b > a || b != b ? b : a;
     }
-    a = group_max(a);
+    return group_max(a, l);
+}
+
+// 8 consecutive elements of a lane (its row of 16 lanes holds the group of 128)
+// to codes at out and, by the group's first lane, its scale.  All lanes of a
+// wave come here.  The codes are taken in fp32, whose quotients are off by less
+// than 127 * 4.1 * 2^-24 < 3.2e-5 (the roundings of value, a, 127 / a and the
+// product); a wave with one nearer than 4e-5 to a tie (4 % of the waves), or
+// whose 127 / a is no number, takes them in 64 bits.
+template <bool ROT>
+__device__ __forceinline__ void store_i8(const float (&h)[8], const float (&g)[8], float inv, bool on, int l,
+                                         int8_t* out, float* out_scale) {
+    const float a = abs_max<float, ROT>(h, g, l);   // the rounded largest value: rounding keeps the order
+    const bool finite = a <= 3.4028234663852886e38f;
+    bool slow = !(a > 1e-30f);
+    const float r = 127.0f / a;
+    float q[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float t = value<float, ROT>(h[j], g[j]) * r;
+        q[j] = __builtin_rintf(t);
+        slow |= __builtin_fabsf(t - q[j]) > 0.5f - 4e-5f;
+    }
+    if (__ballot(slow && finite && on)) {
+        const double d = abs_max<double, ROT>(h, g, l);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            q[j] = d > 0 ? float(__builtin_rint(127.0 * value<double, ROT>(h[j], g[j]) / d)) : 0.0f;
+    }
     if (!on) return;
-    const float af = float(a);
-    const bool finite = af <= 3.4028234663852886e38f;
-    // in fp32 off a tie by less than 127 * 3 * 2^-24; nearer than 1e-4 to one
-    // (or where 127 / a is no number) the quotient is taken in 64 bits
-    const bool slow = !(af > 1e-30f);
-    const float r = 127.0f / af;
     uint32_t w[2] = {};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float t = float(p[j]) * r;
-        float q = __builtin_rintf(t);
-        if (finite && (slow || __builtin_fabsf(__builtin_fabsf(t - q) - 0.5f) < 1e-4f))
-            q = a > 0 ? float(__builtin_rint(127.0 * double(p[j]) / double(a))) : 0.0f;
-        const int c = finite ? int(q) : 0;
+        const int c = finite ? int(q[j]) : 0;
         w[j >> 2] |= (uint32_t(c) & 0xFFu) << (8 * (j & 3));
     }
-    *reinterpret_cast<uint2*>(out) = uint2{w[0], w[1]};
-    if ((l & 15) == 0) *out_scale = finite ? af * inv * (1.0f / 127.0f) : __builtin_nanf("");
+    put<false>(reinterpret_cast<u32x2*>(out), u32x2{w[0], w[1]});
+    if ((l & 15) == 0) *out_scale = finite ? a * inv * (1.0f / 127.0f) : __builtin_nanf("");
 }
 
-// p of a lane's 8 consecutive elements written, `scale` the row's factor
-template <typename O, typename P>
-__device__ __forceinline__ void store_out(const P (&p)[8], float scale, bool on, int l, int64_t at, int64_t group,
-                                          void* out, float* out_scales) {
+// a lane's 8 consecutive elements written, `scale` the row's factor
+template <typename O, bool ROT>
+__device__ __forceinline__ void store_out(const float (&h)[8], const float (&g)[8], float scale, bool on, int l,
+                                          int64_t at, int64_t group, void* out, float* out_scales) {
     if constexpr (O::kType == TL_I8) {
-        store_i8<P>(p, scale, on, l, static_cast<int8_t*>(out) + at, out_scales + group);
+        store_i8<ROT>(h, g, scale, on, l, static_cast<int8_t*>(out) + at, out_scales + group);
     } else if (on) {
         float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = float(p[j]) * scale;
+        for (int j = 0; j < 8; ++j) v[j] = value<float, ROT>(h[j], g[j]) * scale;
         store8<O>(out, at, v);
     }
 }
@@ -103,9 +127,6 @@ __device__ __forceinline__ float wave_sum(float v, int l) {
     return v;
 }
 
-template <typename O, bool ROT>
-using PType = typename std::conditional<O::kType == TL_I8 && !ROT, double, float>::type;
-
 // NB 1024-blocks a wave, as many waves as the row needs
 template <typename T, typename O, bool ROT, int NB>
 __global__ __launch_bounds__(NB == 1 ? 1024 : 768) void rms_norm_kernel(const void* x, const void* residual,
@@ -113,7 +134,6 @@ __global__ __launch_bounds__(NB == 1 ? 1024 : 768) void rms_norm_kernel(const vo
                                                                          int64_t m, int64_t k, float eps,
                                                                          void* sum_out, void* out,
                                                                          float* out_scales) {
-    using P = PType<O, ROT>;
     __shared__ float part[2][16];
     const int l = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = int(blockDim.x >> 6);
     const float inv_k = 1.0f / float(k);
@@ -200,10 +220,7 @@ __global__ __launch_bounds__(NB == 1 ? 1024 : 768) void rms_norm_kernel(const vo
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int64_t i = 1024 * (wave + int64_t(b) * waves) + 512 * e + 8 * l;
-                P p[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) p[j] = ROT ? P(h[b][e][j]) : P(h[b][e][j]) * P(g[b][e][j]);
-                store_out<O, P>(p, scale, i < k, l, base + i, (base + i) / 128, out, out_scales);
+                store_out<O, ROT>(h[b][e], g[b][e], scale, i < k, l, base + i, (base + i) / 128, out, out_scales);
             }
     }
 }
@@ -214,7 +231,6 @@ __global__ __launch_bounds__(kThreads) void rms_norm_long_kernel(const void* x, 
                                                                  int64_t m, int64_t k, float eps,
                                                                  void* sum_out, void* out,
                                                                  float* out_scales) {
-    using P = PType<O, ROT>;
     __shared__ float part[kWaves];
     const int l = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int64_t row = blockIdx.x; row < m; row += gridDim.x) {
@@ -237,7 +253,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_long_kernel(const void* x, 
                 if (i >= k) continue;
                 float v[8];
                 load_h(i, x, residual != nullptr, v);
-                if (sum_out) store8<T>(sum_out, base + i, v);
+                if (sum_out) store8<T, true>(sum_out, base + i, v);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(v[j], v[j], ss);
             }
@@ -271,10 +287,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_long_kernel(const void* x, 
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int64_t i = element(b, e);
-                P p[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) p[j] = ROT ? P(h[e][j]) : P(h[e][j]) * P(g[e][j]);
-                store_out<O, P>(p, scale, i < k, l, base + i, (base + i) / 128, out, out_scales);
+                store_out<O, ROT>(h[e], g[e], scale, i < k, l, base + i, (base + i) / 128, out, out_scales);
             }
         }
     }
