@@ -199,6 +199,28 @@ def test_sum_in_place(gpu):
             assert same is where and torch.equal(where, total) and torch.equal(got, want)
 
 
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_sum_rounds_to_nearest_even(gpu, kind):
+    """The stored sum is the rounded sum, bit for bit: ordinary values, halves
+    of the last bit, subnormal and overflowing sums, infinities and NaN."""
+    t, m, k = TYPES[kind], 8, 1024
+    g = torch.Generator().manual_seed(5)
+    bits = {2: torch.int16, 4: torch.int32}[t.itemsize]
+    any_bits = lambda: torch.randint(-2 ** 31, 2 ** 31, (m, k), generator=g).to(bits).view(t)  # noqa: E731
+    x, r = any_bits(), any_bits()
+    x[0], r[0] = 1.0, 0.5 * torch.finfo(t).eps * torch.arange(k).to(t)          # ties of every kind
+    x[1], r[1] = x[1].sign() * torch.finfo(t).tiny, r[1].sign() * torch.finfo(t).tiny * 0.5
+    x[2, :512], r[2, :512] = torch.finfo(t).max, torch.finfo(t).max
+    x[3], r[3] = x[3].float().nan_to_num(1.0).clamp(-8, 8).to(t), r[3].float().nan_to_num(1.0).clamp(-8, 8).to(t)
+    got = torch.empty(m, k, dtype=t, device=gpu)
+    tl.rms_norm(x.to(gpu), torch.ones(k, dtype=t, device=gpu), EPS, residual=r.to(gpu), sum_out=got)
+    want = (x.float() + r.float()).to(t)
+    got = got.cpu()
+    assert torch.equal(got.isnan(), want.isnan())
+    ok = ~want.isnan()
+    assert torch.equal(got.view(bits)[ok], want.view(bits)[ok])
+
+
 def test_residual_may_be_x_itself(gpu):
     x, _, gain, _ = make(2, 5120, "bf16", gpu, residual=False)
     got, total = tl.rms_norm(x, gain, EPS, residual=x)
