@@ -94,22 +94,30 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) 
     }
 }
 
-// v of lane l ^ m: DPP quad permutes for m = 1, 2, a rotation of a row of 16
-// for m = 8, swaps of rows and halves for m = 16, 32, a lane permute for m = 4
+// v of lane l ^ m: DPP quad permutes for m = 1, 2, a lane permute through LDS's
+// crossbar for m = 4, a rotation of a row of 16 for m = 8, swaps of rows and
+// halves for m = 16, 32.  (Two DPP mirrors for m = 4 are slower in the rotation,
+// which has no vector instructions to spare: 2048 x 5120 rows 21.1 us, 19.7 with
+// the permute.)
 __device__ __forceinline__ float lane_xor(float v, int m, int l) {
     const int b = __builtin_bit_cast(int, v);
     if (m == 1) return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(b, 0xB1, 0xF, 0xF, false));
     if (m == 2) return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(b, 0x4E, 0xF, 0xF, false));
+    if (m == 4) return __shfl_xor(v, m, 64);
     if (m == 8) return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(b, 0x128, 0xF, 0xF, false));
     if (m == 16) {
         const auto sw = __builtin_amdgcn_permlane16_swap(uint32_t(b), uint32_t(b), false, false);
         return __builtin_bit_cast(float, (l & 16) ? sw[0] : sw[1]);
     }
-    if (m == 32) {
-        const auto sw = __builtin_amdgcn_permlane32_swap(uint32_t(b), uint32_t(b), false, false);
-        return __builtin_bit_cast(float, l < 32 ? sw[1] : sw[0]);
-    }
-    return __shfl_xor(v, m, 64);
+    const auto sw = __builtin_amdgcn_permlane32_swap(uint32_t(b), uint32_t(b), false, false);
+    return __builtin_bit_cast(float, l < 32 ? sw[1] : sw[0]);
+}
+
+// lane_xor's step m of a reduction, whose quads hold one value once m = 4 is
+// reached: a mirrored half row does there
+__device__ __forceinline__ float reduce_xor(float v, int m, int l) {
+    if (m != 4) return lane_xor(v, m, l);
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x141, 0xF, 0xF, false));
 }
 
 // The unscaled transform H (s * v) of a 1024-block whose index bits lie in 4

@@ -20,6 +20,8 @@
 // kLongRow are gone through twice: the sum of squares (h goes to sum_out), then
 // the values; a lane handles the same elements in both passes, so the second
 // may read h back from sum_out, which may be x or the residual.
+#include <type_traits>
+
 #include "elem.h"
 #include "tl_internal.h"
 
@@ -37,36 +39,31 @@ struct I8 {
     static constexpr int kType = TL_I8, kBytes = 1;
 };
 
-// largest value of the 16 lanes that hold 128 elements, NaN above infinity
-// above numbers
-template <typename P>
-__device__ __forceinline__ P group_max(P a, int l) {
-#pragma unroll
-    for (int m = 1; m < 16; m <<= 1) {
-        P o;
-        if constexpr (sizeof(P) == 4) o = lane_xor(a, m, l);
-        else o = __shfl_xor(a, m, 64);
-        a = o > a || o != o ? o : a;
-    }
-    return a;
-}
-
 // values of a lane as the output takes them: h * g, or h that was rotated
 template <typename P, bool ROT>
 __device__ __forceinline__ P value(float h, float g) {
     return ROT ? P(h) : P(h) * P(g);
 }
 
+// largest |value| of the 16 lanes that hold 128 elements, NaN above infinity
+// above numbers: the order of their bits
 template <typename P, bool ROT>
 __device__ __forceinline__ P abs_max(const float (&h)[8], const float (&g)[8], int l) {
-    P a = 0;
+    using B = typename std::conditional<sizeof(P) == 4, uint32_t, uint64_t>::type;
+    B a = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const P p = value<P, ROT>(h[j], g[j]);
-        const P b = p < 0 ? -p : p;
-        a = b > a || b != b ? b : a;
+        const B b = __builtin_bit_cast(B, value<P, ROT>(h[j], g[j])) & (~B(0) >> 1);
+        a = b > a ? b : a;
     }
-    return group_max(a, l);
+#pragma unroll
+    for (int m = 1; m < 16; m <<= 1) {
+        B o;
+        if constexpr (sizeof(P) == 4) o = __builtin_bit_cast(B, reduce_xor(__builtin_bit_cast(float, a), m, l));
+        else o = __shfl_xor(a, m, 64);
+        a = o > a ? o : a;
+    }
+    return __builtin_bit_cast(P, a);
 }
 
 // 8 consecutive elements of a lane (its row of 16 lanes holds the group of 128)
@@ -123,7 +120,7 @@ __device__ __forceinline__ void store_out(const float (&h)[8], const float (&g)[
 // sum over the wave, the same in every lane
 __device__ __forceinline__ float wave_sum(float v, int l) {
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1) v += lane_xor(v, m, l);
+    for (int m = 1; m < 64; m <<= 1) v += reduce_xor(v, m, l);
     return v;
 }
 
