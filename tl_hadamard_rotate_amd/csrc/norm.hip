@@ -9,7 +9,7 @@
 // The row's factor 1 / sqrt(...) is common to all values, so it commutes with
 // the rotation and cancels in the codes: both are taken of p = h * gain, and
 // the factor is applied at the end.  Without the rotation p is exact in 64
-// bits (24 by 24 bits), and the codes are decided there: a quotient of 16-bit
+// bits (24 by 24 bits), and close codes are decided there: a quotient of 16-bit
 // types (22 bits by 22) lies on a tie only if the true one does.
 //
 // One workgroup per row.  A wave holds one or two 1024-blocks in registers,
@@ -71,32 +71,46 @@ __device__ __forceinline__ P abs_max(const float (&h)[8], const float (&g)[8], i
 // wave come here.  The codes are taken in fp32, whose quotients are off by less
 // than 127 * 4.1 * 2^-24 < 3.2e-5 (the roundings of value, a, 127 / a and the
 // product); a wave with one nearer than 4e-5 to a tie (4 % of the waves), or
-// whose 127 / a is no number, takes them in 64 bits.
+// whose 127 / a is no number, decides them in 64 bits: by the quotient, or,
+// where the values are fp32, by the exact remainder (eight quotients at once
+// beside the rotation's registers went to scratch: one row of 5120 took 5 us
+// more).
 template <bool ROT>
 __device__ __forceinline__ void store_i8(const float (&h)[8], const float (&g)[8], float inv, bool on, int l,
                                          int8_t* out, float* out_scale) {
     const float a = abs_max<float, ROT>(h, g, l);   // the rounded largest value: rounding keeps the order
     const bool finite = a <= 3.4028234663852886e38f;
-    bool slow = !(a > 1e-30f);
-    const float r = 127.0f / a;
+    const float up = ROT && a < 1e-30f ? 0x1p100f : 1.0f;
+    bool slow = !ROT && !(a > 1e-30f);
+    const float r = 127.0f / (a * up);
     float q[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float t = value<float, ROT>(h[j], g[j]) * r;
+        const float t = value<float, ROT>(h[j], g[j]) * up * r;
         q[j] = __builtin_rintf(t);
         slow |= __builtin_fabsf(t - q[j]) > 0.5f - 4e-5f;
     }
     if (__ballot(slow && finite && on)) {
-        const double d = abs_max<double, ROT>(h, g, l);
+        if constexpr (ROT) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            q[j] = d > 0 ? float(__builtin_rint(127.0 * value<double, ROT>(h[j], g[j]) / d)) : 0.0f;
+            for (int j = 0; j < 8; ++j) {
+                const double e = __builtin_fma(127.0, double(h[j]), -double(q[j]) * double(a));
+                const double gap = 2.0 * __builtin_fabs(e) - double(a);
+                if (gap > 0 || (gap == 0 && (int(q[j]) & 1))) q[j] += e > 0 ? 1.0f : -1.0f;
+            }
+        } else {
+            const double d = abs_max<double, ROT>(h, g, l);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                q[j] = d > 0 ? float(__builtin_rint(127.0 * value<double, ROT>(h[j], g[j]) / d)) : 0.0f;
+        }
     }
     if (!on) return;
+    const bool none = !finite || (ROT && a == 0);
     uint32_t w[2] = {};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const int c = finite ? int(q[j]) : 0;
+        const int c = none ? 0 : int(q[j]);
         w[j >> 2] |= (uint32_t(c) & 0xFFu) << (8 * (j & 3));
     }
     put<false>(reinterpret_cast<u32x2*>(out), u32x2{w[0], w[1]});
