@@ -402,10 +402,11 @@ TL_API int64_t tl_q4_gemv_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * [M, N] of y_dtype (TL_F32, TL_F16 or TL_BF16, rounded once to nearest even).
  * Products of codes and activations are exact and summed in fp32 (binary16,
  * bfloat16) or exactly (8 bits) within a group, groups in fp32.  bfloat16
- * activations are taken exactly except those below 2^-28 of the largest of
- * their 128, which count as 0; where one of the 128 is an infinity or a NaN,
- * the token's outputs are NaN.  A token's result is the same bits whatever
- * the other tokens hold, and from call to call.
+ * activations are taken exactly from 2^-28 of the largest of their 128 up, and
+ * off by at most 2^-29 of it below; where one of the 128 is an infinity or a
+ * NaN, the token's outputs are NaN.  Where a scale times the largest activation
+ * of its 128 lies past fp32, outputs may be infinite or NaN.  A token's result
+ * is the same bits whatever the other tokens hold, and from call to call.
  * Requires 1 <= M, N <= 2^24, 128 <= K <= TL_MAX_K, K % 128 == 0, M * K, N * K
  * and M * N <= 2^36, group 32, 64 or 128 (TL_ERR_FORMAT).  Tuned for M <= 64;
  * any M is accepted.  workspace: tl_q4_gemv_workspace_bytes(M, N, K) bytes

@@ -6,8 +6,8 @@ exact; the sum within a group of G passes a term through at most G additions,
 the scales and the sum over the groups add at most K/32 + 16 roundings, so
     |got - want| <= (G + K/32 + 16) u * sum_k |x w|,
 whatever the order; 8-bit activations have exact group sums and scales of their
-own (two more roundings).  bfloat16 activations below 2^-28 of their group's
-largest count as 0: at most 2^-28 * max |x| * sum |w| of the group.  The output
+own (two more roundings).  bfloat16 activations below 2^-28 of the largest of
+their 128 are off by at most 2^-29 of it: under 2^-28 * max |x| * sum |w|.  The output
 adds half a step of its type."""
 import numpy as np
 import pytest
@@ -349,6 +349,21 @@ def test_offsets_past_32_bits(gpu):
     c2, s2 = oracle.q4_quantize(codes.astype(np.float64), 128)
     assert np.array_equal(again[ends].cpu().numpy(), oracle.q4_pack(c2))
     assert np.array_equal(s[ends].cpu().numpy(), s2)
+
+
+def test_more_tokens_than_one_launch(gpu):
+    """One token more than a launch takes: it is alone in the last one, whose
+    split is still that of all tokens (scales in pieces of ten chunks)."""
+    m, n, k = 65535 * 16 + 1, 16384, 1408
+    g = torch.Generator(device=gpu).manual_seed(3)
+    packed = torch.randint(0, 256, (n, k // 2), generator=g, device=gpu, dtype=torch.uint8)
+    scales = torch.rand(n, k // 32, generator=g, device=gpu).add_(0.5).half()
+    x = torch.randint(-127, 128, (m, k), generator=g, device=gpu, dtype=torch.int8)
+    xs = torch.rand(m, k // 128, generator=g, device=gpu).add_(0.5).div_(4096)
+    y = tl.q4_gemv(packed, scales, x, xs, out_dtype=torch.float16)
+    some = [0, 63, 64, 500000, m - 2, m - 1]
+    check_product(y[some], x[some], xs[some], oracle.q4_unpack(packed.cpu().numpy()), scales.cpu().numpy(),
+                  torch.float16)
 
 
 # ------------------------------------------------------------ together

@@ -583,9 +583,10 @@ Plan q4_plan(int64_t m, int64_t n, int64_t k) {
     // one token tile: two workgroups on a compute unit; more: one
     const int64_t per_cu = p.mt == 1 ? 2 : 1, room = kLdsCu / per_cu;
     const int64_t tiles = (n + 16 * p.r - 1) / (16 * p.r), slots = cus * per_cu * kWaves;
+    const int64_t fewest = chunks * tokens * chunk_bytes<XT>() / room;   // fewer parts do not fit
     for (p.ks = kWaves; p.ks >= 1; p.ks /= 2) {
         int tried = 0;
-        for (p.parts = 1; p.parts <= chunks && tried < 5; ++p.parts) {
+        for (p.parts = fewest > 1 ? int(fewest) : 1; p.parts <= chunks && tried < 5; ++p.parts) {
             if (p.parts > 1 && m * k <= kOnePart) break;
             p.l = int((chunks + p.parts - 1) / p.parts);
             size_lds<XT, G>(p, tokens);
@@ -639,7 +640,7 @@ hipError_t launch(Args a, const Plan& p, hipStream_t stream) {
 template <int XT, int G>
 hipError_t launch_rows(const Args& a, int64_t m, hipStream_t stream) {
     const Plan p = q4_plan<XT, G>(m, a.n, a.k);
-    if (a.m == 1) return launch<XT, G, 1, 1, 1>(a, p, stream);
+    if (m == 1) return launch<XT, G, 1, 1, 1>(a, p, stream);   // (the last slice of many may be one token: their plan)
     switch (p.mt) {
         case 1: return launch<XT, G, 1, 1, 4>(a, p, stream);
         case 2: return p.r == 2 ? launch<XT, G, 2, 2, 4>(a, p, stream) : launch<XT, G, 1, 2, 4>(a, p, stream);
