@@ -353,7 +353,7 @@ def test_offsets_past_32_bits(gpu):
 
 def test_more_tokens_than_one_launch(gpu):
     """One token more than a launch takes: it is alone in the last one, whose
-    split is still that of all tokens (scales in pieces of ten chunks)."""
+    split is still that of all tokens."""
     m, n, k = 65535 * 16 + 1, 16384, 1408
     g = torch.Generator(device=gpu).manual_seed(3)
     packed = torch.randint(0, 256, (n, k // 2), generator=g, device=gpu, dtype=torch.uint8)

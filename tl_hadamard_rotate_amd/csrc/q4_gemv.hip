@@ -29,10 +29,10 @@
 //
 // Work split.  K is cut into `parts` of L chunks such that the activations of
 // a part fit in LDS; a workgroup stages one part once and each of its waves
-// then goes through tiles of 16 R weight rows on its own, without a barrier,
-// D chunks at a time: their weights are requested together and used in order
-// (a ring refilled chunk by chunk behind conditions made the compiler wait for
-// every load in flight before each use).  Where rows are few, KS waves share a tile,
+// then goes through tiles of 16 weight rows on its own, without a barrier,
+// its weights in a ring of D chunks that is refilled in pairs, 128 bytes of a row
+// at a time (one chunk at a time: 131072 x 5120 of one token 66 us, 63 in
+// pairs).  Where rows are few, KS waves share a tile,
 // each a run of the part's chunks, and add their sums through LDS.  With
 // several parts the sums go to the workspace and a second kernel adds them.
 // All sums are taken in a fixed order.  A tile's scales, one run of memory or
@@ -42,6 +42,8 @@
 // they waited for one another), in places of 16 (4) bytes a lane in order; the
 // pieces of a token's activations are exchanged by 3 bits of its number, so
 // that 8 tokens at one place lie on different banks.
+#include <cmath>
+
 #include "elem.h"
 #include "tl_internal.h"
 
@@ -139,6 +141,16 @@ __device__ __forceinline__ void load_lds(const void* g, void* l) {
     else __builtin_amdgcn_global_load_lds(from, to, 2, 0, 0);
 }
 
+// Wait until at most N loads are on the way.  By the builtin, which the compiler
+// counts: behind a wait it cannot see, it takes the loads into LDS for pending
+// and waits for every later load before it reads LDS.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | 7 << 4 | 15 << 8 | (N >> 4) << 14);
+    asm volatile("" ::: "memory");
+}
+
 // Octets of the chunk that lane quarter q and (16 bits, or groups of 32) word
 // j, (8 bits) pair of words j, meet in: first_octet(q) + octet_step(j)
 template <int G>
@@ -157,53 +169,44 @@ constexpr int chunk_bytes() { return XT == TL_I8 ? 128 : 256; }
 template <int XT>
 constexpr int chunk_floats() { return XT == TL_F16 ? 0 : 1; }
 
-// One chunk's sums added to acc[r][t]: lane (q, c) holds weight row 16 r + c
-// and tokens 16 t + 4 q .. + V - 1.  In LDS: xa[t] the lane's token's
-// activations (xsw[t] in the offset: where the lane starts, exchanged by the
-// token's bits), fa[t] the chunk's factors of tokens 16 t + 4 q .. + 3, sc its
-// scales of row c (row 16 r + c is r * row_step bytes further).
-template <int XT, int G, int R, int MT, int V>
-__device__ __forceinline__ void consume(const uint4v (&wr)[R], const uint8_t* const (&xa)[MT],
-                                        const int (&xsw)[MT], const uint8_t* sc, int row_step, const float* const (&fa)[MT], float (&acc)[R][MT][V]) {
+// One chunk's sums added to acc[t]: lane (q, c) holds weight row c and tokens
+// 16 t + 4 q .. + V - 1.  In LDS: xa[t] the lane's token's activations (xsw[t]
+// in the offset: where the lane starts, exchanged by the token's bits), fa[t]
+// the chunk's factors of tokens 16 t + 4 q .. + 3, sc its scales of row c.
+template <int XT, int G, int MT, int V>
+__device__ __forceinline__ void consume(const uint4v& wr, const uint8_t* const (&xa)[MT], const int (&xsw)[MT],
+                                        const uint8_t* sc, const float* const (&fa)[MT], float (&acc)[MT][V]) {
     constexpr int NS = 128 / G;               // scales of the chunk
     constexpr bool kPair = XT == TL_I8 && G != 32;
     constexpr int NX = kPair ? 2 : 4;         // matrix instructions along K
-    uint32_t w[R][4];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[r][i] = wr[r][i];
-        if constexpr (G != 128) {
-            swap32(w[r][0], w[r][2]);
-            swap32(w[r][1], w[r][3]);
-        }
-        if constexpr (G == 32) {
-            swap16(w[r][0], w[r][1]);
-            swap16(w[r][2], w[r][3]);
-        }
+    uint32_t w[4] = {wr[0], wr[1], wr[2], wr[3]};
+    if constexpr (G != 128) {
+        swap32(w[0], w[2]);
+        swap32(w[1], w[3]);
+    }
+    if constexpr (G == 32) {
+        swap16(w[0], w[1]);
+        swap16(w[2], w[3]);
     }
     float4v f[MT];
     if constexpr (XT != TL_F16)
 #pragma unroll
         for (int t = 0; t < MT; ++t)
             f[t] = *reinterpret_cast<const float4v*>(fa[t]);
-    float s[R][NS];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        uint32_t sb[2] = {};
-        if constexpr (NS == 1) sb[0] = *reinterpret_cast<const uint16_t*>(sc + r * row_step);
-        else if constexpr (NS == 2) sb[0] = *reinterpret_cast<const uint32_t*>(sc + r * row_step);
-        else {
-            const uint2 u = *reinterpret_cast<const uint2*>(sc + r * row_step);
-            sb[0] = u.x, sb[1] = u.y;
-        }
-#pragma unroll
-        for (int g = 0; g < NS; ++g)
-            s[r][g] = float(__builtin_bit_cast(_Float16, uint16_t(sb[g >> 1] >> (16 * (g & 1))))) *
-                      (XT == TL_I8 ? 0.0625f : 1.0f);
+    uint32_t sb[2] = {};
+    if constexpr (NS == 1) sb[0] = *reinterpret_cast<const uint16_t*>(sc);
+    else if constexpr (NS == 2) sb[0] = *reinterpret_cast<const uint32_t*>(sc);
+    else {
+        const uint2 u = *reinterpret_cast<const uint2*>(sc);
+        sb[0] = u.x, sb[1] = u.y;
     }
-    float4v d[R][MT];
-    int4v di[R][MT];
+    float s[NS];
+#pragma unroll
+    for (int g = 0; g < NS; ++g)
+        s[g] = float(__builtin_bit_cast(_Float16, uint16_t(sb[g >> 1] >> (16 * (g & 1))))) *
+               (XT == TL_I8 ? 0.0625f : 1.0f);
+    float4v d[MT];
+    int4v di[MT];
 #pragma unroll
     for (int j = 0; j < NX; ++j) {
         const bool first = j % (NX / NS) == 0, last = (j + 1) % (NX / NS) == 0;
@@ -214,60 +217,43 @@ __device__ __forceinline__ void consume(const uint4v (&wr)[R], const uint8_t* co
             half8v a[MT];
 #pragma unroll
             for (int t = 0; t < MT; ++t) a[t] = *reinterpret_cast<const half8v*>(xa[t] + (at ^ xsw[t]));
+            const half8v b = decode_f16(w[j]);
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const half8v b = decode_f16(w[r][j]);
-#pragma unroll
-                for (int t = 0; t < MT; ++t)
-                    d[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[t], b, first ? float4v{} : d[r][t], 0, 0, 0);
-            }
+            for (int t = 0; t < MT; ++t)
+                d[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[t], b, first ? float4v{} : d[t], 0, 0, 0);
         } else if constexpr (!kPair) {
-            int64_t a[MT];
+            const uint32_t lo = (w[j] << 4) & 0xF0F0F0F0u, hi = w[j] & 0xF0F0F0F0u;
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 const uint2 v = *reinterpret_cast<const uint2*>(xa[t] + (at ^ xsw[t]));
-                const uint32_t lo = __builtin_amdgcn_perm(v.y, v.x, 0x05010400u);
-                const uint32_t hi = __builtin_amdgcn_perm(v.y, v.x, 0x07030602u);
-                a[t] = int64_t(uint64_t(hi) << 32 | lo);
-            }
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const uint32_t lo = (w[r][j] << 4) & 0xF0F0F0F0u, hi = w[r][j] & 0xF0F0F0F0u;
-#pragma unroll
-                for (int t = 0; t < MT; ++t)
-                    di[r][t] = __builtin_amdgcn_mfma_i32_16x16x32_i8(a[t], int64_t(uint64_t(hi) << 32 | lo),
-                                                                     first ? int4v{} : di[r][t], 0, 0, 0);
+                const uint32_t xl = __builtin_amdgcn_perm(v.y, v.x, 0x05010400u);
+                const uint32_t xh = __builtin_amdgcn_perm(v.y, v.x, 0x07030602u);
+                di[t] = __builtin_amdgcn_mfma_i32_16x16x32_i8(int64_t(uint64_t(xh) << 32 | xl),
+                                                              int64_t(uint64_t(hi) << 32 | lo),
+                                                              first ? int4v{} : di[t], 0, 0, 0);
             }
         } else {
-            int4v a[MT];
+            const uint32_t u = w[2 * j], v = w[2 * j + 1];
+            const int4v b = {int((u << 4) & 0xF0F0F0F0u), int(u & 0xF0F0F0F0u), int((v << 4) & 0xF0F0F0F0u),
+                             int(v & 0xF0F0F0F0u)};
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
-                uint4v v = *reinterpret_cast<const uint4v*>(xa[t] + (at ^ xsw[t]));
-                order_i8(v);
-                a[t] = __builtin_bit_cast(int4v, v);
-            }
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const uint32_t u = w[r][2 * j], v = w[r][2 * j + 1];
-                const int4v b = {int((u << 4) & 0xF0F0F0F0u), int(u & 0xF0F0F0F0u), int((v << 4) & 0xF0F0F0F0u),
-                                 int(v & 0xF0F0F0F0u)};
-#pragma unroll
-                for (int t = 0; t < MT; ++t)
-                    di[r][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[t], b, first ? int4v{} : di[r][t], 0, 0, 0);
+                uint4v x = *reinterpret_cast<const uint4v*>(xa[t] + (at ^ xsw[t]));
+                order_i8(x);
+                di[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(int4v, x), b,
+                                                              first ? int4v{} : di[t], 0, 0, 0);
             }
         }
         if (last)
 #pragma unroll
-            for (int r = 0; r < R; ++r)
+            for (int t = 0; t < MT; ++t)
 #pragma unroll
-                for (int t = 0; t < MT; ++t)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        float v;
-                        if constexpr (XT == TL_I8) v = float(di[r][t][i]);
-                        else v = d[r][t][i];
-                        acc[r][t][i] = __builtin_fmaf(v, XT == TL_F16 ? s[r][g] : s[r][g] * f[t][i], acc[r][t][i]);
-                    }
+                for (int i = 0; i < V; ++i) {
+                    float v;
+                    if constexpr (XT == TL_I8) v = float(di[t][i]);
+                    else v = d[t][i];
+                    acc[t][i] = __builtin_fmaf(v, XT == TL_F16 ? s[g] : s[g] * f[t][i], acc[t][i]);
+                }
     }
 }
 
@@ -281,7 +267,7 @@ struct Args {
     int64_t n, k;
     int m, y_dtype;
     // parts of L chunks; KS waves share a tile, LW = ceil(L / KS) chunks each;
-    // tiles of 16 R rows, row groups (workgroups of a part); chunks whose
+    // tiles of 16 rows, row groups (workgroups of a part); chunks whose
     // scales a wave has in LDS at a time, and their bytes
     int parts, l, ks, lw, tiles, groups, seg, s_bytes;
 };
@@ -294,7 +280,7 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, float v, int y_dtyp
     else static_cast<uint16_t*>(y)[at] = uint16_t(y_dtype == TL_F16 ? f16_bits(v) : bf16_bits(v));
 }
 
-template <int XT, int G, int R, int MT, int D, int V>
+template <int XT, int G, int MT, int D, int V>
 __global__ __launch_bounds__(64 * kWaves, MT == 1 ? 4 : 2) void q4_gemv_kernel(const Args p) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     constexpr int kCB = chunk_bytes<XT>();
@@ -332,37 +318,31 @@ __global__ __launch_bounds__(64 * kWaves, MT == 1 ? 4 : 2) void q4_gemv_kernel(c
     const int stride = p.groups * tws;
     int tile = group * tws + tw;
 
-    // Weights on the way: D chunks of a tile.  voff: the lane's rows of the
-    // tile (rows that do not exist repeat the last one; their sums are not
-    // stored).
-    uint4v buf[D][R];
-    uint32_t voff[R];
+    // Weights on the way: D chunks of a tile.  voff: the lane's row of the tile
+    // (rows that do not exist repeat the last one; their sums are not stored).
+    uint4v buf[D];
+    uint32_t voff = 0;
     const auto enter = [&](int t) {
-        const int64_t n0 = int64_t(t) * (16 * R);
-        const int last = int(p.n - n0 < 16 * R ? p.n - n0 : 16 * R) - 1;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int row = 16 * r + c;
-            voff[r] = uint32_t(row < last ? row : last) * uint32_t(row_bytes) + 16u * uint32_t(q);
-        }
+        const int64_t n0 = int64_t(t) * 16;
+        const int last = int(p.n - n0 < 16 ? p.n - n0 : 16) - 1;
+        voff = uint32_t(c < last ? c : last) * uint32_t(row_bytes) + 16u * uint32_t(q);
         return p.packed + (n0 * row_bytes + int64_t(c0 + w0) * 64);
     };
-    // chunks i0 .. i0 + D - 1 (past the end the last one again)
-    const auto fetch = [&](const uint8_t* b, int i0) {
+    // chunk i into place d (past the end the last one again)
+    const auto fetch = [&](const uint8_t* b, int i, int d) {
+        buf[d] = *reinterpret_cast<const uint4v*>(b + 64 * (i < mine ? i : mine - 1) + voff);
+    };
+    const auto fetch_first = [&](const uint8_t* b) {
 #pragma unroll
-        for (int d = 0; d < D; ++d) {
-            const uint8_t* const from = b + 64 * (i0 + d < mine ? i0 + d : mine - 1);
-#pragma unroll
-            for (int r = 0; r < R; ++r) buf[d][r] = *reinterpret_cast<const uint4v*>(from + voff[r]);
-        }
+        for (int d = 0; d < D; ++d) fetch(b, d, d);
     };
     // Scales of chunks [i0, i0 + SEG) of this wave's of a tile into its LDS,
     // [row][chunk]: one run of memory when they are all of the rows, else
     // places of 4 bytes (a scale, or two)
     constexpr int kPlaces = NS > 2 ? NS / 2 : 1;
     const auto load_s = [&](int t, int i0) {
-        const int64_t n0 = int64_t(t) * (16 * R);
-        const int rows = int(p.n - n0 < 16 * R ? p.n - n0 : 16 * R);
+        const int64_t n0 = int64_t(t) * 16;
+        const int rows = int(p.n - n0 < 16 ? p.n - n0 : 16);
         const int span = mine - i0 < p.seg ? mine - i0 : p.seg;
         const uint16_t* const src = p.scales + (n0 * chunks + c0 + w0 + i0) * NS;
         if (span == chunks) {
@@ -404,9 +384,9 @@ __global__ __launch_bounds__(64 * kWaves, MT == 1 ? 4 : 2) void q4_gemv_kernel(c
     if (work) {
         load_s(tile, 0);
         base = enter(tile);
-        fetch(base, 0);
+        fetch_first(base);
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    wait_loads<0>();
     __syncthreads();
     if constexpr (XT == TL_BF16) {
         const int count = tokens * len;   // (token, chunk), a row of 16 lanes each
@@ -435,34 +415,44 @@ __global__ __launch_bounds__(64 * kWaves, MT == 1 ? 4 : 2) void q4_gemv_kernel(c
     for (int t = 0; t < MT; ++t)   // (factors of absent tokens: any)
         fa[t] = lf + w0 * (kF * ts) + (16 * t + 4 * q < ts ? 16 * t + 4 * q : ts - 4);
     for (; tile < p.tiles; tile += stride) {
-        float acc[R][MT][V] = {};
-        const int64_t n0 = int64_t(tile) * (16 * R);
-        const int rows = int(p.n - n0 < 16 * R ? p.n - n0 : 16 * R);
+        float acc[MT][V] = {};
+        const int64_t n0 = int64_t(tile) * 16;
+        const int rows = int(p.n - n0 < 16 ? p.n - n0 : 16);
         const bool more = tile + stride < p.tiles;
         int seg0 = 0;
         for (int i0 = 0; i0 < mine;) {
             if (i0 == seg0 + p.seg) {
                 seg0 = i0;
                 load_s(tile, seg0);
-                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                wait_loads<0>();
             }
             const int span = mine - seg0 < p.seg ? mine - seg0 : p.seg;
             const int s_step = span == chunks ? 2 * NS : 4 * kPlaces, row_step = span * s_step;   // bytes
             const uint8_t* const sc = ls + c * row_step - seg0 * s_step;
-#pragma unroll
-            for (int d = 0; d < D; ++d) {
-                const int i = i0 + d;
-                if (i >= mine) break;
+            const auto step = [&](int i, const uint4v& w) {
                 const uint8_t* xc[MT];
 #pragma unroll
                 for (int t = 0; t < MT; ++t) xc[t] = xa[t] + i * kCB;
                 const float* fc[MT];
 #pragma unroll
                 for (int t = 0; t < MT; ++t) fc[t] = fa[t] + i * (kF * ts);
-                consume<XT, G, R, MT, V>(buf[d], xc, xsw, sc + i * s_step, 16 * row_step, fc, acc);
+                consume<XT, G, MT, V>(w, xc, xsw, sc + i * s_step, fc, acc);
+            };
+            if (i0 + D < mine) {
+#pragma unroll
+                for (int d = 0; d < D; ++d) {
+                    step(i0 + d, buf[d]);
+                    if (d & 1) fetch(base, i0 + D + d - 1, d - 1);
+                    if ((d & 1) || d == D - 1) fetch(base, i0 + D + d, d);
+                }
+            } else {
+#pragma unroll
+                for (int d = 0; d < D; ++d) {
+                    if (i0 + d >= mine) break;
+                    step(i0 + d, buf[d]);
+                }
             }
             i0 += D;
-            if (i0 < mine) fetch(base, i0);
         }
         if (p.ks > 1) {
             // (one tile a wave then)
@@ -470,46 +460,40 @@ __global__ __launch_bounds__(64 * kWaves, MT == 1 ? 4 : 2) void q4_gemv_kernel(c
 #pragma unroll
             for (int t = 0; t < MT; ++t)
 #pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        red[((wave * MT + t) * R + r) * 256 + (4 * q + i) * 16 + c] = acc[r][t][i];
+                for (int i = 0; i < V; ++i) red[(wave * MT + t) * 256 + (4 * q + i) * 16 + c] = acc[t][i];
             break;
         }
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+        for (int t = 0; t < MT; ++t)
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int row = 16 * r + c, tok = 16 * t + 4 * q + i;
-                    if (row >= rows || tok >= tokens) continue;
-                    const int64_t at = (m0 + tok) * p.n + n0 + row;
-                    if (p.parts > 1) p.sums[part * sums_stride(int64_t(p.m) * p.n) + at] = acc[r][t][i];
-                    else store_y(p.y, at, acc[r][t][i], p.y_dtype);
-                }
+            for (int i = 0; i < V; ++i) {
+                const int tok = 16 * t + 4 * q + i;
+                if (c >= rows || tok >= tokens) continue;
+                const int64_t at = (m0 + tok) * p.n + n0 + c;
+                if (p.parts > 1) p.sums[part * sums_stride(int64_t(p.m) * p.n) + at] = acc[t][i];
+                else store_y(p.y, at, acc[t][i], p.y_dtype);
+            }
         if (more) {
             // the next tile's scales (the old ones have been read), then its
             // weights; all but the latter are awaited
             load_s(tile + stride, 0);
             asm volatile("" ::: "memory");
             base = enter(tile + stride);
-            fetch(base, 0);
-            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(D * R) : "memory");
+            fetch_first(base);
+            wait_loads<D>();
         }
     }
     if (p.ks > 1) {
         // waves without a tile meet the others at both barriers
         if (tile >= p.tiles) __syncthreads();
         __syncthreads();
-        const int64_t n0 = int64_t(group) * tws * (16 * R);
-        const int rows = int(p.n - n0 < tws * 16 * R ? p.n - n0 : tws * 16 * R);
+        const int64_t n0 = int64_t(group) * tws * 16;
+        const int rows = int(p.n - n0 < tws * 16 ? p.n - n0 : tws * 16);
         for (int o = tid; o < rows * tokens; o += threads) {
             const int tok = o / rows, row = o - tok * rows;
-            const int w1 = row / (16 * R), rr = row - w1 * (16 * R);
-            const float* src = red + ((w1 * p.ks * MT + (tok >> 4)) * R + (rr >> 4)) * 256 + (tok & 15) * 16 + (rr & 15);
+            const float* src = red + ((row / 16 * p.ks) * MT + (tok >> 4)) * 256 + (tok & 15) * 16 + row % 16;
             float v = 0.0f;
-            for (int w = 0; w < p.ks; ++w) v += src[w * (MT * R * 256)];
+            for (int w = 0; w < p.ks; ++w) v += src[w * (MT * 256)];
             const int64_t at = (m0 + tok) * p.n + n0 + row;
             if (p.parts > 1) p.sums[part * sums_stride(int64_t(p.m) * p.n) + at] = v;
             else store_y(p.y, at, v, p.y_dtype);
@@ -540,37 +524,42 @@ __global__ __launch_bounds__(256) void q4_join_kernel(const float* __restrict__ 
 
 constexpr int64_t kLdsCu = 160 * 1024;
 constexpr int64_t kOnePart = 16384;   // M * K that is never cut into parts: its activations fit in LDS
-constexpr int kScaleLds = 2560;       // scales of a wave: K = 5120 of 32 rows in groups of 128
+constexpr int kScaleLds = 2560;       // scales of a wave: K = 5120 in groups of 64
 
 // How a call is split; the same for the workspace and the launch.
 struct Plan {
-    int r, mt, l, parts, ks, d, seg;
+    int mt, l, parts, ks, d, seg;
     int64_t s_bytes, lds;
 };
 
-// chunks of weights a wave has on the way
-constexpr int ring_depth(int r, int mt) { return r == 2 ? 2 : mt == 1 ? 4 : 5; }
+// chunks of weights a wave has on the way (64 tokens: 4 spill; 17408 x 5120 by
+// 64 binary16 tokens 28.8 us with 2, 30.1 with 1.  Two row tiles of a wave that
+// share the activations' reads, with 1 chunk, are slower from 8 to 64 tokens
+// on most shapes: 5120 x 17408 by 20 tokens 22.8 us, 18.1 with one)
+constexpr int ring_depth(int mt) { return mt == 4 ? 2 : 4; }
 
 // LDS bytes of a workgroup with parts of l chunks, and of a wave's scales
 template <int XT, int G>
 void size_lds(Plan& p, int64_t tokens) {
     const int lw = (p.l + p.ks - 1) / p.ks;
-    int chunk = 16 * p.r * (G == 128 ? 4 : 256 / G);        // bytes of a chunk's scales
-    if (p.parts == 1 && p.ks == 1 && lw * chunk / (G == 128 ? 2 : 1) <= kScaleLds) chunk = 16 * p.r * (256 / G);
+    int chunk = 16 * (G == 128 ? 4 : 256 / G);        // bytes of a chunk's scales
+    if (p.parts == 1 && p.ks == 1 && lw * chunk / (G == 128 ? 2 : 1) <= kScaleLds) chunk = 16 * (256 / G);
     p.seg = lw;
     if (lw * chunk > kScaleLds) p.seg = kScaleLds / chunk / p.d * p.d;   // whole steps
     p.s_bytes = (p.seg * chunk + 15) / 16 * 16;
     p.lds = tokens * int64_t(p.l) * chunk_bytes<XT>() + int64_t(p.l) * chunk_floats<XT>() * ((tokens + 3) / 4 * 16) +
             kWaves * p.s_bytes;
-    const int64_t red = p.ks > 1 ? int64_t(kWaves) * p.mt * p.r * 1024 : 0;
+    const int64_t red = p.ks > 1 ? int64_t(kWaves) * p.mt * 1024 : 0;
     if (p.lds < red) p.lds = red;
 }
 
 // The split with the least estimated time.  What it weighs was measured at N x
 // K from 1024 x 5120 to 131072 x 5120: weights arrive at 5.3 bytes per ps
 // once about 0.7 of the waves that fit are busy (0.4 of that with few), more
-// waves than fit cost a tenth; staged activations at 12; a second kernel costs
-// 2 us and its sums 6 bytes per ps.
+// waves than fit cost a tenth, tiles that do not divide among the waves half of
+// what they leave idle (without that, 17408 x 5120 by 45 8-bit tokens took 27.3
+// us, 22.8 with); staged activations at 12; a second kernel costs 2 us and its
+// sums 6 bytes per ps.
 template <int XT, int G>
 Plan q4_plan(int64_t m, int64_t n, int64_t k) {
     const int64_t chunks = k / 128, cus = cu_count();
@@ -578,11 +567,10 @@ Plan q4_plan(int64_t m, int64_t n, int64_t k) {
     double least = 0;
     p.mt = m <= 16 ? 1 : m <= 32 ? 2 : m <= 48 ? 3 : 4;
     const int64_t tokens = m < 16 * p.mt ? m : 16 * p.mt, slices = (m + 16 * p.mt - 1) / (16 * p.mt);
-    p.r = p.mt > 1 && n >= 64 * cus ? 2 : 1;
-    p.d = ring_depth(p.r, p.mt);
+    p.d = ring_depth(p.mt);
     // one token tile: two workgroups on a compute unit; more: one
     const int64_t per_cu = p.mt == 1 ? 2 : 1, room = kLdsCu / per_cu;
-    const int64_t tiles = (n + 16 * p.r - 1) / (16 * p.r), slots = cus * per_cu * kWaves;
+    const int64_t tiles = (n + 15) / 16, slots = cus * per_cu * kWaves;
     const int64_t fewest = chunks * tokens * chunk_bytes<XT>() / room;   // fewer parts do not fit
     for (p.ks = kWaves; p.ks >= 1; p.ks /= 2) {
         int tried = 0;
@@ -598,7 +586,13 @@ Plan q4_plan(int64_t m, int64_t n, int64_t k) {
             const double over = p.ks > 1 && waves > 1.125 * slots ? 1.1 : 1.0;
             double groups = double((tiles + kWaves / p.ks - 1) / (kWaves / p.ks)) * p.parts;
             if (p.ks == 1 && groups > double(cus * per_cu)) groups = double(cus * per_cu);
-            double us = double(n) * k / 2 * slices / 5.3e6 * over / (0.4 + 0.6 * busy) +
+            // tiles a wave goes through, over their mean
+            double uneven = 1.0;
+            if (p.ks == 1) {
+                const double each = double(tiles) / (double(kWaves) * groups / p.parts);
+                uneven = 0.5 + 0.5 * std::ceil(each) / each;
+            }
+            double us = double(n) * k / 2 * slices / 5.3e6 * over * uneven / (0.4 + 0.6 * busy) +
                         groups * slices * double(tokens) * p.l * chunk_bytes<XT>() / 12e6;
             if (p.parts > 1) us += 2.0 + double(p.parts) * m * n * 8 / 6e6;
             if (least == 0 || us < least) {
@@ -610,14 +604,14 @@ Plan q4_plan(int64_t m, int64_t n, int64_t k) {
     return best;
 }
 
-template <int XT, int G, int R, int MT, int V>
+template <int XT, int G, int MT, int V>
 hipError_t launch(Args a, const Plan& p, hipStream_t stream) {
-    const auto kernel = q4_gemv_kernel<XT, G, R, MT, ring_depth(R, MT), V>;
+    const auto kernel = q4_gemv_kernel<XT, G, MT, ring_depth(MT), V>;
     a.parts = p.parts;
     a.l = p.l;
     a.ks = p.ks;
     a.lw = (p.l + p.ks - 1) / p.ks;
-    a.tiles = int((a.n + 16 * R - 1) / (16 * R));
+    a.tiles = int((a.n + 15) / 16);
     const int tws = kWaves / p.ks;
     a.groups = (a.tiles + tws - 1) / tws;
     const int per_cu = MT == 1 ? 2 : 1;
@@ -640,12 +634,12 @@ hipError_t launch(Args a, const Plan& p, hipStream_t stream) {
 template <int XT, int G>
 hipError_t launch_rows(const Args& a, int64_t m, hipStream_t stream) {
     const Plan p = q4_plan<XT, G>(m, a.n, a.k);
-    if (m == 1) return launch<XT, G, 1, 1, 1>(a, p, stream);   // (the last slice of many may be one token: their plan)
+    if (m == 1) return launch<XT, G, 1, 1>(a, p, stream);   // (the last slice of many may be one token: their plan)
     switch (p.mt) {
-        case 1: return launch<XT, G, 1, 1, 4>(a, p, stream);
-        case 2: return p.r == 2 ? launch<XT, G, 2, 2, 4>(a, p, stream) : launch<XT, G, 1, 2, 4>(a, p, stream);
-        case 3: return p.r == 2 ? launch<XT, G, 2, 3, 4>(a, p, stream) : launch<XT, G, 1, 3, 4>(a, p, stream);
-        default: return p.r == 2 ? launch<XT, G, 2, 4, 4>(a, p, stream) : launch<XT, G, 1, 4, 4>(a, p, stream);
+        case 1: return launch<XT, G, 1, 4>(a, p, stream);
+        case 2: return launch<XT, G, 2, 4>(a, p, stream);
+        case 3: return launch<XT, G, 3, 4>(a, p, stream);
+        default: return launch<XT, G, 4, 4>(a, p, stream);
     }
 }
 
