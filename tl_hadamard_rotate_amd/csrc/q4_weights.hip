@@ -11,6 +11,11 @@
 // can c from a correctly rounded fp32 quotient: with S of 11 bits and k + 1/2
 // of at most 4, w is a multiple of 2^-24 of itself away from S (k + 1/2), and
 // that is more than half the quotient's last place for each k.
+//
+// Bound by memory: a lane reads 8 weights (32 or 16 bytes) and writes 4 bytes, a
+// group's maximum is exchanged among 4 to 16 neighbouring lanes, nothing goes
+// through LDS.  17408 x 5120 fp32 weights to 4 bits and back to binary16, 627
+// MB, take 110 us in both launches together, 5.7 TB/s.
 #include "elem.h"
 #include "tl_internal.h"
 
