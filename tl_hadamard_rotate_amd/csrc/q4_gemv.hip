@@ -541,11 +541,18 @@ struct Plan {
     int64_t s_bytes, lds;
 };
 
-// chunks of weights a wave has on the way (64 tokens: 4 spill; 17408 x 5120 by
-// 64 binary16 tokens 28.8 us with 2, 30.1 with 1.  Two row tiles of a wave that
-// share the activations' reads, with 1 chunk, are slower from 8 to 64 tokens
-// on most shapes: 5120 x 17408 by 20 tokens 22.8 us, 18.1 with one)
-constexpr int ring_depth(int mt) { return mt == 4 ? 2 : 4; }
+// Chunks of weights a wave has on the way: 2 or 4.  64 tokens: 4 spill (17408 x
+// 5120 by binary16 28.8 us with 2, 30.1 with 1).  Up to 16 tokens 2 are as good or
+// better (131072 x 5120 of one token 62.0 us, 64.2 with 4; 6144 x 5120 of 16
+// binary16 tokens 11.4 and 12.3) but for several 8-bit ones (10240 x 4096 of 4 9.0
+// us, 8.05 with 4); 32 and 48 tokens: 32003 x 5120 of 20 binary16 27.7 us, 26.3
+// with 4.  (Two row tiles of a wave that share the activations' reads are slower
+// from 8 to 64 tokens on most shapes: 5120 x 17408 by 20 tokens 22.8 us, 18.1
+// with one.)
+template <int XT>
+constexpr int ring_depth(int mt, bool one_token) {
+    return mt == 4 || (mt == 1 && (one_token || XT != TL_I8)) ? 2 : 4;
+}
 
 // LDS bytes of a workgroup with parts of l chunks, and of a wave's scales
 template <int XT, int G>
@@ -576,7 +583,7 @@ Plan q4_plan(int64_t m, int64_t n, int64_t k) {
     double least = 0;
     p.mt = m <= 16 ? 1 : m <= 32 ? 2 : m <= 48 ? 3 : 4;
     const int64_t tokens = m < 16 * p.mt ? m : 16 * p.mt, slices = (m + 16 * p.mt - 1) / (16 * p.mt);
-    p.d = ring_depth(p.mt);
+    p.d = ring_depth<XT>(p.mt, m == 1);
     // one token tile: two workgroups on a compute unit; more: one
     const int64_t per_cu = p.mt == 1 ? 2 : 1, room = kLdsCu / per_cu;
     const int64_t tiles = (n + 15) / 16, slots = cus * per_cu * kWaves;
@@ -615,7 +622,7 @@ Plan q4_plan(int64_t m, int64_t n, int64_t k) {
 
 template <int XT, int G, int MT, int V>
 hipError_t launch(Args a, const Plan& p, hipStream_t stream) {
-    const auto kernel = q4_gemv_kernel<XT, G, MT, ring_depth(MT), V>;
+    const auto kernel = q4_gemv_kernel<XT, G, MT, ring_depth<XT>(MT, V == 1), V>;
     a.parts = p.parts;
     a.l = p.l;
     a.ks = p.ks;
