@@ -31,7 +31,7 @@
 // a part fit in LDS; a workgroup stages one part once and each of its waves
 // then goes through tiles of 16 weight rows on its own, without a barrier,
 // its weights in a ring of D chunks that is refilled in pairs, 128 bytes of a row
-// at a time (one chunk at a time: 131072 x 5120 of one token 66 us, 63 in
+// at a time (one chunk at a time: 131072 x 5120 of one token 66 us, 62.5 in
 // pairs).  Where rows are few, KS waves share a tile,
 // each a run of the part's chunks, and add their sums through LDS.  With
 // several parts the sums go to the workspace and a second kernel adds them.
@@ -44,12 +44,12 @@
 // that 8 tokens at one place lie on different banks.
 //
 // Bound.  One token: the weights' bytes from HBM (131072 x 5120 in groups of 128,
-// 346 MB, 62.5 us, 5.5 TB/s; a plain read of as much 55 us).  Few tokens: besides
+// 346 MB, 60.9 us, 5.7 TB/s; a plain read of as much 55 us).  Few tokens: besides
 // that the staging of a part's activations, which every workgroup does before its
 // first product, and the second kernel (5120 x 17408 by 8 bfloat16 tokens, 47 MB,
-// 18.9 us of which 2.7 the second kernel).  From some 40 tokens on the vector
+// 19.0 us of which 2.7 the second kernel).  From some 40 tokens on the vector
 // instructions: decoding, and one fma for each group, token and row (32003 x 5120
-// in groups of 32 by 45 tokens, 42 us: 18 us of vector and 6 of matrix
+// in groups of 32 by 45 tokens, 43 us: 18 us of vector and 6 of matrix
 // instructions on each SIMD, 6 in the second kernel).
 #include <cmath>
 
