@@ -149,6 +149,17 @@ def test_i8_ties_go_to_even(gpu):
         assert np.array_equal(host(q)[0], want)
 
 
+@pytest.mark.parametrize("rot", [False, True])
+def test_i8_codes_do_not_depend_on_a_power_of_two(gpu, rot):
+    """A gain of 2^-110 leaves every rounding as it was: the same codes, scales
+    times 2^-110 (their values then lie below 1e-30)."""
+    x, _, _, s = make(3, 2048, "f32", gpu, residual=False, rot=rot)
+    one = torch.ones(2048, device=gpu)
+    q, sc = tl.rms_norm_i8(x, one, EPS, signs=s)
+    tiny, tiny_sc = tl.rms_norm_i8(x, one * 2.0 ** -110, EPS, signs=s)
+    assert torch.equal(q, tiny) and torch.equal(sc * 2.0 ** -110, tiny_sc)
+
+
 def test_zero_rows_and_groups(gpu):
     x, _, gain, s = make(4, 2048, "f16", gpu, residual=False, rot=True)
     x[1] = 0
