@@ -51,6 +51,15 @@ def test_norm_overlaps():
         assert _norm(od=3, scales=base) == 5
 
 
+def test_norm_of_one_row_refuses_the_sum_over_its_gain():
+    """With one row the gain is as long as x: the same buffer as x, residual
+    and gain may be read by all three, but not written as the sum in place."""
+    for k in (1024, 32768):                                 # one pass, two passes
+        assert _norm(m=1, k=k, gain=B[0], sum_out=B[0]) == 5
+        assert _norm(m=1, k=k, gain=B[1], sum_out=B[1]) == 5
+        assert _norm(m=1, k=k, x=B[0], residual=B[0], gain=B[0], sum_out=B[0]) == 5
+
+
 def _quant(w=B[0], signs=NULL, n=4, k=1024, wd=0, group=128, packed=B[2], scales=B[3]):
     return tl.lib().tl_q4_quantize(w, signs, n, k, wd, group, packed, scales, NULL)
 

@@ -367,14 +367,18 @@ tl_status tl_rms_norm(const void* x, const void* residual, const void* gain, con
     const int64_t e = dtype_bytes(x_dtype), xb = M * K * e, ob = M * K * dtype_bytes(out_dtype);
     const int64_t sb = M * (K / TL_GROUP) * 4;
     // the outputs against the inputs and each other; sum_out may be x or residual
-    const std::pair<const void*, int64_t> ins[] = {{x, xb}, {residual, xb}, {gain, K * e}, {signs, K}};
+    // (the gain of one row is as long as they are, so the address does not tell them apart)
+    const struct {
+        const void* p;
+        int64_t bytes;
+        bool in_place;
+    } ins[] = {{x, xb, true}, {residual, xb, true}, {gain, K * e, false}, {signs, K, false}};
     for (const auto& in : ins) {
-        if (!in.first) continue;
-        if (overlap(out, ob, in.first, in.second)) return TL_ERR_ALIAS;
-        if (out_scales && overlap(out_scales, sb, in.first, in.second)) return TL_ERR_ALIAS;
-        const bool in_place = sum_out == in.first && (in.first == x || in.first == residual) &&
-                              in.second == xb;
-        if (sum_out && !in_place && overlap(sum_out, xb, in.first, in.second)) return TL_ERR_ALIAS;
+        if (!in.p) continue;
+        if (overlap(out, ob, in.p, in.bytes)) return TL_ERR_ALIAS;
+        if (out_scales && overlap(out_scales, sb, in.p, in.bytes)) return TL_ERR_ALIAS;
+        if (sum_out && !(in.in_place && sum_out == in.p) && overlap(sum_out, xb, in.p, in.bytes))
+            return TL_ERR_ALIAS;
     }
     if (sum_out && overlap(sum_out, xb, out, ob)) return TL_ERR_ALIAS;
     if (out_scales && (overlap(out_scales, sb, out, ob) ||
