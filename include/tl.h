@@ -338,8 +338,9 @@ TL_API tl_status tl_quantize(const float* w, const int8_t* signs, int64_t N, int
  *     follow exactly from h and gain (decided in 64 bits at ties and near
  *     them).  A group that holds an infinity or a NaN gets codes 0 and the
  *     scale NaN.
- * Sums are fp32: a row whose h^2 overflow fp32 (|h| above about 1.8e19) gives
- * 0.  Bitwise reproducible from call to call.
+ * Sums are fp32: a row whose sum of h^2 passes fp32 (3.4e38) gives 0, as one
+ * with an infinity does beside it; 8-bit codes of such values, and of a row with
+ * a NaN, are 0.  Bitwise reproducible from call to call.
  * Requires 1 <= M <= 2^24, 8 <= K <= TL_MAX_K, K % 8 == 0 (K % 1024 == 0 with
  * signs, K % 128 == 0 with TL_I8), M * K <= 2^36; eps a positive normal fp32
  * number (TL_ERR_VALUE); every pointer 16-byte aligned, out_scales 4-byte.  sum_out may equal x

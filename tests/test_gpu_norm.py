@@ -190,6 +190,26 @@ def test_nonfinite_values_stay_in_their_rows(gpu, kind):
     assert torch.isnan(scales[1]).all() and torch.isnan(scales[3, 11]) and not q[3, 1408:1536].any()
 
 
+@pytest.mark.parametrize("rot", [False, True])
+@pytest.mark.parametrize("k", [2048, 36864])
+def test_i8_codes_of_rows_without_finite_norms(gpu, k, rot):
+    """A NaN makes its whole row NaN; an infinity, or squares whose sum passes
+    fp32, make the rest of the row 0: codes 0 in every group, scales NaN or 0."""
+    x, _, gain, s = make(5, k, "f32", gpu, residual=False, rot=rot)
+    clean = tl.rms_norm_i8(x, gain, EPS, signs=s)
+    x[1, 7], x[2, 1500] = float("nan"), float("inf")
+    x[3] *= 1e25
+    q, scales = tl.rms_norm_i8(x, gain, EPS, signs=s)
+    assert torch.equal(q[[0, 4]], clean[0][[0, 4]]) and torch.equal(scales[[0, 4]], clean[1][[0, 4]])
+    assert not q[1:4].any()
+    sc = host(scales)
+    hit = np.zeros(k // 128, bool)
+    hit[8:16 if rot else 8] = True
+    hit[11] = True
+    assert np.isnan(sc[1]).all() and not sc[3].any()
+    assert np.isnan(sc[2, hit]).all() and not sc[2, ~hit].any()
+
+
 def test_large_and_tiny_values(gpu):
     """binary16 rows near its largest and smallest numbers, eps of the smallest
     normal number."""

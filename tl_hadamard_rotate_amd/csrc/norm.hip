@@ -112,7 +112,9 @@ __device__ __forceinline__ void store_i8(const float (&h)[8], const float (&g)[8
         }
     }
     if (!on) return;
-    const bool none = !finite || (ROT && a == 0);
+    // (inv is 0 or NaN where the row has an infinity, a NaN or squares past fp32:
+    // all its values are 0 or NaN then)
+    const bool none = !finite || !(inv > 0.0f) || (ROT && a == 0);
     uint32_t w[2] = {};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
