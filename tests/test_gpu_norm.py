@@ -210,6 +210,34 @@ def test_i8_codes_of_rows_without_finite_norms(gpu, k, rot):
     assert np.isnan(sc[2, hit]).all() and not sc[2, ~hit].any()
 
 
+@pytest.mark.parametrize("xf,gf,eps", [(1e15, 1e25, EPS), (1e-17, 1e-25, 2.0 ** -126)])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("m,k", [(3, 2048), (2, 17408), (1, 33024)])
+def test_products_with_the_gain_past_fp32(gpu, m, k, kind, xf, gf, eps):
+    """Outputs that fit although h * gain passes fp32, or lies below its
+    normal numbers."""
+    x, _, gain, _ = make(m, k, kind, gpu, seed=k, residual=False)
+    x, gain = (x.double() * xf).to(x.dtype), (gain.double() * gf).to(x.dtype)
+    h, y, want = reference(x, None, gain, None, kind, eps=eps)
+    for out in ("f32", "bf16"):
+        got = tl.rms_norm(x, gain, eps, out_dtype=TYPES[out])
+        assert np.all(np.abs(host(got) - want) <= bounds(want, y, k, TYPES[out], False))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("gf", [2.0 ** -49, 2.0 ** 49])
+@pytest.mark.parametrize("xf,eps", [(1e16, EPS), (1e-17, 2.0 ** -126)])
+def test_gains_within_the_stated_range(gpu, kind, gf, xf, eps):
+    """Rotated and 8-bit outputs at the ends of the gains that tl.h states."""
+    for rot in (False, True):
+        x, _, gain, s = make(3, 2048, kind, gpu, residual=False, rot=rot)
+        x, gain = (x.double() * xf).to(x.dtype), (gain.double() * gf).to(x.dtype)
+        h, y, want = reference(x, None, gain, s, kind, eps=eps)
+        got = tl.rms_norm(x, gain, eps, signs=s, out_dtype=torch.float32)
+        assert np.all(np.abs(host(got) - want) <= bounds(want, y, 2048, torch.float32, rot))
+        i8_check(*tl.rms_norm_i8(x, gain, eps, signs=s), want, y, 2048, None if rot else h * host(gain))
+
+
 def test_large_and_tiny_values(gpu):
     """binary16 rows near its largest and smallest numbers, eps of the smallest
     normal number."""

@@ -7,8 +7,8 @@
 //   code = rint(127 value / a)
 //
 // The row's factor 1 / sqrt(...) is common to all values, so it commutes with
-// the rotation and cancels in the codes: both are taken of p = h * gain, and
-// the factor is applied at the end.  Without the rotation p is exact in 64
+// the rotation and cancels in the codes: both are taken of p = h * gain, in
+// fp32 like the rotation's sums, and the factor is applied at the end.  Without the rotation p is exact in 64
 // bits (24 by 24 bits), and close codes are decided there: a quotient of 16-bit
 // types (22 bits by 22) lies on a tie only if the true one does.
 //
@@ -125,7 +125,8 @@ __device__ __forceinline__ void store_i8(const float (&h)[8], const float (&g)[8
     if ((l & 15) == 0) *out_scale = finite ? a * inv * (1.0f / 127.0f) : __builtin_nanf("");
 }
 
-// a lane's 8 consecutive elements written, `scale` the row's factor
+// a lane's 8 consecutive elements written, `scale` the row's factor: taken before
+// the gain, as h * scale stays within sqrt(K) where h * gain may pass fp32
 template <typename O, bool ROT>
 __device__ __forceinline__ void store_out(const float (&h)[8], const float (&g)[8], float scale, bool on, int l,
                                           int64_t at, int64_t group, void* out, float* out_scales) {
@@ -134,7 +135,7 @@ __device__ __forceinline__ void store_out(const float (&h)[8], const float (&g)[
     } else if (on) {
         float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = value<float, ROT>(h[j], g[j]) * scale;
+        for (int j = 0; j < 8; ++j) v[j] = ROT ? h[j] * scale : h[j] * scale * g[j];
         store8<O>(out, at, v);
     }
 }
