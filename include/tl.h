@@ -394,7 +394,9 @@ TL_API tl_status tl_q4_dequantize(const uint8_t* packed, const uint16_t* scales,
 
 /* Bytes of device workspace tl_q4_gemv needs for this shape (0: none), enough
  * for every type and group size: fp32 sums of up to as many parts of K as
- * activations fit in LDS at a time.  None is needed while M * K <= 16384.
+ * activations fit in LDS at a time.  None is needed while M * K <= 16384, and
+ * never more than 256 MiB or, where that is more, what 64 tokens need (more
+ * tokens are done in turn).
  * Host only; it depends on the compute-unit count of the current device.  -1
  * when the shape is not accepted. */
 TL_API int64_t tl_q4_gemv_workspace_bytes(int64_t M, int64_t N, int64_t K);

@@ -133,6 +133,15 @@ def test_q4_gemv_workspace():
         tl.q4_gemv_workspace_bytes(4, 64, 100)
 
 
+def test_q4_gemv_workspace_does_not_grow_with_the_tokens():
+    """256 MiB, or what 64 tokens need where that is more."""
+    for m, n, k in ((300, 131072, 5120), (4096, 17408, 5120), (4096, 131072, 5120), (1 << 20, 16384, 5120),
+                    (1048561, 16384, 1408), (1 << 24, 1024, 4096), (1 << 12, 1 << 20, 65536), (128, 1 << 24, 4096)):
+        few = tl.q4_gemv_workspace_bytes(64, n, k)
+        need = tl.q4_gemv_workspace_bytes(m, n, k)
+        assert 0 <= need <= max(1 << 28, few)
+
+
 def test_q4_packed_bytes():
     assert tl.q4_packed_bytes(1, 128) == 64 and tl.q4_packed_bytes(17408, 5120) == 17408 * 2560
     for n, k in ((0, 128), (4, 0), (4, 64), (4, 130)):

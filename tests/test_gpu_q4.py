@@ -366,6 +366,48 @@ def test_more_tokens_than_one_launch(gpu):
                   torch.float16)
 
 
+@pytest.mark.parametrize("kind", ["f16", "i8"])
+def test_more_tokens_than_the_workspace_holds(gpu, kind):
+    """A prompt whose parts' sums are done in turn, the last turn of few
+    tokens: tokens at the ends of the turns, nothing written behind the
+    workspace, replays of a graph."""
+    m, n, k = 1601, 17408, 5120
+    g = torch.Generator(device=gpu).manual_seed(4)
+    packed = torch.randint(0, 256, (n, k // 2), generator=g, device=gpu, dtype=torch.uint8)
+    scales = torch.rand(n, k // 128, generator=g, device=gpu).add_(0.5).half()
+    xs = None
+    if kind == "i8":
+        x = torch.randint(-127, 128, (m, k), generator=g, device=gpu, dtype=torch.int8)
+        xs = torch.rand(m, k // 128, generator=g, device=gpu).add_(0.5).div_(4096)
+    else:
+        x = torch.randn(m, k, generator=g, device=gpu).half()
+    need = tl.q4_gemv_workspace_bytes(m, n, k)
+    assert 0 < need <= 1 << 28
+    ws = torch.full((need + 512,), 255, dtype=torch.uint8, device=gpu)
+    y = torch.empty(m, n, device=gpu)
+    tl.q4_gemv(packed, scales, x, xs, out=y, workspace=ws[:need])
+    assert (ws[need:] == 255).all()
+    rows = torch.cat([torch.arange(0, n, 997, device=gpu), torch.tensor([n - 1], device=gpu)])
+    some = [0, 1, 63, 64, 511, 512, 575, 576, 639, 640, 767, 768, 769, 1023, 1024, 1535, 1536, m - 2, m - 1]
+    check_product(y[some][:, rows], x[some], None if xs is None else xs[some],
+                  oracle.q4_unpack(packed[rows].cpu().numpy()), scales[rows].cpu().numpy(), torch.float32)
+    # every token: 128 at a time, another split.  Each result is off by (128 + k/32 + 16) u
+    # = 1.9e-5 of sum |x w|, which is about 0.64 sqrt(k) = 46 deviations of y, the largest
+    # of a batch at least 3: together under 2 * 1.9e-5 * 46 / 3 = 6e-4 of the largest
+    for i in range(0, m, 128):
+        part = tl.q4_gemv(packed, scales, x[i:i + 128], None if xs is None else xs[i:i + 128])
+        assert torch.allclose(part, y[i:i + 128], rtol=1e-3, atol=1e-3 * float(part.abs().max()))
+    want = y.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tl.q4_gemv(packed, scales, x, xs, out=y, workspace=ws[:need])
+    for _ in range(3):
+        y.zero_(), ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+
+
 # ------------------------------------------------------------ together
 
 @pytest.mark.parametrize("rot", [False, True])

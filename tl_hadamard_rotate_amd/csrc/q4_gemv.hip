@@ -533,6 +533,7 @@ __global__ __launch_bounds__(256) void q4_join_kernel(const float* __restrict__ 
 
 constexpr int64_t kLdsCu = 160 * 1024;
 constexpr int64_t kOnePart = 16384;   // M * K that is never cut into parts: its activations fit in LDS
+constexpr int64_t kMaxSums = int64_t(1) << 28;   // bytes of the parts' sums, if 64 tokens' fit in them
 constexpr int kScaleLds = 2560;       // scales of a wave: K = 5120 in groups of 64
 
 // How a call is split; the same for the workspace and the launch.
@@ -620,6 +621,14 @@ Plan q4_plan(int64_t m, int64_t n, int64_t k) {
     return best;
 }
 
+// Tokens of one launch: whole slices, so many that the parts' sums stay within
+// kMaxSums (one slice if it does not fit) and the grid's second dimension ends
+// at 65535
+int64_t launch_tokens(const Plan& p, int64_t n) {
+    const int64_t most = 65535 * 16, fit = p.parts > 1 ? kMaxSums / (4 * p.parts * n) / 64 * 64 : most;
+    return fit < 64 ? 64 : fit < most ? fit : most;
+}
+
 template <int XT, int G, int MT, int V>
 hipError_t launch(Args a, const Plan& p, hipStream_t stream) {
     const auto kernel = q4_gemv_kernel<XT, G, MT, ring_depth<XT>(MT, V == 1), V>;
@@ -648,22 +657,34 @@ hipError_t launch(Args a, const Plan& p, hipStream_t stream) {
 }
 
 template <int XT, int G>
-hipError_t launch_rows(const Args& a, int64_t m, hipStream_t stream) {
-    const Plan p = q4_plan<XT, G>(m, a.n, a.k);
-    if (m == 1) return launch<XT, G, 1, 1>(a, p, stream);   // (the last slice of many may be one token: their plan)
-    switch (p.mt) {
-        case 1: return launch<XT, G, 1, 4>(a, p, stream);
-        case 2: return launch<XT, G, 2, 4>(a, p, stream);
-        case 3: return launch<XT, G, 3, 4>(a, p, stream);
-        default: return launch<XT, G, 4, 4>(a, p, stream);
+hipError_t launch_rows(const Args& all, int64_t m, hipStream_t stream) {
+    const Plan p = q4_plan<XT, G>(m, all.n, all.k);
+    const int64_t step = launch_tokens(p, all.n), yb = all.y_dtype == TL_F32 ? 4 : 2;
+    // (the last launch of several may be of few tokens, or one: their plan)
+    for (int64_t m0 = 0; m0 < m; m0 += step) {
+        Args a = all;
+        a.x += m0 * all.k * (chunk_bytes<XT>() / 128);
+        if (XT == TL_I8) a.xs += m0 * (all.k / 128);
+        a.y = static_cast<uint8_t*>(all.y) + m0 * all.n * yb;
+        a.m = int(m - m0 < step ? m - m0 : step);
+        const hipError_t e = m == 1        ? launch<XT, G, 1, 1>(a, p, stream)
+                             : p.mt == 1 ? launch<XT, G, 1, 4>(a, p, stream)
+                             : p.mt == 2 ? launch<XT, G, 2, 4>(a, p, stream)
+                             : p.mt == 3 ? launch<XT, G, 3, 4>(a, p, stream)
+                                         : launch<XT, G, 4, 4>(a, p, stream);
+        if (e != hipSuccess) return e;
     }
+    return hipSuccess;
 }
 
 }  // namespace
 
 int64_t q4_gemv_need(int64_t m, int64_t n, int64_t k, int x_dtype, int group) {
     if (m * k <= kOnePart) return 0;
-    const auto bytes = [&](const Plan& p) { return p.parts > 1 ? p.parts * sums_stride(m * n) * 4 : int64_t(0); };
+    const auto bytes = [&](const Plan& p) {
+        const int64_t step = launch_tokens(p, n);
+        return p.parts > 1 ? p.parts * sums_stride((m < step ? m : step) * n) * 4 : int64_t(0);
+    };
 #define TL_Q4_NEED(XT)                                      \
     bytes(group == 32   ? q4_plan<XT, 32>(m, n, k)          \
           : group == 64 ? q4_plan<XT, 64>(m, n, k)          \
@@ -684,24 +705,15 @@ int64_t q4_gemv_workspace_bytes(int64_t m, int64_t n, int64_t k) {
 hipError_t launch_q4_gemv(const uint8_t* packed, const uint16_t* scales, int group, const void* x,
                           int x_dtype, const float* x_scales, int64_t m, int64_t n, int64_t k, void* y,
                           int y_dtype, void* ws, hipStream_t stream) {
-    // a grid's second dimension ends at 65535: at most 65535 * 16 tokens a launch
-    constexpr int64_t kMaxTokens = 65535 * 16;
-    const int64_t xb = x_dtype == TL_I8 ? 1 : 2, yb = y_dtype == TL_F32 ? 4 : 2;
-    for (int64_t m0 = 0; m0 < m; m0 += kMaxTokens) {
-        const int64_t mt = m - m0 < kMaxTokens ? m - m0 : kMaxTokens;
-        const Args a = {packed, scales, static_cast<const uint8_t*>(x) + m0 * k * xb,
-                        x_scales ? x_scales + m0 * (k / 128) : nullptr, static_cast<uint8_t*>(y) + m0 * n * yb,
-                        static_cast<float*>(ws), n, k, int(mt), y_dtype, 0, 0, 0, 0, 0, 0, 0, 0};
+    const Args a = {packed, scales, static_cast<const uint8_t*>(x), x_scales, y, static_cast<float*>(ws),
+                    n, k, 0, y_dtype, 0, 0, 0, 0, 0, 0, 0, 0};
 #define TL_Q4_GROUP(XT)                                                \
     (group == 32   ? launch_rows<XT, 32>(a, m, stream)                 \
      : group == 64 ? launch_rows<XT, 64>(a, m, stream)                 \
                    : launch_rows<XT, 128>(a, m, stream))
-        const hipError_t e = x_dtype == TL_I8    ? TL_Q4_GROUP(TL_I8)
-                             : x_dtype == TL_F16 ? TL_Q4_GROUP(TL_F16)
-                                                 : TL_Q4_GROUP(TL_BF16);
-        if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
+    return x_dtype == TL_I8    ? TL_Q4_GROUP(TL_I8)
+           : x_dtype == TL_F16 ? TL_Q4_GROUP(TL_F16)
+                               : TL_Q4_GROUP(TL_BF16);
 }
 
 }  // namespace tl
