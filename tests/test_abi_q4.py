@@ -1,6 +1,8 @@
 """Host-side refusals of the norm and the 4-bit calls (no GPU needed): every
 call here fails validation on made-up addresses, so nothing touches a device."""
 import math
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -170,3 +172,23 @@ def test_binding_refuses_host_tensors_and_wrong_types():
             call()
     with pytest.raises(TypeError):
         tl.q4_gemv(packed.int(), scales, x)
+
+
+def test_package_imports_on_a_torch_without_gpu_support():
+    """Such a torch lacks the look-ups of device and stream; the package still
+    imports, and its calls refuse host tensors as elsewhere."""
+    program = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import tl_hadamard_rotate_amd as tl
+try:
+    tl.rms_norm(torch.zeros(1, 1024), torch.ones(1024), 1e-6)
+except ValueError as e:
+    print("refused:", e)
+"""
+    run = subprocess.run([sys.executable, "-c", program], capture_output=True, text=True, timeout=100,
+                         cwd=tl.__file__.rsplit("/", 2)[0])
+    assert run.returncode == 0, run.stderr
+    assert run.stdout.startswith("refused:")

@@ -321,8 +321,9 @@ def linear(packed, scales, fmt, x, signs, out_dtype=torch.float32, out=None,
 
 _REAL = {torch.float32: TL_F32, torch.float16: TL_F16, torch.bfloat16: TL_BF16}
 _I8, _U8, _F16, _F32 = torch.int8, torch.uint8, torch.float16, torch.float32
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_get_device = torch._C._cuda_getDevice
+# (a torch without GPU support has neither; the calls refuse its tensors before they ask)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
 
 # The calls below take microseconds, so their checks are written out: each
 # tensor's type, shape, device and contiguity in one condition, and only a
