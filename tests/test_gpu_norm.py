@@ -238,6 +238,30 @@ def test_gains_within_the_stated_range(gpu, kind, gf, xf, eps):
         i8_check(*tl.rms_norm_i8(x, gain, eps, signs=s), want, y, 2048, None if rot else h * host(gain))
 
 
+@pytest.mark.parametrize("k", [5120, 17408, 36864])
+@pytest.mark.parametrize("rot", [False, True])
+def test_rows_alone_are_the_same_bits(gpu, k, rot):
+    """A row's outputs, sum, codes and scales do not depend on the rows beside
+    it or on their number."""
+    x, r, gain, s = make(9, k, "bf16", gpu, rot=rot)
+    many = (*tl.rms_norm(x, gain, EPS, residual=r, signs=s), *tl.rms_norm_i8(x, gain, EPS, residual=r, signs=s))
+    for i in (0, 4, 8):
+        a, b = x[i:i + 1].clone(), r[i:i + 1].clone()
+        one = (*tl.rms_norm(a, gain, EPS, residual=b, signs=s), *tl.rms_norm_i8(a, gain, EPS, residual=b, signs=s))
+        for got, want in zip(one, many):
+            assert torch.equal(got, want[i:i + 1])
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("m,k", [(2, 24576), (2, 25600), (1, 36864)])
+def test_norm_i8_rotated_long_rows(gpu, m, k, kind):
+    x, r, gain, s = make(m, k, kind, gpu, seed=m + k, rot=True)
+    q, scales, total = tl.rms_norm_i8(x, gain, EPS, residual=r, signs=s)
+    h, y, want = reference(x, r, gain, s, kind)
+    assert np.array_equal(host(total), h)
+    i8_check(q, scales, want, y, k)
+
+
 def test_large_and_tiny_values(gpu):
     """binary16 rows near its largest and smallest numbers, eps of the smallest
     normal number."""
@@ -368,6 +392,21 @@ def test_offsets_past_32_bits(gpu):
     ends = tl.rms_norm(x[[0, 1, -1]].contiguous(), gain, EPS)
     assert torch.equal(y[[0, 1, -1]], ends)
     assert bool((y[1:-1] == ends[1, 0]).all())
+
+
+@pytest.mark.parametrize("k,rot", [(24, False), (128, False), (1024, True)])
+def test_more_rows_than_workgroups(gpu, k, rot):
+    """Rows past 2^20 are a workgroup's second: every row repeats one of 1021,
+    and so do its outputs."""
+    m, some = (1 << 20) + 5, 1021
+    x, _, gain, s = make(some, k, "f16", gpu, residual=False, rot=rot)
+    rows = torch.arange(m, device=gpu) % some
+    want = tl.rms_norm(x, gain, EPS, signs=s)
+    assert torch.equal(tl.rms_norm(x[rows], gain, EPS, signs=s), want[rows])
+    if k % 128 == 0:
+        want = tl.rms_norm_i8(x, gain, EPS, signs=s)
+        got = tl.rms_norm_i8(x[rows], gain, EPS, signs=s)
+        assert torch.equal(got[0], want[0][rows]) and torch.equal(got[1], want[1][rows])
 
 
 def test_norm_feeds_the_ternary_product(gpu):

@@ -170,6 +170,13 @@ def test_product_at_projection_sizes(gpu, m, n, k, kind):
 
 
 @pytest.mark.parametrize("kind", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("m,group", [(1, 128), (5, 64), (20, 32), (64, 128)])
+def test_product_of_the_longest_rows(gpu, m, group, kind):
+    x, xs, packed, scales, codes, sc = make(m, 19, 1 << 20, kind, group, gpu, seed=m)
+    check_product(tl.q4_gemv(packed, scales, x, x_scales=xs), x, xs, codes, sc, torch.float32)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16", "i8"])
 def test_one_hot_activations_give_the_weights(gpu, kind):
     """y of a one-hot token is one column of the weights, exactly; every token
     and column position is tried."""
