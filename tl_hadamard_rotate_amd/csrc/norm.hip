@@ -24,8 +24,10 @@
 // Bound by memory for many rows, by the launch for few.  Outputs are stored
 // past the caches' replacement order: 4096 x 5120 bfloat16 rows with a residual
 // (168 MB) 27.8 us, 6.0 TB/s, against 39 with ordinary stores; as 8-bit codes
-// 38-40 us (147 MB; the codes' instructions).  2048 rotated binary16 rows (84
-// MB) 18.8 us, 4.5 TB/s: the rotation's 10 levels.  One row of 5120 4.6 us.
+// (147 MB) 28.7 us with gains around 1, 38.6 with a gain of ones, whose quotients
+// lie near ties more often.  2048 rotated binary16 rows (84 MB) 18.9 us, 4.5 TB/s:
+// the rotation's 10 levels; 4096 of them as 8-bit codes 57 us, the rotation's and
+// the codes' instructions.  One row of 5120 4.6-5.3 us, 16 to 8 bits 5.7.
 #include <type_traits>
 
 #include "elem.h"

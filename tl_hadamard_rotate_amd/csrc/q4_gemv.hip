@@ -15,7 +15,8 @@
 // Decode.  A nibble n of two's complement is code + 8 = n ^ 8.  For 16-bit
 // activations, (w & 0x000F000F) ^ 0x64086408 is the binary16 pair 1024 + (code
 // + 8) and (w & 0x00F000F0) ^ 0x64806480 the pair 1024 + 16 (code + 8); one
-// packed add or fma makes them the codes, exactly.  (Feeding code + 8 as a
+// packed add or fma makes them the codes, exactly: the known way to widen
+// interleaved 4-bit integers through the mantissa of 1024 + n.  (Feeding code + 8 as a
 // subnormal pattern and taking the 8 off the sums saves those, but then rows
 // of small codes carry the rounding errors of 8 * sum x.)  For 8 bits, w &
 // 0xF0F0F0F0 and (w << 4) & 0xF0F0F0F0 are four signed bytes 16 * code each;
@@ -44,13 +45,17 @@
 // that 8 tokens at one place lie on different banks.
 //
 // Bound.  One token: the weights' bytes from HBM (131072 x 5120 in groups of 128,
-// 346 MB, 60.9 us, 5.7 TB/s; a plain read of as much 55 us).  Few tokens: besides
+// 346 MB, 60.6 us, 5.7 TB/s; a plain read of as much 55 us).  Few tokens: besides
 // that the staging of a part's activations, which every workgroup does before its
 // first product, and the second kernel (5120 x 17408 by 8 bfloat16 tokens, 47 MB,
-// 19.0 us of which 2.7 the second kernel).  From some 40 tokens on the vector
+// 19.1 us; traced one by one, 21.5 and 4.1).  From some 40 tokens on the
 // instructions: decoding, and one fma for each group, token and row (32003 x 5120
-// in groups of 32 by 45 tokens, 43 us: 18 us of vector and 6 of matrix
-// instructions on each SIMD, 6 in the second kernel).
+// in groups of 32 by 45 tokens, 42.7 us, traced 40.2 and 5.8: counters give 18.6
+// us of vector and 6.3 of matrix instructions on each SIMD and 13.1 us of LDS
+// reads on each compute unit, 6.5 of them bank conflicts, which two waves a SIMD
+// overlap little).  Narrow matrices from 17 tokens on: the split leaves most
+// compute units idle (1024 x 5120 by 20 8-bit tokens 12.4 us in 16 workgroups; by
+// 16 tokens 7.5 us).
 #include <cmath>
 
 #include "elem.h"
@@ -534,7 +539,10 @@ __global__ __launch_bounds__(256) void q4_join_kernel(const float* __restrict__ 
 constexpr int64_t kLdsCu = 160 * 1024;
 constexpr int64_t kOnePart = 16384;   // M * K that is never cut into parts: its activations fit in LDS
 constexpr int64_t kMaxSums = int64_t(1) << 28;   // bytes of the parts' sums, if 64 tokens' fit in them
-constexpr int kScaleLds = 2560;       // scales of a wave: K = 5120 in groups of 64
+// Scales of a wave in LDS, 20 KB of a workgroup's 80.  Longer runs come in segments,
+// each of which waits for the weights on the way; that shows nowhere (17408 rows in
+// groups of 64, one token: K = 5120 3.47 TB/s, 5248 3.42, 5632 3.50, 6144 3.73)
+constexpr int kScaleLds = 2560;
 
 // How a call is split; the same for the workspace and the launch.
 struct Plan {
@@ -543,13 +551,18 @@ struct Plan {
 };
 
 // Chunks of weights a wave has on the way: 2 or 4.  64 tokens: 4 spill (17408 x
-// 5120 by binary16 28.8 us with 2, 30.1 with 1).  Up to 16 tokens 2 are as good or
-// better (131072 x 5120 of one token 62.0 us, 64.2 with 4; 6144 x 5120 of 16
-// binary16 tokens 11.4 and 12.3) but for several 8-bit ones (10240 x 4096 of 4 9.0
-// us, 8.05 with 4); 32 and 48 tokens: 32003 x 5120 of 20 binary16 27.7 us, 26.3
-// with 4.  (Two row tiles of a wave that share the activations' reads are slower
-// from 8 to 64 tokens on most shapes: 5120 x 17408 by 20 tokens 22.8 us, 18.1
-// with one.)
+// 5120 by binary16 28.8 us with 2, 30.1 with 1; for bfloat16 in groups of 128 2 do
+// as well, 20 bytes a lane).  Up to 16 tokens, 2 against 4, means over six shapes from
+// 1024 x 5120 to 32003 x 5120 and 5120 x 17408 at 1, 4 and 16 tokens: binary16 in
+// groups of 128 2 to 3 % shorter (131072 x 5120 of one token 62.0 us, 64.2 with 4),
+// in groups of 64 and 32 0 to 2 % longer (the worst: 32003 x 5120 of one token 21.4
+// us, 19.4 with 4; the best: 17408 x 5120 of 4 16.7 and 17.8); bfloat16 1 to 5 %
+// shorter, but for one token in groups of 128 (1 % longer); 8 bits: one token 4 to
+// 6 % shorter, several 1 to 5 % longer (10240 x 4096 of 4 9.5 us, 8.6 with 4), in
+// groups of 32 1 to 3 % shorter.  The rule goes by the types' means.  32 and 48
+// tokens: 32003 x 5120 of 20 binary16 27.7 us, 26.3 with 4.  (Two row tiles of a
+// wave that share the activations' reads are slower from 8 to 64 tokens on most
+// shapes: 5120 x 17408 by 20 tokens 22.8 us, 18.1 with one.)
 template <int XT>
 constexpr int ring_depth(int mt, bool one_token) {
     return mt == 4 || (mt == 1 && (one_token || XT != TL_I8)) ? 2 : 4;

@@ -15,7 +15,9 @@
 // Bound by memory: a lane reads 8 weights (32 or 16 bytes) and writes 4 bytes, a
 // group's maximum is exchanged among 4 to 16 neighbouring lanes, nothing goes
 // through LDS.  17408 x 5120 fp32 weights to 4 bits and back to binary16, 627
-// MB, take 110 us in both launches together, 5.7 TB/s.
+// MB, take 110 us in both launches together, 5.7 TB/s.  With the rotation a lane
+// holds 16 neighbouring weights, so its loads lie 64 bytes from the next lane's:
+// the way there takes 125 us instead of 71-82 (402 MB, 3.2 TB/s).
 #include "elem.h"
 #include "tl_internal.h"
 
