@@ -343,8 +343,8 @@ TL_API tl_status tl_quantize(const float* w, const int8_t* signs, int64_t N, int
  * a NaN, are 0.  With the rotation or TL_I8 the products h * gain come first and
  * are fp32 too: where they (with the rotation, their sums over a block) pass
  * 3.4e38 the outputs are infinite or NaN, and products below 2^-126 lose bits.
- * Gains from 2^-50 to 2^50 reach neither in a row whose squares fit.  Bitwise
- * reproducible from call to call.
+ * Gains from 2^-50 to 2^50 never reach the one in a row whose squares fit, and
+ * the other only where |h| < 2^-76.  Bitwise reproducible from call to call.
  * Requires 1 <= M <= 2^24, 8 <= K <= TL_MAX_K, K % 8 == 0 (K % 1024 == 0 with
  * signs, K % 128 == 0 with TL_I8), M * K <= 2^36; eps a positive normal fp32
  * number (TL_ERR_VALUE); every pointer 16-byte aligned, out_scales 4-byte.  sum_out may equal x
