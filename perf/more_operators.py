@@ -51,7 +51,7 @@ def listed():
         # down projection of thirteen decoding sequences
         {"name": "product batch down", "op": "product", "m": 13, "n": 5120, "k": 17408, "out": "bf16"},
         # scoring a text: the head of every position, a vocabulary that divides by nothing
-        {"name": "product ragged head", "op": "product", "m": 1000, "n": 32003, "k": 5120, "out": "f32"},
+        {"name": "product ragged head", "op": "product", "m": 1000, "n": 32003, "k": 5120, "out": "f16"},
         # gate/up projection of a prompt
         {"name": "product prompt gate", "op": "product", "m": 4096, "n": 17408, "k": 5120, "out": "bf16"},
         # one sequence about to draw its next token
