@@ -426,6 +426,92 @@ TL_API tl_status tl_q4_gemv(const uint8_t* packed, const uint16_t* scales, int32
                             int64_t N, int64_t K, void* y, int32_t y_dtype, void* workspace,
                             int64_t workspace_bytes, hipStream_t stream);
 
+/* ---- the model's two ends: rows of the embedding, the head's product in 8-bit
+ * floating point, its logits made ready for drawing a token ---- */
+
+/* 8-bit floating point rows ("f8"): e4m3 codes (1 sign, 4 exponent, 3 mantissa
+ * bits, bias 7; no infinity, 0x7F and 0xFF are NaN, the largest number 448) and
+ * one scale per 128 consecutive values of a row, a power of two 2^(b - 127) held
+ * as its biased exponent b in a byte (0xFF: NaN); value (r, k) = code *
+ * scale[r, k / 128].  codes: uint8 [M, K]; scales: uint8 [M, K/128].  8.0625
+ * bits per value.  Weights and activations have the same form; scales that are
+ * powers of two are what the matrix cores apply by themselves. */
+
+/* Round rows to f8: with a = max |x| over the finite values of a group,
+ *   scale = the smallest power of two from 2^-127 up with a <= 448 * scale,
+ *   code = the e4m3 number nearest to x / scale, ties to even;
+ * infinities and NaN become the code 0x7F.  Codes and scales follow exactly
+ * from x.  x: [M, K] of x_dtype (TL_F32, TL_F16 or TL_BF16).  Requires
+ * 1 <= M <= 2^24, 128 <= K <= TL_MAX_K, K % 128 == 0, M * K <= 2^36; every
+ * pointer 16-byte aligned; codes and scales overlap nothing else. */
+TL_API tl_status tl_f8_quantize(const void* x, int64_t M, int64_t K, int32_t x_dtype, uint8_t* codes,
+                                uint8_t* scales, hipStream_t stream);
+
+/* The values of f8 rows, rounded to nearest even in out_dtype (exact in TL_F32,
+ * and in TL_BF16 from 2^-126 up).  out: [M, K]; rules as tl_f8_quantize; out
+ * overlaps neither input. */
+TL_API tl_status tl_f8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K, void* out,
+                                  int32_t out_dtype, hipStream_t stream);
+
+/* Bytes of device workspace tl_f8_gemm needs for this shape (0: none), enough
+ * for every output type.  Host only; it depends on the compute-unit count of
+ * the current device.  -1 when the shape is not accepted. */
+TL_API int64_t tl_f8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* Product of f8 rows with f8 weights, one token or a prompt:
+ *   y[m, n] = sum_k x[m, k] * w[n, k]
+ * codes, scales: the weights, [N, K] and [N, K/128]; x, x_scales: [M, K] and
+ * [M, K/128]; y: [M, N] of y_dtype (TL_F32, TL_F16 or TL_BF16, rounded once to
+ * nearest even).  Requires 1 <= M, N <= 2^24, 128 <= K <= TL_MAX_K, K % 128 ==
+ * 0, M * K, N * K and M * N <= 2^36.  workspace: tl_f8_gemm_workspace_bytes(M,
+ * N, K) bytes (may be NULL when that is 0; TL_ERR_WORKSPACE); its contents on
+ * entry do not matter, and calls that may run at the same time need separate
+ * ones.  Every pointer 16-byte aligned; y and workspace overlap nothing else. */
+TL_API tl_status tl_f8_gemm(const uint8_t* codes, const uint8_t* scales, const uint8_t* x,
+                            const uint8_t* x_scales, int64_t M, int64_t N, int64_t K, void* y, int32_t y_dtype,
+                            void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* Embedding lookup in a q4 or an f8 table of N rows, times a factor:
+ *   out[m, k] = w[ids[m], k] * factor
+ * ids: int32 [M]; an id outside 0 .. N - 1 (padding) gives a row of zeros, any
+ * may occur more than once.  The product is fp32, then rounded to nearest even
+ * in out_dtype (TL_F32, TL_F16 or TL_BF16).  out: [M, K].  A q4 table must have
+ * been rounded without the rotation.  Requires 1 <= M, N <= 2^24, 128 <= K <=
+ * TL_MAX_K, K % 128 == 0, M * K and N * K <= 2^36; factor finite (TL_ERR_VALUE);
+ * group as tl_q4_quantize; every pointer 16-byte aligned, ids 4-byte; out
+ * overlaps nothing else. */
+TL_API tl_status tl_q4_rows(const uint8_t* packed, const uint16_t* scales, int32_t group, const int32_t* ids,
+                            int64_t M, int64_t N, int64_t K, float factor, void* out, int32_t out_dtype,
+                            hipStream_t stream);
+TL_API tl_status tl_f8_rows(const uint8_t* codes, const uint8_t* scales, const int32_t* ids, int64_t M,
+                            int64_t N, int64_t K, float factor, void* out, int32_t out_dtype, hipStream_t stream);
+
+/* Penalties for repeated tokens, biases and a grammar's mask on logits.  For
+ * row m (a sequence) and token v, in fp32, in this order:
+ *   x = logits[m, v]
+ *   v among the row's history:  x = x > 0 ? x / repetition[m] : x * repetition[m]
+ *   v n > 0 times in it after the prompt:  x = x - frequency[m] * n - presence[m]
+ *   v named by bias_ids[m, :]:  x = x + the bias_values entry of its last place there
+ *   bit v of the row's mask is 0:  x = -infinity (whatever x was)
+ * and out[m, v] = x, rounded to nearest even in out_dtype.  A row whose mask
+ * allows nothing becomes -infinity throughout.
+ * logits: [M, V] of dtype, out: [M, V] of out_dtype (each TL_F32, TL_F16 or
+ * TL_BF16).  history: int32 [M, H] or NULL; the row's is its first
+ * history_lens[m] ids (NULL: H; taken within 0 .. H), of which the first
+ * prompt_lens[m] (NULL: 0) are the prompt's.  repetition, presence, frequency:
+ * fp32 [M] or NULL (1, 0, 0).  These five need a history (TL_ERR_NULL).
+ * bias_ids: int32 [M, B] and bias_values: fp32 [M, B], both or neither.  Ids
+ * outside 0 .. V - 1 are passed over (padding).  mask: uint32 [M, ceil(V / 32)]
+ * or NULL; bit v % 32 of word v / 32, 1 = allowed.  Requires 1 <= M, V <= 2^24,
+ * 0 <= H, B <= 2^24, M * V, M * H and M * B <= 2^36; logits and out 16-byte
+ * aligned, the others 4-byte.  out may equal logits when the types agree (in
+ * place) and overlaps nothing else. */
+TL_API tl_status tl_adjust_logits(const void* logits, int64_t M, int64_t V, int32_t dtype, const int32_t* history,
+                                  int64_t H, const int32_t* history_lens, const int32_t* prompt_lens,
+                                  const float* repetition, const float* presence, const float* frequency,
+                                  const int32_t* bias_ids, const float* bias_values, int64_t B,
+                                  const uint32_t* mask, void* out, int32_t out_dtype, hipStream_t stream);
+
 /* Static name of a status code ("TL_OK", ...). */
 TL_API const char* tl_status_str(tl_status status);
 

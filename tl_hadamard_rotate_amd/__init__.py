@@ -78,6 +78,13 @@ def lib() -> ctypes.CDLL:
             "tl_q4_dequantize": (i32, [p, p, i64, i64, i32, p, i32, p]),
             "tl_q4_gemv_workspace_bytes": (i64, [i64, i64, i64]),
             "tl_q4_gemv": (i32, [p, p, i32, p, i32, p, i64, i64, i64, p, i32, p, i64, p]),
+            "tl_f8_quantize": (i32, [p, i64, i64, i32, p, p, p]),
+            "tl_f8_dequantize": (i32, [p, p, i64, i64, p, i32, p]),
+            "tl_f8_gemm_workspace_bytes": (i64, [i64, i64, i64]),
+            "tl_f8_gemm": (i32, [p, p, p, p, i64, i64, i64, p, i32, p, i64, p]),
+            "tl_q4_rows": (i32, [p, p, i32, p, i64, i64, i64, f32, p, i32, p]),
+            "tl_f8_rows": (i32, [p, p, p, i64, i64, i64, f32, p, i32, p]),
+            "tl_adjust_logits": (i32, [p, i64, i64, i32, p, i64, p, p, p, p, p, p, p, i64, p, p, i32, p]),
             "tl_status_str": (ctypes.c_char_p, [i32]),
             "tl_last_error": (ctypes.c_char_p, []),
         }
@@ -603,6 +610,217 @@ class Q4Linear:
         return q4_gemv(self.packed, self.scales, x, x_scales, out_dtype)
 
     __call__ = forward
+
+
+_F8, _E8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+_I32 = torch.int32
+
+
+def f8_quantize(x, codes=None, scales=None):
+    """Rows x [M, K] (float32, float16 or bfloat16; weights or activations) to
+    8-bit floating point with a power-of-two scale per 128: returns (codes
+    float8_e4m3fn [M, K], scales float8_e8m0fnu [M, K/128]); value = code * scale."""
+    dt, shape, index = _rows(x, "x")
+    m, k = shape
+    if k % GROUP:
+        raise ValueError("K must be a multiple of 128")
+    groups = (m, k // GROUP)
+    if codes is None:
+        codes = torch.empty(shape, dtype=_F8, device=x.device)
+    elif not (isinstance(codes, torch.Tensor) and codes.dtype is _F8 and codes.shape == shape and
+              codes.get_device() == index and codes.is_contiguous()):
+        _refuse(codes, "codes", _F8, shape, index)
+    if scales is None:
+        scales = torch.empty(groups, dtype=_E8, device=x.device)
+    elif not (isinstance(scales, torch.Tensor) and scales.dtype is _E8 and scales.shape == groups and
+              scales.get_device() == index and scales.is_contiguous()):
+        _refuse(scales, "scales", _E8, groups, index)
+    _call("tl_f8_quantize", index, (x.data_ptr(), m, k, dt, codes.data_ptr(), scales.data_ptr()))
+    return codes, scales
+
+
+def _f8_shape(codes, scales, what="codes"):
+    """(rows, K, device index) of 8-bit floating point rows and their scales."""
+    if not (isinstance(codes, torch.Tensor) and isinstance(scales, torch.Tensor)):
+        raise TypeError(f"{what} and their scales must be torch.Tensors")
+    if codes.dtype is not _F8 or scales.dtype is not _E8:
+        raise TypeError(f"{what} must be float8_e4m3fn and their scales float8_e8m0fnu")
+    index = codes.get_device()
+    if index < 0 or scales.get_device() != index:
+        raise ValueError(f"{what} and their scales must be device tensors, on the same device")
+    cs, ss = codes.shape, scales.shape
+    if len(cs) != 2 or len(ss) != 2 or not codes.is_contiguous() or not scales.is_contiguous():
+        raise ValueError(f"{what} and their scales must be contiguous with 2 dims")
+    n, k = cs
+    if ss[0] != n or k % GROUP or ss[1] * GROUP != k:
+        raise ValueError(f"{what} {tuple(cs)} and their scales {tuple(ss)} must be "
+                         "[rows, K] and [rows, K/128], K a multiple of 128")
+    return n, k, index
+
+
+def f8_dequantize(codes, scales, out_dtype=torch.float16, out=None) -> torch.Tensor:
+    """The values [M, K] that 8-bit floating point rows stand for."""
+    m, k, index = _f8_shape(codes, scales)
+    dt = _out_type(out_dtype)
+    if out is None:
+        out = torch.empty((m, k), dtype=out_dtype, device=codes.device)
+    elif not (isinstance(out, torch.Tensor) and out.dtype is out_dtype and out.shape == (m, k) and
+              out.get_device() == index and out.is_contiguous()):
+        _refuse(out, "out", out_dtype, (m, k), index)
+    _call("tl_f8_dequantize", index, (codes.data_ptr(), scales.data_ptr(), m, k, out.data_ptr(), dt))
+    return out
+
+
+def f8_gemm_workspace_bytes(m: int, n: int, k: int) -> int:
+    """Device workspace bytes tl_f8_gemm needs (0: none)."""
+    b = int(lib().tl_f8_gemm_workspace_bytes(m, n, k))
+    if b < 0:
+        raise TLError("tl_f8_gemm_workspace_bytes", 2)
+    return b
+
+
+@functools.lru_cache(maxsize=4096)
+def _f8_workspace(index: int, m: int, n: int, k: int) -> int:
+    """f8_gemm_workspace_bytes of a shape, asked once a device."""
+    with torch.cuda.device(index):
+        return f8_gemm_workspace_bytes(m, n, k)
+
+
+def f8_gemm(codes, scales, x, x_scales, out_dtype=torch.float32, out=None, workspace=None) -> torch.Tensor:
+    """y[M, N] = x . w^T with both in 8-bit floating point (``f8_quantize``):
+    weights codes [N, K] and scales, activations x [M, K] and x_scales, one
+    token or a prompt.  ``workspace`` (uint8, at least
+    ``f8_gemm_workspace_bytes``) is taken from torch's allocator when not given."""
+    n, k, index = _f8_shape(codes, scales)
+    m, kx, at = _f8_shape(x, x_scales, "x")
+    if kx != k or at != index:
+        raise ValueError(f"x must be [M, {k}] on {codes.device}, got {tuple(x.shape)} on {x.device}")
+    yd = _out_type(out_dtype)
+    if out is None:
+        out = torch.empty((m, n), dtype=out_dtype, device=codes.device)
+    elif not (isinstance(out, torch.Tensor) and out.dtype is out_dtype and out.shape == (m, n) and
+              out.get_device() == index and out.is_contiguous()):
+        _refuse(out, "out", out_dtype, (m, n), index)
+    wp, wb = None, 0
+    if workspace is not None:
+        if not (isinstance(workspace, torch.Tensor) and workspace.dtype is _U8 and workspace.dim() == 1 and
+                workspace.get_device() == index and workspace.is_contiguous()):
+            _refuse(workspace, "workspace", _U8, ("bytes",), index)
+        wp, wb = workspace.data_ptr(), workspace.numel()
+    else:
+        wb = _f8_workspace(index, m, n, k)
+        if wb:
+            workspace = torch.empty(wb, dtype=_U8, device=codes.device)
+            wp = workspace.data_ptr()
+    _call("tl_f8_gemm", index, (codes.data_ptr(), scales.data_ptr(), x.data_ptr(), x_scales.data_ptr(), m, n, k,
+                                out.data_ptr(), yd, wp, wb))
+    return out
+
+
+class F8Linear:
+    """A linear layer with weights in 8-bit floating point, for the matrices
+    beside the ternary ones; ``forward`` rounds its input rows to the same form."""
+
+    def __init__(self, codes, scales):
+        self.codes, self.scales = codes, scales
+
+    def forward(self, x: torch.Tensor, out_dtype=torch.float32) -> torch.Tensor:
+        return f8_gemm(self.codes, self.scales, *f8_quantize(x), out_dtype)
+
+    __call__ = forward
+
+
+def _lookup(call, n, k, index, head, ids, factor, out_dtype, out, device):
+    dt = _out_type(out_dtype)
+    if not isinstance(ids, torch.Tensor):
+        raise TypeError("ids must be a torch.Tensor")
+    m = ids.numel()
+    if ids.dtype is not _I32 or ids.dim() != 1 or ids.get_device() != index or not ids.is_contiguous():
+        _refuse(ids, "ids", _I32, ("M",), index)
+    if out is None:
+        out = torch.empty((m, k), dtype=out_dtype, device=device)
+    elif not (isinstance(out, torch.Tensor) and out.dtype is out_dtype and out.shape == (m, k) and
+              out.get_device() == index and out.is_contiguous()):
+        _refuse(out, "out", out_dtype, (m, k), index)
+    _call(call, index, (*head, ids.data_ptr(), m, n, k, factor, out.data_ptr(), dt))
+    return out
+
+
+def q4_rows(packed, scales, ids, factor=1.0, out_dtype=torch.float16, out=None) -> torch.Tensor:
+    """Embedding lookup in a table of 4-bit weights (``q4_quantize`` without
+    signs): row ids[m] times ``factor`` for each of ids (int32 [M]), zeros for an
+    id outside the table."""
+    n, k, group, index = _q4_shape(packed, scales)
+    return _lookup("tl_q4_rows", n, k, index, (packed.data_ptr(), scales.data_ptr(), group), ids, factor, out_dtype,
+                   out, packed.device)
+
+
+def f8_rows(codes, scales, ids, factor=1.0, out_dtype=torch.float16, out=None) -> torch.Tensor:
+    """``q4_rows`` in a table of 8-bit floating point (``f8_quantize``)."""
+    n, k, index = _f8_shape(codes, scales)
+    return _lookup("tl_f8_rows", n, k, index, (codes.data_ptr(), scales.data_ptr()), ids, factor, out_dtype, out,
+                   codes.device)
+
+
+def adjust_logits(logits, history=None, history_lens=None, prompt_lens=None, repetition=None, presence=None,
+                  frequency=None, bias_ids=None, bias_values=None, mask=None, out_dtype=None, out=None):
+    """Penalties for repeated tokens, biases and a grammar's mask on logits [M, V]
+    (float32, float16 or bfloat16), in this order (see tl_adjust_logits):
+    history int32 [M, H], of which a row's first ``history_lens`` ids count and
+    its first ``prompt_lens`` are the prompt's (int32 [M]); repetition, presence
+    and frequency float32 [M]; bias_ids int32 and bias_values float32 [M, B], the
+    last entry of a token counts; mask int32 [M, ceil(V/32)], bit 1 = allowed.
+    Ids outside the vocabulary are padding.  ``out`` may be logits itself."""
+    dt, shape, index = _rows(logits, "logits")
+    m, v = shape
+    od = dt if out_dtype is None else _out_type(out_dtype)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype or logits.dtype, device=logits.device)
+    elif not (isinstance(out, torch.Tensor) and out.dtype is (out_dtype or logits.dtype) and out.shape == shape and
+              out.get_device() == index and out.is_contiguous()):
+        _refuse(out, "out", out_dtype or logits.dtype, shape, index)
+    row = (m,)
+    h = b = 0
+    hp = ip = vp = mp = None
+    each = []
+    if history is not None:
+        if not (isinstance(history, torch.Tensor) and history.dtype is _I32 and history.dim() == 2 and
+                history.shape[0] == m and history.get_device() == index and history.is_contiguous()):
+            _refuse(history, "history", _I32, (m, "H"), index)
+        h = history.shape[1]
+        hp = history.data_ptr()
+    for name, t, dtype in (("history_lens", history_lens, _I32), ("prompt_lens", prompt_lens, _I32),
+                           ("repetition", repetition, _F32), ("presence", presence, _F32),
+                           ("frequency", frequency, _F32)):
+        if t is None:
+            each.append(None)
+            continue
+        if history is None:
+            raise ValueError(f"{name} needs a history")
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == row and t.get_device() == index and
+                t.is_contiguous()):
+            _refuse(t, name, dtype, row, index)
+        each.append(t.data_ptr() if h else None)    # (an empty history has no address)
+    if bias_ids is not None or bias_values is not None:
+        if not (isinstance(bias_ids, torch.Tensor) and bias_ids.dtype is _I32 and bias_ids.dim() == 2 and
+                bias_ids.shape[0] == m and bias_ids.get_device() == index and bias_ids.is_contiguous()):
+            _refuse(bias_ids, "bias_ids", _I32, (m, "B"), index)
+        if not (isinstance(bias_values, torch.Tensor) and bias_values.dtype is _F32 and
+                bias_values.shape == bias_ids.shape and bias_values.get_device() == index and
+                bias_values.is_contiguous()):
+            _refuse(bias_values, "bias_values", _F32, bias_ids.shape, index)
+        b = bias_ids.shape[1]
+        if b:
+            ip, vp = bias_ids.data_ptr(), bias_values.data_ptr()
+    if mask is not None:
+        words = (m, (v + 31) // 32)
+        if not (isinstance(mask, torch.Tensor) and mask.dtype is _I32 and mask.shape == words and
+                mask.get_device() == index and mask.is_contiguous()):
+            _refuse(mask, "mask", _I32, words, index)
+        mp = mask.data_ptr()
+    _call("tl_adjust_logits", index, (logits.data_ptr(), m, v, dt, hp if h else None, h, *each, ip, vp, b, mp,
+                                      out.data_ptr(), od))
+    return out
 
 
 class TernaryLinear:

@@ -1,0 +1,38 @@
+// The 8-bit floating point form of rows: e4m3 codes (1 sign, 4 exponent, 3
+// mantissa bits, bias 7, no infinity, 0x7F NaN) and for each 128 of a row a
+// scale 2^(b - 127) held as its biased exponent b (0xFF: NaN).
+#pragma once
+
+#include "tl_internal.h"
+
+namespace tl {
+namespace f8 {
+
+constexpr uint32_t kInf = 0x7F800000u;
+
+// biased exponent of the smallest power of two S with a <= 448 S; a by its bits, finite
+__device__ __forceinline__ uint32_t scale_of(uint32_t a) {
+    const int s = int(a >> 23) - 8 + ((a & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return uint32_t(s > 0 ? s : 0);
+}
+
+__device__ __forceinline__ float scale_value(uint32_t b) {
+    return __builtin_bit_cast(float, b == 255 ? 0x7FC00000u : b == 0 ? 0x00400000u : b << 23);
+}
+
+// the values of 8 codes; exact in fp32 (but below 2^-126)
+__device__ __forceinline__ void values8(uint2 c, float s, float (&v)[8]) {
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const f2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(w[h], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(w[h], true);
+        v[4 * h] = lo[0] * s;
+        v[4 * h + 1] = lo[1] * s;
+        v[4 * h + 2] = hi[0] * s;
+        v[4 * h + 3] = hi[1] * s;
+    }
+}
+
+}  // namespace f8
+}  // namespace tl

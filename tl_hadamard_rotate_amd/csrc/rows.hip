@@ -1,0 +1,91 @@
+// Embedding lookup: rows of a table of 4-bit or 8-bit floating point weights,
+// times a factor,
+//
+//   out[m, k] = value(ids[m], k) * factor   (0 for an id outside the table)
+//
+// value is exact in fp32, the product is rounded there and once more to the
+// output's type.  A lane takes 8 values; nothing is shared, so the bound is
+// memory (a prompt) or the latency of two dependent loads, id then row (a token).
+#include "elem.h"
+#include "f8.h"
+#include "tl_internal.h"
+
+namespace tl {
+namespace {
+
+using namespace elem;
+using namespace f8;
+
+constexpr int kThreads = 256;
+
+// 8 values of table row `id` from its place j (in eights)
+template <int G>   // 4-bit codes with a scale per G
+struct Q4 {
+    static __device__ __forceinline__ void load(const uint8_t* codes, const void* scales, int64_t id, uint32_t eights,
+                                                uint32_t j, float (&v)[8]) {
+        const uint32_t q = reinterpret_cast<const uint32_t*>(codes)[id * eights + j];
+        const uint16_t h = static_cast<const uint16_t*>(scales)[id * (eights / (G / 8)) + j / (G / 8)];
+        const float s = float(__builtin_bit_cast(_Float16, h));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = float(int32_t(q << (28 - 4 * (i >> 1) - 16 * (i & 1))) >> 28) * s;
+    }
+};
+
+struct E4M3 {
+    static __device__ __forceinline__ void load(const uint8_t* codes, const void* scales, int64_t id, uint32_t eights,
+                                                uint32_t j, float (&v)[8]) {
+        const uint2 c = reinterpret_cast<const uint2*>(codes)[id * eights + j];
+        values8(c, scale_value(static_cast<const uint8_t*>(scales)[id * (eights / 16) + j / 16]), v);
+    }
+};
+
+template <typename W, typename T>
+__global__ __launch_bounds__(kThreads) void rows_kernel(const uint8_t* __restrict__ codes,
+                                                        const void* __restrict__ scales,
+                                                        const int32_t* __restrict__ ids, int64_t m, int64_t n,
+                                                        uint32_t eights, float factor, void* __restrict__ out) {
+    // the workgroup's first item by one division of scalars, a lane's by 32-bit ones
+    const int64_t first = int64_t(blockIdx.x) * kThreads, row0 = first / eights;
+    const uint32_t off = uint32_t(first - row0 * eights) + threadIdx.x;
+    const int64_t row = row0 + off / eights;
+    const uint32_t j = off % eights;
+    if (row >= m) return;
+    const int32_t id = ids[row];
+    float v[8] = {};
+    if (id >= 0 && id < n) {
+        W::load(codes, scales, id, eights, j, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= factor;
+    }
+    store8<T, true>(out, 8 * (row * eights + j), v);
+}
+
+template <typename W>
+hipError_t rows(const uint8_t* codes, const void* scales, const int32_t* ids, int64_t m, int64_t n, int64_t k,
+                float factor, void* out, int out_dtype, hipStream_t stream) {
+    const uint32_t eights = uint32_t(k / 8);
+    const dim3 grid(unsigned((m * eights + kThreads - 1) / kThreads)), block(kThreads);
+    if (out_dtype == TL_F32)
+        hipLaunchKernelGGL((rows_kernel<W, F32>), grid, block, 0, stream, codes, scales, ids, m, n, eights, factor, out);
+    else if (out_dtype == TL_F16)
+        hipLaunchKernelGGL((rows_kernel<W, F16>), grid, block, 0, stream, codes, scales, ids, m, n, eights, factor, out);
+    else
+        hipLaunchKernelGGL((rows_kernel<W, BF16>), grid, block, 0, stream, codes, scales, ids, m, n, eights, factor, out);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_q4_rows(const uint8_t* packed, const uint16_t* scales, int group, const int32_t* ids, int64_t m,
+                          int64_t n, int64_t k, float factor, void* out, int out_dtype, hipStream_t stream) {
+    return group == 32   ? rows<Q4<32>>(packed, scales, ids, m, n, k, factor, out, out_dtype, stream)
+           : group == 64 ? rows<Q4<64>>(packed, scales, ids, m, n, k, factor, out, out_dtype, stream)
+                         : rows<Q4<128>>(packed, scales, ids, m, n, k, factor, out, out_dtype, stream);
+}
+
+hipError_t launch_f8_rows(const uint8_t* codes, const uint8_t* scales, const int32_t* ids, int64_t m, int64_t n,
+                          int64_t k, float factor, void* out, int out_dtype, hipStream_t stream) {
+    return rows<E4M3>(codes, scales, ids, m, n, k, factor, out, out_dtype, stream);
+}
+
+}  // namespace tl

@@ -98,6 +98,18 @@ bool q4_product_shape_ok(int64_t m, int64_t n, int64_t k) {
     return q4_shape_ok(n, k) && m >= 1 && m <= kMaxRows && m * k <= kMaxElems && m * n <= kMaxElems;
 }
 
+// the checks that both kinds of embedding tables share
+tl_status check_rows(const void* codes, int64_t code_bytes, const void* scales, int64_t scale_bytes,
+                     const int32_t* ids, int64_t m, int64_t k, float factor, const void* out, int32_t out_dtype) {
+    if (!real_dtype(out_dtype)) return TL_ERR_DTYPE;
+    if (!std::isfinite(factor)) return TL_ERR_VALUE;
+    if (!aligned16(codes) || !aligned16(scales) || !aligned4(ids) || !aligned16(out)) return TL_ERR_ALIGN;
+    const int64_t ob = m * k * dtype_bytes(out_dtype);
+    if (overlap(out, ob, codes, code_bytes) || overlap(out, ob, scales, scale_bytes) || overlap(out, ob, ids, m * 4))
+        return TL_ERR_ALIAS;
+    return TL_OK;
+}
+
 // TL_DEBUG=1: count the packed bytes that are not valid encodings before a
 // call that decodes them; a device int per GPU holds the count
 bool debug_on() {
@@ -447,6 +459,104 @@ tl_status tl_q4_gemv(const uint8_t* packed, const uint16_t* scales, int32_t grou
     if (st != TL_OK) return st;
     return launched(tl::launch_q4_gemv(packed, scales, group, x, x_dtype, x_scales, M, N, K, y,
                                        y_dtype, workspace, stream));
+}
+
+tl_status tl_f8_quantize(const void* x, int64_t M, int64_t K, int32_t x_dtype, uint8_t* codes,
+                         uint8_t* scales, hipStream_t stream) {
+    if (!x || !codes || !scales) return TL_ERR_NULL;
+    if (!q4_shape_ok(M, K)) return TL_ERR_SHAPE;
+    if (!real_dtype(x_dtype)) return TL_ERR_DTYPE;
+    if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return TL_ERR_ALIGN;
+    const int64_t xb = M * K * dtype_bytes(x_dtype), cb = M * K, sb = M * (K / TL_GROUP);
+    if (overlap(codes, cb, x, xb) || overlap(scales, sb, x, xb) || overlap(codes, cb, scales, sb))
+        return TL_ERR_ALIAS;
+    return launched(tl::launch_f8_quantize(x, M, K, x_dtype, codes, scales, stream));
+}
+
+tl_status tl_f8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K, void* out,
+                           int32_t out_dtype, hipStream_t stream) {
+    if (!codes || !scales || !out) return TL_ERR_NULL;
+    if (!q4_shape_ok(M, K)) return TL_ERR_SHAPE;
+    if (!real_dtype(out_dtype)) return TL_ERR_DTYPE;
+    if (!aligned16(codes) || !aligned16(scales) || !aligned16(out)) return TL_ERR_ALIGN;
+    const int64_t ob = M * K * dtype_bytes(out_dtype);
+    if (overlap(out, ob, codes, M * K) || overlap(out, ob, scales, M * (K / TL_GROUP))) return TL_ERR_ALIAS;
+    return launched(tl::launch_f8_dequantize(codes, scales, M, K, out, out_dtype, stream));
+}
+
+int64_t tl_f8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    return q4_product_shape_ok(M, N, K) ? tl::f8_gemm_workspace_bytes(M, N, K) : -1;
+}
+
+tl_status tl_f8_gemm(const uint8_t* codes, const uint8_t* scales, const uint8_t* x, const uint8_t* x_scales,
+                     int64_t M, int64_t N, int64_t K, void* y, int32_t y_dtype, void* workspace,
+                     int64_t workspace_bytes, hipStream_t stream) {
+    if (!codes || !scales || !x || !x_scales || !y) return TL_ERR_NULL;
+    if (!q4_product_shape_ok(M, N, K)) return TL_ERR_SHAPE;
+    if (!real_dtype(y_dtype)) return TL_ERR_DTYPE;
+    if (!aligned16(codes) || !aligned16(scales) || !aligned16(x) || !aligned16(x_scales) || !aligned16(y))
+        return TL_ERR_ALIGN;
+    const int64_t cb = N * K, sb = N * (K / TL_GROUP), xb = M * K, xsb = M * (K / TL_GROUP);
+    const int64_t yb = M * N * dtype_bytes(y_dtype);
+    if (overlap(y, yb, codes, cb) || overlap(y, yb, scales, sb) || overlap(y, yb, x, xb) ||
+        overlap(y, yb, x_scales, xsb))
+        return TL_ERR_ALIAS;
+    const tl_status st =
+        check_workspace(tl::f8_gemm_workspace_bytes(M, N, K), workspace, workspace_bytes,
+                        {{codes, cb}, {scales, sb}, {x, xb}, {x_scales, xsb}, {y, yb}});
+    if (st != TL_OK) return st;
+    return launched(tl::launch_f8_gemm(codes, scales, x, x_scales, M, N, K, y, y_dtype, workspace, stream));
+}
+
+tl_status tl_q4_rows(const uint8_t* packed, const uint16_t* scales, int32_t group, const int32_t* ids,
+                     int64_t M, int64_t N, int64_t K, float factor, void* out, int32_t out_dtype,
+                     hipStream_t stream) {
+    if (!packed || !scales || !ids || !out) return TL_ERR_NULL;
+    if (!q4_shape_ok(N, K) || !q4_shape_ok(M, K)) return TL_ERR_SHAPE;
+    if (!q4_group_ok(group)) return TL_ERR_FORMAT;
+    const tl_status st = check_rows(packed, N * (K / 2), scales, N * (K / group) * 2, ids, M, K, factor, out, out_dtype);
+    if (st != TL_OK) return st;
+    return launched(tl::launch_q4_rows(packed, scales, group, ids, M, N, K, factor, out, out_dtype, stream));
+}
+
+tl_status tl_f8_rows(const uint8_t* codes, const uint8_t* scales, const int32_t* ids, int64_t M, int64_t N,
+                     int64_t K, float factor, void* out, int32_t out_dtype, hipStream_t stream) {
+    if (!codes || !scales || !ids || !out) return TL_ERR_NULL;
+    if (!q4_shape_ok(N, K) || !q4_shape_ok(M, K)) return TL_ERR_SHAPE;
+    const tl_status st = check_rows(codes, N * K, scales, N * (K / TL_GROUP), ids, M, K, factor, out, out_dtype);
+    if (st != TL_OK) return st;
+    return launched(tl::launch_f8_rows(codes, scales, ids, M, N, K, factor, out, out_dtype, stream));
+}
+
+tl_status tl_adjust_logits(const void* logits, int64_t M, int64_t V, int32_t dtype, const int32_t* history,
+                           int64_t H, const int32_t* history_lens, const int32_t* prompt_lens,
+                           const float* repetition, const float* presence, const float* frequency,
+                           const int32_t* bias_ids, const float* bias_values, int64_t B, const uint32_t* mask,
+                           void* out, int32_t out_dtype, hipStream_t stream) {
+    if (!logits || !out) return TL_ERR_NULL;
+    if (!history && (history_lens || prompt_lens || repetition || presence || frequency)) return TL_ERR_NULL;
+    if (!bias_ids != !bias_values) return TL_ERR_NULL;
+    if (!(M >= 1 && M <= kMaxRows && V >= 1 && V <= kMaxRows && M * V <= kMaxElems)) return TL_ERR_SHAPE;
+    if (!(H >= 0 && H <= kMaxRows && M * H <= kMaxElems) || (!history && H)) return TL_ERR_SHAPE;
+    if (!(B >= 0 && B <= kMaxRows && M * B <= kMaxElems) || (!bias_ids && B)) return TL_ERR_SHAPE;
+    if (!real_dtype(dtype) || !real_dtype(out_dtype)) return TL_ERR_DTYPE;
+    if (!aligned16(logits) || !aligned16(out)) return TL_ERR_ALIGN;
+    const int64_t lb = M * V * dtype_bytes(dtype), ob = M * V * dtype_bytes(out_dtype);
+    if (!(out == logits && out_dtype == dtype) && overlap(out, ob, logits, lb)) return TL_ERR_ALIAS;
+    const struct {
+        const void* p;
+        int64_t bytes;
+    } ins[] = {{history, M * H * 4}, {history_lens, M * 4}, {prompt_lens, M * 4}, {repetition, M * 4},
+               {presence, M * 4}, {frequency, M * 4}, {bias_ids, M * B * 4}, {bias_values, M * B * 4},
+               {mask, M * ((V + 31) / 32) * 4}};
+    for (const auto& in : ins) {
+        if (!in.p) continue;
+        if (!aligned4(in.p)) return TL_ERR_ALIGN;
+        if (in.bytes && overlap(out, ob, in.p, in.bytes)) return TL_ERR_ALIAS;
+    }
+    return launched(tl::launch_adjust_logits(logits, M, V, dtype, history, H, history_lens, prompt_lens, repetition,
+                                             presence, frequency, bias_ids, bias_values, B, mask, out, out_dtype,
+                                             stream));
 }
 
 const char* tl_status_str(tl_status status) {

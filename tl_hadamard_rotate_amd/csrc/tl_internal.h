@@ -150,4 +150,27 @@ hipError_t launch_q4_gemv(const uint8_t* packed, const uint16_t* scales, int gro
                           int x_dtype, const float* x_scales, int64_t m, int64_t n, int64_t k, void* y,
                           int y_dtype, void* ws, hipStream_t stream);
 
+// 8-bit floating point rows with block scales: rounding, values, and the
+// product of rows with weights (few tokens; any number)
+hipError_t launch_f8_quantize(const void* x, int64_t m, int64_t k, int x_dtype, uint8_t* codes, uint8_t* scales,
+                              hipStream_t stream);
+hipError_t launch_f8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t n, int64_t k, void* w,
+                                int w_dtype, hipStream_t stream);
+hipError_t launch_f8_gemv(const uint8_t* codes, const uint8_t* scales, const uint8_t* x, const uint8_t* x_scales,
+                          int64_t m, int64_t n, int64_t k, void* y, int y_dtype, hipStream_t stream);
+int64_t f8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k);
+hipError_t launch_f8_gemm(const uint8_t* codes, const uint8_t* scales, const uint8_t* x, const uint8_t* x_scales,
+                          int64_t m, int64_t n, int64_t k, void* y, int y_dtype, void* ws, hipStream_t stream);
+// Embedding rows of both kinds of tables
+hipError_t launch_q4_rows(const uint8_t* packed, const uint16_t* scales, int group, const int32_t* ids, int64_t m,
+                          int64_t n, int64_t k, float factor, void* out, int out_dtype, hipStream_t stream);
+hipError_t launch_f8_rows(const uint8_t* codes, const uint8_t* scales, const int32_t* ids, int64_t m, int64_t n,
+                          int64_t k, float factor, void* out, int out_dtype, hipStream_t stream);
+// Penalties, biases and mask of logits; null pointers as in tl_adjust_logits
+hipError_t launch_adjust_logits(const void* logits, int64_t m, int64_t v, int dtype, const int32_t* history,
+                                int64_t h, const int32_t* history_lens, const int32_t* prompt_lens,
+                                const float* repetition, const float* presence, const float* frequency,
+                                const int32_t* bias_ids, const float* bias_values, int64_t b, const uint32_t* mask,
+                                void* out, int out_dtype, hipStream_t stream);
+
 }  // namespace tl
