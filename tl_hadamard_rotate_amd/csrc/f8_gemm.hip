@@ -1,12 +1,396 @@
+// Product of rows and weights in 8-bit floating point on the matrix cores:
+//
+//   y[m, n] = sum_k X[m, k] * W[n, k],   X, W = e4m3 code * 2^(scale of its 128)
+//
+// v_mfma_scale_f32_32x32x64_f8f6f4 takes both operands' codes and scales as they
+// are: weights are the A rows, tokens the B columns.
+#include "elem.h"
+#include "f8.h"
 #include "tl_internal.h"
 
 namespace tl {
+namespace {
 
-int64_t f8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k) { return 0; }
+using namespace elem;
+
+typedef int int8v __attribute__((ext_vector_type(8)));
+typedef float float16v __attribute__((ext_vector_type(16)));
+typedef __bf16 bf2v __attribute__((ext_vector_type(2)));
+typedef __bf16 bf8v __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) uint32_t lds_u32;
+
+constexpr int kThreads = 512;    // 8 waves: 4 along the weight rows, 2 along the tokens
+constexpr int kRows = 256;       // weight rows of a tile
+constexpr int kStep = 64;        // K of a step
+
+struct Args {
+    const uint8_t *w, *ws, *x, *xs;
+    void* y;
+    float* sums;
+    int64_t m, n, k;
+    int y_dtype, groups;             // groups: K / 128
+    int tiles_m, tiles_n, tiles, whole, splits, chunk_a, chunk_b;
+};
+
+// 16 (1) bytes a lane from base + offset to LDS, lane i at `to` + 16 (4) i.
+// Written out, with the waits of the loop: the compiler would make every LDS
+// read wait for every load on the way into LDS.
+__device__ __forceinline__ void load_lds16(const uint8_t* base, uint32_t offset, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(to), "v"(offset), "s"(base)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ void load_lds1(const uint8_t* base, uint32_t offset, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, %2"
+                 :
+                 : "s"(to), "v"(offset), "s"(base)
+                 : "memory", "m0");
+}
+
+// One 32 x 32 tile of a lane's sums to y: register r of lane (q, c) is weight row
+// 8 (r / 4) + 4 q + r % 4 and token c of the tile
+__device__ __forceinline__ void store_tile(const float16v& acc, const Args& a, int64_t n0, int64_t token, int q) {
+    if (a.y_dtype == TL_F32) {
+        float* y = static_cast<float*>(a.y) + token * a.n;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int64_t n = n0 + 8 * g + 4 * q;
+            const float v[4] = {acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]};
+            if (token >= a.m) continue;
+            if (n + 4 <= a.n) {
+                __builtin_memcpy(y + n, v, 16);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (n + r < a.n) y[n + r] = v[r];
+            }
+        }
+        return;
+    }
+    uint16_t* y = static_cast<uint16_t*>(a.y) + token * a.n;
+    const auto pair = [&](float u, float v) {
+        return a.y_dtype == TL_F16 ? f16_bits(u) | f16_bits(v) << 16 : bf16_pair(u, v);
+    };
+    // the halves of the wave exchange rows, so that each lane has 8 in a row
+#pragma unroll
+    for (int g = 0; g < 4; g += 2) {
+        const auto s0 = __builtin_amdgcn_permlane32_swap(pair(acc[4 * g], acc[4 * g + 1]),
+                                                         pair(acc[4 * g + 4], acc[4 * g + 5]), false, false);
+        const auto s1 = __builtin_amdgcn_permlane32_swap(pair(acc[4 * g + 2], acc[4 * g + 3]),
+                                                         pair(acc[4 * g + 6], acc[4 * g + 7]), false, false);
+        const uint32_t v[4] = {s0[0], s1[0], s0[1], s1[1]};
+        const int64_t n = n0 + 8 * (g + q);
+        if (token >= a.m) continue;
+        if (n + 8 <= a.n) {
+            __builtin_memcpy(y + n, v, 16);
+        } else {
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (n + r < a.n) y[n + r] = uint16_t(v[r >> 1] >> (16 * (r & 1)));
+        }
+    }
+}
+
+__device__ __forceinline__ void tile_origin(const Args& a, int tile, int tokens, int64_t& n0, int64_t& m0) {
+    // four rows of tokens' tiles at a time, those fastest
+    const int per = 4 * a.tiles_n, band = tile / per, in = tile - band * per;
+    const int high = a.tiles_m - 4 * band < 4 ? a.tiles_m - 4 * band : 4;
+    m0 = int64_t(4 * band + in % high) * tokens;
+    n0 = int64_t(in / high) * kRows;
+}
+
+__device__ __forceinline__ bf8v widen(uint32_t a, uint32_t b, float s) {
+    const bf2v p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, s, false);
+    const bf2v p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, s, true);
+    const bf2v p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, s, false);
+    const bf2v p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, s, true);
+    return bf8v{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+}
+
+template <int IT, bool WIDE>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void f8_gemm_kernel(const Args a) {
+    constexpr int kTokens = 64 * IT;
+    constexpr int kStage = (kRows + kTokens) * kStep, kScaleStage = (kRows + kTokens) * 4;
+    constexpr int kTokenLoads = kTokens / 16, kPerWave = kTokenLoads < 8 ? 1 : kTokenLoads / 8;
+    constexpr int kLoads = 2 + kPerWave;        // of a wave in a step, and one of scales every other step
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    const uint32_t lds = uint32_t(uintptr_t((__attribute__((address_space(3))) uint8_t*)(smem)));
+    const uint32_t scale_lds = lds + 4 * kStage;
+
+    int tile, sp = 0, slot = 0;
+    bool split = false;
+    if (int(blockIdx.x) < 8 * a.chunk_a) {
+        tile = int(blockIdx.x & 7) * a.chunk_a + int(blockIdx.x >> 3);
+        if (tile >= a.whole) return;
+    } else {
+        const int u = int(blockIdx.x) - 8 * a.chunk_a;
+        slot = (u & 7) * a.chunk_b + (u >> 3);
+        if (slot >= (a.tiles - a.whole) * a.splits) return;
+        tile = a.whole + slot / a.splits;
+        sp = slot % a.splits;
+        split = a.splits > 1;
+    }
+    int64_t m0, n0;
+    tile_origin(a, tile, kTokens, n0, m0);
+    const int g0 = split ? int(int64_t(sp) * a.groups / a.splits) : 0;
+    const int g1 = split ? int(int64_t(sp + 1) * a.groups / a.splits) : a.groups;
+    const int steps = 2 * (g1 - g0);
+
+    const int tid = threadIdx.x, l = tid & 63, q = l >> 5, c = l & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = 64 * (wave & 3), wt = 32 * IT * (wave >> 2);
+
+    // lane i of a load of 1 KB brings 16 bytes of row i / 4 to place i % 4, those
+    // of chunk (i % 4) ^ ((row / 4) % 4): 16 rows read at one chunk meet all banks
+    const uint8_t* const wb = a.w + n0 * a.k + int64_t(g0) * 128;
+    const uint8_t* const xb = a.x + m0 * a.k + int64_t(g0) * 128;
+    const uint8_t* const wsb = a.ws + n0 * a.groups + g0;
+    const uint8_t* const xsb = a.xs + m0 * a.groups + g0;
+    const uint32_t k32 = uint32_t(a.k);
+    const int64_t left_n = a.n - n0, left_m = a.m - m0;
+    const auto row_n = [&](int r) { return uint32_t(r < left_n ? r : left_n - 1); };   // rows past the end: the last
+    const auto row_m = [&](int r) { return uint32_t(r < left_m ? r : left_m - 1); };
+    const uint32_t chunk = 16u * uint32_t((l & 3) ^ ((l >> 4) & 3));
+    uint32_t w_off[2], x_off[kPerWave];
+    uint32_t w_to[2], x_to[kPerWave];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        w_off[u] = row_n(32 * wave + 16 * u + (l >> 2)) * k32 + chunk;
+        w_to[u] = uint32_t(32 * wave + 16 * u) * kStep;
+    }
+#pragma unroll
+    for (int u = 0; u < kPerWave; ++u) {
+        const int first = 16 * ((kPerWave * wave + u) % kTokenLoads);
+        x_off[u] = row_m(first + (l >> 2)) * k32 + chunk;
+        x_to[u] = uint32_t(kRows + first) * kStep;
+    }
+    const int sw = wave % (4 + IT);     // 64 rows' scales
+    const bool s_w = sw < 4;
+    const uint8_t* const sb = s_w ? wsb : xsb;
+    const uint32_t s_off = (s_w ? row_n(64 * sw + l) : row_m(64 * (sw - 4) + l)) * uint32_t(a.groups);
+    const uint32_t s_to = scale_lds + 256u * uint32_t(sw);
+
+    const auto load_step = [&](int t, int stage) {   // t past the end: the last step again
+        const uint32_t at = uint32_t(t < steps ? t : steps - 1) * kStep;
+        const uint32_t to = lds + uint32_t(stage) * kStage;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) load_lds16(wb, w_off[u] + at, to + w_to[u]);
+#pragma unroll
+        for (int u = 0; u < kPerWave; ++u) load_lds16(xb, x_off[u] + at, to + x_to[u]);
+    };
+    const auto load_scales = [&](int t, int stage) {
+        const uint32_t g = uint32_t(t < steps ? t : steps - 1) >> 1;
+        load_lds1(sb, s_off + g, s_to + uint32_t(stage) * kScaleStage);
+    };
+
+    // a lane's fragment of a 32-row tile: 32 bytes of row c, at 32 q
+    const uint32_t f0 = uint32_t(c) * kStep + 16u * uint32_t((2 * q) ^ ((c >> 2) & 3));
+    const uint32_t f1 = uint32_t(c) * kStep + 16u * uint32_t((2 * q + 1) ^ ((c >> 2) & 3));
+    const auto fragment = [&](uint32_t at) {
+        const u32x4 lo = *reinterpret_cast<lds_u32x4*>(at + f0), hi = *reinterpret_cast<lds_u32x4*>(at + f1);
+        return int8v{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]), int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])};
+    };
+
+    int8v wf[2][2], xf[2][IT];
+    int wsc[2][2], xsc[2][IT];
+    const auto read_step = [&](int buf, int stage) {
+        const uint32_t at = lds + uint32_t(stage) * kStage;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) wf[buf][i] = fragment(at + uint32_t(wn + 32 * i) * kStep);
+#pragma unroll
+        for (int j = 0; j < IT; ++j) xf[buf][j] = fragment(at + uint32_t(kRows + wt + 32 * j) * kStep);
+    };
+    const auto read_scales = [&](int buf, int stage) {
+        const uint32_t at = scale_lds + uint32_t(stage) * kScaleStage + 4u * uint32_t(c);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) wsc[buf][i] = int(*reinterpret_cast<lds_u32*>(at + 4u * uint32_t(wn + 32 * i)));
+#pragma unroll
+        for (int j = 0; j < IT; ++j) xsc[buf][j] = int(*reinterpret_cast<lds_u32*>(at + 4u * uint32_t(kRows + wt + 32 * j)));
+    };
+
+    float16v acc[2][IT];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < IT; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+    load_scales(0, 0);
+#pragma unroll
+    for (int t = 0; t < 3; ++t) load_step(t, t);
+    load_scales(2, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    read_scales(0, 0);
+    read_step(0, 0);
+
+    const auto step = [&](int t, auto s_c) {
+        constexpr int S = decltype(s_c)::value, cur = S & 1, nxt = cur ^ 1, group = S >> 1;
+        // step t + 3 into the stage that step t - 1 used; its scales with an even step
+        load_step(t + 3, (S + 3) & 3);
+        if (S & 1) load_scales(t + 3, ((S + 3) >> 1) & 1);
+        __builtin_amdgcn_sched_barrier(0);
+        if (S & 1) read_scales(group ^ 1, group ^ 1);
+        read_step(nxt, (S + 1) & 3);
+        if constexpr (WIDE) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                bf8v wv[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    wv[i] = widen(uint32_t(wf[cur][i][2 * h]), uint32_t(wf[cur][i][2 * h + 1]),
+                                  __builtin_bit_cast(float, wsc[group][i] << 23));
+#pragma unroll
+                for (int j = 0; j < IT; ++j) {
+                    const bf8v xv = widen(uint32_t(xf[cur][j][2 * h]), uint32_t(xf[cur][j][2 * h + 1]),
+                                          __builtin_bit_cast(float, xsc[group][j] << 23));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wv[i], xv, acc[i][j], 0, 0, 0);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < IT; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                        wf[cur][i], xf[cur][j], acc[i][j], 0, 0, 0, wsc[group][i], 0, xsc[group][j]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // all but this step's own loads are there: what the next step reads
+        if (S & 1) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kLoads + 1) : "memory");
+        else asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kLoads) : "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    using C0 = std::integral_constant<int, 0>;
+    using C1 = std::integral_constant<int, 1>;
+    using C2 = std::integral_constant<int, 2>;
+    using C3 = std::integral_constant<int, 3>;
+    int t = 0;
+    for (; t + 4 <= steps; t += 4) {
+        step(t, C0{});
+        step(t + 1, C1{});
+        step(t + 2, C2{});
+        step(t + 3, C3{});
+    }
+    if (t < steps) {
+        step(t, C0{});
+        step(t + 1, C1{});
+    }
+    // loads into stages nobody reads may still be on the way: wait for them before
+    // the workgroup's LDS goes to another
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+
+    if (split) {
+        float* mine = a.sums + size_t(slot) * (kRows * kTokens);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < IT; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) mine[((i * IT + j) * 16 + r) * kThreads + tid] = acc[i][j][r];
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < IT; ++j)
+            store_tile(acc[i][j], a, n0 + wn + 32 * i, m0 + wt + 32 * j + c, q);
+}
+
+// The parts of a tile's sums added in their order
+template <int IT>
+__global__ __launch_bounds__(kThreads) void f8_join_kernel(const Args a) {
+    constexpr int kTokens = 64 * IT;
+    const int t = int(blockIdx.x) / (2 * IT), e = int(blockIdx.x) % (2 * IT);
+    int64_t m0, n0;
+    tile_origin(a, a.whole + t, kTokens, n0, m0);
+    const int tid = threadIdx.x, l = tid & 63, wave = tid >> 6;
+    const float* parts = a.sums + size_t(t) * a.splits * (kRows * kTokens) + size_t(e) * 16 * kThreads + tid;
+    float16v sum;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) sum[r] = parts[r * kThreads];
+    for (int p = 1; p < a.splits; ++p) {
+        parts += kRows * kTokens;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sum[r] += parts[r * kThreads];
+    }
+    store_tile(sum, a, n0 + 64 * (wave & 3) + 32 * (e / IT), m0 + 32 * IT * (wave >> 2) + 32 * (e % IT) + (l & 31), l >> 5);
+}
+
+struct Plan {
+    int it, splits;
+    int64_t tiles_m, tiles_n, tiles, whole;
+};
+
+constexpr int64_t kMaxParts = 512;
+
+Plan make_plan(int64_t m, int64_t n, int64_t k) {
+    Plan p;
+    p.it = m <= 64 ? 1 : m <= 128 ? 2 : 4;
+    p.tiles_m = (m + 64 * p.it - 1) / (64 * p.it);
+    p.tiles_n = (n + kRows - 1) / kRows;
+    p.tiles = p.tiles_m * p.tiles_n;
+    const int64_t cus = cu_count(), rem = p.tiles % cus, groups = k / 128;
+    p.whole = p.tiles;
+    p.splits = 1;
+    double best = double(groups);
+    for (int s = 2; rem && s <= 32 && s <= groups / 2 && rem * s <= kMaxParts; ++s) {
+        const double cost = double((rem * s + cus - 1) / cus) * (double((groups + s - 1) / s) + 1.0) + 0.02 * double(rem * s) + 2.0;
+        if (cost < best - 1.0) {
+            best = cost;
+            p.whole = p.tiles - rem;
+            p.splits = s;
+        }
+    }
+    return p;
+}
+
+template <int IT, bool WIDE>
+hipError_t launch(Args a, const Plan& p, hipStream_t stream) {
+    const auto kernel = f8_gemm_kernel<IT, WIDE>;
+    constexpr int lds = 4 * (kRows + 64 * IT) * kStep + 2 * (kRows + 64 * IT) * 4;
+    hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), lds);
+    if (e != hipSuccess) return e;
+    const int64_t items = (p.tiles - p.whole) * p.splits;
+    a.tiles_m = int(p.tiles_m);
+    a.tiles_n = int(p.tiles_n);
+    a.tiles = int(p.tiles);
+    a.whole = int(p.whole);
+    a.splits = p.splits;
+    a.chunk_a = int((p.whole + 7) / 8);
+    a.chunk_b = int((items + 7) / 8);
+    hipLaunchKernelGGL(kernel, dim3(unsigned(8 * (a.chunk_a + a.chunk_b))), dim3(kThreads), lds, stream, a);
+    if (p.splits > 1) {
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        hipLaunchKernelGGL(f8_join_kernel<IT>, dim3(unsigned(2 * IT * (p.tiles - p.whole))), dim3(kThreads), 0, stream, a);
+    }
+    return hipGetLastError();
+}
+
+constexpr int64_t kFewTokens = 64;
+
+}  // namespace
+
+int64_t f8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+    if (m <= kFewTokens) return 0;
+    const Plan p = make_plan(m, n, k);
+    return p.splits > 1 ? (p.tiles - p.whole) * p.splits * kRows * 64 * p.it * 4 : 0;
+}
 
 hipError_t launch_f8_gemm(const uint8_t* codes, const uint8_t* scales, const uint8_t* x, const uint8_t* x_scales,
                           int64_t m, int64_t n, int64_t k, void* y, int y_dtype, void* ws, hipStream_t stream) {
-    return launch_f8_gemv(codes, scales, x, x_scales, m, n, k, y, y_dtype, stream);
+    if (m <= kFewTokens) return launch_f8_gemv(codes, scales, x, x_scales, m, n, k, y, y_dtype, stream);
+    const Plan p = make_plan(m, n, k);
+    const Args a = {codes, scales, x, x_scales, y, static_cast<float*>(ws), m, n, k, y_dtype, int(k / 128), 0, 0, 0, 0, 0, 0, 0};
+    if (y_dtype == TL_F32)
+        return p.it == 1 ? launch<1, true>(a, p, stream) : p.it == 2 ? launch<2, true>(a, p, stream) : launch<4, true>(a, p, stream);
+    return p.it == 1 ? launch<1, false>(a, p, stream) : p.it == 2 ? launch<2, false>(a, p, stream) : launch<4, false>(a, p, stream);
 }
 
 }  // namespace tl
