@@ -117,6 +117,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     constexpr int kLoads = 2 + kPerWave;        // of a wave in a step, and one of scales every other step
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const uint32_t lds = uint32_t(uintptr_t((__attribute__((address_space(3))) uint8_t*)(smem)));
+    constexpr uint32_t kXStages = 4 * kRows * kStep;
     const uint32_t scale_lds = lds + 4 * kStage;
 
     int tile, sp = 0, slot = 0;
@@ -164,7 +165,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     for (int u = 0; u < kPerWave; ++u) {
         const int first = 16 * ((kPerWave * wave + u) % kTokenLoads);
         x_off[u] = row_m(first + (l >> 2)) * k32 + chunk;
-        x_to[u] = uint32_t(kRows + first) * kStep;
+        x_to[u] = kXStages + uint32_t(first) * kStep;
     }
     const int sw = wave % (4 + IT);     // 64 rows' scales
     const bool s_w = sw < 4;
@@ -172,42 +173,48 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     const uint32_t s_off = (s_w ? row_n(64 * sw + l) : row_m(64 * (sw - 4) + l)) * uint32_t(a.groups);
     const uint32_t s_to = scale_lds + 256u * uint32_t(sw);
 
-    const auto load_step = [&](int t, int stage) {   // t past the end: the last step again
+    // load u of step t (past the end: of the last one again)
+    const auto load_w = [&](int t, int stage, int u) {
         const uint32_t at = uint32_t(t < steps ? t : steps - 1) * kStep;
-        const uint32_t to = lds + uint32_t(stage) * kStage;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) load_lds16(wb, w_off[u] + at, to + w_to[u]);
-#pragma unroll
-        for (int u = 0; u < kPerWave; ++u) load_lds16(xb, x_off[u] + at, to + x_to[u]);
+        load_lds16(wb + at, w_off[u], lds + uint32_t(stage) * kRows * kStep + w_to[u]);
+    };
+    const auto load_x = [&](int t, int stage, int u) {
+        const uint32_t at = uint32_t(t < steps ? t : steps - 1) * kStep;
+        load_lds16(xb + at, x_off[u], lds + uint32_t(stage) * kTokens * kStep + x_to[u]);
     };
     const auto load_scales = [&](int t, int stage) {
         const uint32_t g = uint32_t(t < steps ? t : steps - 1) >> 1;
-        load_lds1(sb, s_off + g, s_to + uint32_t(stage) * kScaleStage);
+        load_lds1(sb + g, s_off, s_to + uint32_t(stage) * kScaleStage);
     };
 
     // a lane's fragment of a 32-row tile: 32 bytes of row c, at 32 q
     const uint32_t f0 = uint32_t(c) * kStep + 16u * uint32_t((2 * q) ^ ((c >> 2) & 3));
-    const uint32_t f1 = uint32_t(c) * kStep + 16u * uint32_t((2 * q + 1) ^ ((c >> 2) & 3));
-    const auto fragment = [&](uint32_t at) {
-        const u32x4 lo = *reinterpret_cast<lds_u32x4*>(at + f0), hi = *reinterpret_cast<lds_u32x4*>(at + f1);
+    const uint32_t w_at = lds + uint32_t(wn) * kStep + f0, x_at = lds + kXStages + uint32_t(wt) * kStep + f0;
+    const uint32_t w_at1 = w_at ^ 16u, x_at1 = x_at ^ 16u;
+    const uint32_t ws_at = scale_lds + 4u * uint32_t(wn + c), xs_at = scale_lds + 4u * uint32_t(kRows + wt + c);
+    const auto fragment = [&](uint32_t lo_at, uint32_t hi_at) {
+        const u32x4 lo = *reinterpret_cast<lds_u32x4*>(lo_at), hi = *reinterpret_cast<lds_u32x4*>(hi_at);
         return int8v{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]), int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])};
     };
 
-    int8v wf[2][2], xf[2][IT];
-    int wsc[2][2], xsc[2][IT];
-    const auto read_step = [&](int buf, int stage) {
-        const uint32_t at = lds + uint32_t(stage) * kStage;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) wf[buf][i] = fragment(at + uint32_t(wn + 32 * i) * kStep);
-#pragma unroll
-        for (int j = 0; j < IT; ++j) xf[buf][j] = fragment(at + uint32_t(kRows + wt + 32 * j) * kStep);
+    int8v wf[2][2], xf[IT];
+    int wsc[2][2], xsc[IT];
+    const auto read_w = [&](int buf, int stage, int i) {
+        const uint32_t at = uint32_t(stage) * kRows * kStep + 32u * kStep * uint32_t(i);
+        wf[buf][i] = fragment(w_at + at, w_at1 + at);
     };
-    const auto read_scales = [&](int buf, int stage) {
-        const uint32_t at = scale_lds + uint32_t(stage) * kScaleStage + 4u * uint32_t(c);
+    const auto read_x = [&](int stage, int j) {
+        const uint32_t at = uint32_t(stage) * kTokens * kStep + 32u * kStep * uint32_t(j);
+        xf[j] = fragment(x_at + at, x_at1 + at);
+    };
+    const auto read_ws = [&](int buf, int stage) {
+        const uint32_t at = uint32_t(stage) * kScaleStage;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) wsc[buf][i] = int(*reinterpret_cast<lds_u32*>(at + 4u * uint32_t(wn + 32 * i)));
-#pragma unroll
-        for (int j = 0; j < IT; ++j) xsc[buf][j] = int(*reinterpret_cast<lds_u32*>(at + 4u * uint32_t(kRows + wt + 32 * j)));
+        for (int i = 0; i < 2; ++i) wsc[buf][i] = int(*reinterpret_cast<lds_u32*>(ws_at + at + 128u * uint32_t(i)));
+    };
+    const auto read_xs = [&](int stage, int j) {
+        const uint32_t at = uint32_t(stage) * kScaleStage;
+        xsc[j] = int(*reinterpret_cast<lds_u32*>(xs_at + at + 128u * uint32_t(j)));
     };
 
     float16v acc[2][IT];
@@ -220,46 +227,60 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 
     load_scales(0, 0);
 #pragma unroll
-    for (int t = 0; t < 3; ++t) load_step(t, t);
+    for (int t = 0; t < 3; ++t) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) load_w(t, t, u);
+#pragma unroll
+        for (int u = 0; u < kPerWave; ++u) load_x(t, t, u);
+    }
     load_scales(2, 1);
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-    read_scales(0, 0);
-    read_step(0, 0);
+    read_ws(0, 0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) read_w(0, 0, i);
+#pragma unroll
+    for (int j = 0; j < IT; ++j) read_xs(0, j), read_x(0, j);
 
     const auto step = [&](int t, auto s_c) {
         constexpr int S = decltype(s_c)::value, cur = S & 1, nxt = cur ^ 1, group = S >> 1;
-        // step t + 3 into the stage that step t - 1 used; its scales with an even step
-        load_step(t + 3, (S + 3) & 3);
-        if (S & 1) load_scales(t + 3, ((S + 3) >> 1) & 1);
-        __builtin_amdgcn_sched_barrier(0);
-        if (S & 1) read_scales(group ^ 1, group ^ 1);
-        read_step(nxt, (S + 1) & 3);
-        if constexpr (WIDE) {
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                bf8v wv[2];
+        for (int j = 0; j < IT; ++j) {
+            if constexpr (WIDE) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    wv[i] = widen(uint32_t(wf[cur][i][2 * h]), uint32_t(wf[cur][i][2 * h + 1]),
+                for (int h = 0; h < 4; ++h) {
+                    const bf8v xv = widen(uint32_t(xf[j][2 * h]), uint32_t(xf[j][2 * h + 1]),
+                                          __builtin_bit_cast(float, xsc[j] << 23));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                    const bf8v wv = widen(uint32_t(wf[cur][i][2 * h]), uint32_t(wf[cur][i][2 * h + 1]),
                                   __builtin_bit_cast(float, wsc[group][i] << 23));
-#pragma unroll
-                for (int j = 0; j < IT; ++j) {
-                    const bf8v xv = widen(uint32_t(xf[cur][j][2 * h]), uint32_t(xf[cur][j][2 * h + 1]),
-                                          __builtin_bit_cast(float, xsc[group][j] << 23));
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wv[i], xv, acc[i][j], 0, 0, 0);
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wv, xv, acc[i][j], 0, 0, 0);
+                    }
                 }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < IT; ++j)
+            } else {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                        wf[cur][i], xf[cur][j], acc[i][j], 0, 0, 0, wsc[group][i], 0, xsc[group][j]);
+                        wf[cur][i], xf[j], acc[i][j], 0, 0, 0, wsc[group][i], 0, xsc[j]);
+            }
+            if (j == 0) {
+                if (S & 1) read_ws(group ^ 1, group ^ 1);
+                read_w(nxt, (S + 1) & 3, 0);
+                read_w(nxt, (S + 1) & 3, 1);
+            }
+            if (S & 1) read_xs(group ^ 1, j);
+            read_x((S + 1) & 3, j);
+            constexpr int D = IT == 4 ? 0 : 0;
+            if (j == D || IT == 1) load_w(t + 3, (S + 3) & 3, 0), load_w(t + 3, (S + 3) & 3, 1);
+            if (IT == 1) load_x(t + 3, (S + 3) & 3, 0);
+            if (IT > 1 && j == D + 1) {
+#pragma unroll
+                for (int u = 0; u < kPerWave; ++u) load_x(t + 3, (S + 3) & 3, u);
+            }
+            if (S & 1 && j == IT - 1) load_scales(t + 3, ((S + 3) >> 1) & 1);
+            __builtin_amdgcn_sched_barrier(0);
         }
         __builtin_amdgcn_sched_barrier(0);
         // all but this step's own loads are there: what the next step reads
@@ -300,6 +321,237 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < IT; ++j)
+            store_tile(acc[i][j], a, n0 + wn + 32 * i, m0 + wt + 32 * j + c, q);
+}
+
+// ---- many tokens: 256 x 256 tiles, 8-bit matrix instructions ----
+
+constexpr int kScalePitch = 52;      // LDS bytes of a row's scales: 48, and 4 so that rows meet different banks
+constexpr int kSegment = 48;         // groups whose scales are in LDS at a time
+constexpr int kBigLds = 2 * 32768 + 4 * 16384 + 512 * kScalePitch;
+
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void f8_gemm_big_kernel(const Args a) {
+    constexpr int kTokens = 256;
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    const uint32_t lds = uint32_t(uintptr_t((__attribute__((address_space(3))) uint8_t*)(smem)));
+    const uint32_t x_lds = lds + 65536, scale_lds = lds + 131072;
+
+    int tile, sp = 0, slot = 0;
+    bool split = false;
+    if (int(blockIdx.x) < 8 * a.chunk_a) {
+        tile = int(blockIdx.x & 7) * a.chunk_a + int(blockIdx.x >> 3);
+        if (tile >= a.whole) return;
+    } else {
+        const int u = int(blockIdx.x) - 8 * a.chunk_a;
+        slot = (u & 7) * a.chunk_b + (u >> 3);
+        if (slot >= (a.tiles - a.whole) * a.splits) return;
+        tile = a.whole + slot / a.splits;
+        sp = slot % a.splits;
+        split = a.splits > 1;
+    }
+    int64_t m0, n0;
+    tile_origin(a, tile, kTokens, n0, m0);
+    const int g0 = split ? int(int64_t(sp) * a.groups / a.splits) : 0;
+    const int g1 = split ? int(int64_t(sp + 1) * a.groups / a.splits) : a.groups;
+    const int blocks = g1 - g0;
+
+    const int tid = threadIdx.x, l = tid & 63, q = l >> 5, c = l & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = 64 * (wave & 3), half = wave >> 2, wt = 128 * half;
+
+    const uint8_t* const wb = a.w + n0 * a.k + int64_t(g0) * 128;
+    const uint8_t* const xb = a.x + m0 * a.k + int64_t(g0) * 128;
+    const uint32_t k32 = uint32_t(a.k);
+    const int64_t left_n = a.n - n0, left_m = a.m - m0;
+    const auto row_n = [&](int r) { return uint32_t(r < left_n ? r : left_n - 1); };   // rows past the end: the last
+    const auto row_m = [&](int r) { return uint32_t(r < left_m ? r : left_m - 1); };
+    uint32_t w_off[4], x_off[2][2];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        w_off[u] = row_n(32 * wave + 8 * u + (l >> 3)) * k32 + 16u * uint32_t((l & 7) ^ (4 * (u & 1) + (l >> 4)));
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int r = 16 * wave + 8 * u + (l >> 3);
+            x_off[p][u] = row_m(128 * (r >> 6) + 64 * p + (r & 63)) * k32 + 16u * uint32_t((l & 7) ^ (4 * (u & 1) + (l >> 4)));
+        }
+    const auto load_w = [&](int b, int s, int u) {
+        load_lds16(wb + 128u * uint32_t(b < blocks ? b : blocks - 1), w_off[u], lds + uint32_t(s) * 32768u + uint32_t(32 * wave + 8 * u) * 128u);
+    };
+    const auto load_x = [&](int b, int p, int s, int u) {
+        load_lds16(xb + 128u * uint32_t(b < blocks ? b : blocks - 1), x_off[p][u], x_lds + uint32_t(s) * 16384u + uint32_t(16 * wave + 8 * u) * 128u);
+    };
+    // scales of groups [s0, s0 + 48) of the tile's rows, a row a lane
+    const auto stage_scales = [&](int s0) {
+        const bool is_w = tid < 256;
+        const uint8_t* from = (is_w ? a.ws + (n0 + row_n(tid)) * a.groups : a.xs + (m0 + row_m(tid - 256)) * a.groups) + g0 + s0;
+        const int left = blocks - s0;
+        uint32_t v[12] = {};
+#pragma unroll
+        for (int j = 0; j < 12; ++j) {
+            if (4 * j + 4 <= left) __builtin_memcpy(&v[j], from + 4 * j, 4);
+            else
+                for (int e = 0; e < 3; ++e)
+                    if (4 * j + e < left) v[j] |= uint32_t(from[4 * j + e]) << (8 * e);
+        }
+        lds_u32* to = reinterpret_cast<lds_u32*>(scale_lds + uint32_t(tid) * kScalePitch);
+#pragma unroll
+        for (int j = 0; j < 12; ++j) to[j] = v[j];
+    };
+
+    const uint32_t f = uint32_t(c) * 128u + 16u * uint32_t((2 * q) ^ ((c >> 1) & 7));
+    uint32_t w_at[2][2], x_at[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            w_at[h][e] = lds + uint32_t(wn) * 128u + (f ^ (64u * h) ^ (16u * e));
+            x_at[h][e] = x_lds + uint32_t(half) * 8192u + (f ^ (64u * h) ^ (16u * e));
+        }
+    const auto fragment = [&](uint32_t lo_at, uint32_t hi_at) {
+        const u32x4 lo = *reinterpret_cast<lds_u32x4*>(lo_at), hi = *reinterpret_cast<lds_u32x4*>(hi_at);
+        return int8v{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]), int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])};
+    };
+    int8v w0[2], w10, w11[2], xf[2][2];     // weights of K half 0, of half 1; tokens [jj][h]
+    int wsc[2][2], xsc[2][2];
+    const auto read_w = [&](int s, int h, int i) {
+        const uint32_t at = uint32_t(s) * 32768u + uint32_t(i) * 4096u;
+        return fragment(w_at[h][0] + at, w_at[h][1] + at);
+    };
+    const auto read_x = [&](int s, int h, int jj) {
+        const uint32_t at = uint32_t(s) * 16384u + uint32_t(jj) * 4096u;
+        return fragment(x_at[h][0] + at, x_at[h][1] + at);
+    };
+    typedef __attribute__((address_space(3))) uint8_t lds_u8;
+    uint32_t ws_at = scale_lds + uint32_t(wn + c) * kScalePitch, xs_at = scale_lds + uint32_t(256 + wt + c) * kScalePitch;
+    const auto read_ws = [&](int buf, uint32_t g) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) wsc[buf][i] = *reinterpret_cast<lds_u8*>(ws_at + g + 32u * kScalePitch * uint32_t(i));
+    };
+    const auto read_xs = [&](int buf, uint32_t g, int p) {
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj) xsc[buf][jj] = *reinterpret_cast<lds_u8*>(xs_at + g + 32u * kScalePitch * uint32_t(2 * p + jj));
+    };
+
+    float16v acc[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+#pragma unroll
+    for (int u = 0; u < 4; ++u) load_w(0, 0, u);
+#pragma unroll
+    for (int t = 0; t < 3; ++t)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) load_x(t >> 1, t & 1, t, u);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) load_w(1, 1, u);
+    stage_scales(0);
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    w0[0] = read_w(0, 0, 0);
+    w0[1] = read_w(0, 0, 1);
+    xf[0][0] = read_x(0, 0, 0);
+    xf[1][0] = read_x(0, 0, 1);
+    w10 = read_w(0, 1, 0);
+    w11[0] = read_w(0, 1, 1);
+    read_ws(0, 0);
+    read_xs(0, 0, 0);
+
+#define FENCE_ __builtin_amdgcn_sched_barrier(0)
+    const auto phase = [&](int b, auto p_c) {
+        constexpr int P = decltype(p_c)::value, bp = P >> 1, p = P & 1, nx = p ^ 1;
+        const auto mfma = [&](const int8v& w, int i, int jj, int h) {
+            acc[i][2 * p + jj] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                w, xf[jj][h], acc[i][2 * p + jj], 0, 0, 0, wsc[bp][i], 0, xsc[p][jj]);
+        };
+        mfma(w0[0], 0, 0, 0);
+        xf[0][1] = read_x(P, 1, 0);
+        FENCE_;
+        mfma(w0[0], 0, 1, 0);
+        xf[1][1] = read_x(P, 1, 1);
+        load_x(p ? b + 2 : b + 1, nx, (P + 3) & 3, 0);
+        FENCE_;
+        if (p) w0[0] = read_w(bp ^ 1, 0, 0);
+        mfma(w0[1], 1, 0, 0);
+        FENCE_;
+        xf[0][0] = read_x((P + 1) & 3, 0, 0);
+        mfma(w0[1], 1, 1, 0);
+        load_x(p ? b + 2 : b + 1, nx, (P + 3) & 3, 1);
+        FENCE_;
+        xf[1][0] = read_x((P + 1) & 3, 0, 1);
+        mfma(w10, 0, 0, 1);
+        if (p) w0[1] = read_w(bp ^ 1, 0, 1);
+        FENCE_;
+        if (p) w11[bp ^ 1] = read_w(bp ^ 1, 1, 1);
+        mfma(w10, 0, 1, 1);
+        load_w(b + 2, bp, 2 * p);
+        FENCE_;
+        if (p) w10 = read_w(bp ^ 1, 1, 0);
+        if (p) {
+            ws_at += 1;
+            xs_at += 1;
+            read_ws(bp ^ 1, 0);
+        }
+        read_xs(nx, 0, nx);
+        mfma(w11[bp], 1, 0, 1);
+        FENCE_;
+        mfma(w11[bp], 1, 1, 1);
+        load_w(b + 2, bp, 2 * p + 1);
+        FENCE_;
+        // all but this phase's own loads are there: what the next phase reads
+        if (p) asm volatile("s_waitcnt vmcnt(4) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        else asm volatile("s_waitcnt vmcnt(4)\n\ts_barrier" ::: "memory");
+        FENCE_;
+    };
+    using C0 = std::integral_constant<int, 0>;
+    using C1 = std::integral_constant<int, 1>;
+    using C2 = std::integral_constant<int, 2>;
+    using C3 = std::integral_constant<int, 3>;
+    for (int s0 = 0;;) {
+        const int end = blocks < s0 + kSegment ? blocks : s0 + kSegment;
+        int b = s0;
+        for (; b + 2 <= end; b += 2) {
+            phase(b, C0{});
+            phase(b, C1{});
+            phase(b + 1, C2{});
+            phase(b + 1, C3{});
+        }
+        if (b < end) {
+            phase(b, C0{});
+            phase(b, C1{});
+        }
+        s0 = end;
+        if (s0 >= blocks) break;
+        // (all waves are past the barrier behind their last read of a scale)
+        stage_scales(s0);
+        __syncthreads();
+        ws_at -= kSegment;
+        xs_at -= kSegment;
+        read_ws(0, 0);
+        read_xs(0, 0, 0);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+
+    if (split) {
+        float* mine = a.sums + size_t(slot) * (kRows * kTokens);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) mine[((i * 4 + j) * 16 + r) * kThreads + tid] = acc[i][j][r];
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
             store_tile(acc[i][j], a, n0 + wn + 32 * i, m0 + wt + 32 * j + c, q);
 }
 
@@ -353,8 +605,9 @@ Plan make_plan(int64_t m, int64_t n, int64_t k) {
 
 template <int IT, bool WIDE>
 hipError_t launch(Args a, const Plan& p, hipStream_t stream) {
-    const auto kernel = f8_gemm_kernel<IT, WIDE>;
-    constexpr int lds = 4 * (kRows + 64 * IT) * kStep + 2 * (kRows + 64 * IT) * 4;
+    constexpr bool kBig = IT == 4 && !WIDE;
+    const auto kernel = kBig ? f8_gemm_big_kernel : f8_gemm_kernel<IT, kBig || WIDE>;
+    constexpr int lds = kBig ? kBigLds : 4 * (kRows + 64 * IT) * kStep + 2 * (kRows + 64 * IT) * 4;
     hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), lds);
     if (e != hipSuccess) return e;
     const int64_t items = (p.tiles - p.whole) * p.splits;
