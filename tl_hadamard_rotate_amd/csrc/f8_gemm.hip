@@ -14,11 +14,13 @@ namespace {
 using namespace elem;
 
 typedef int int8v __attribute__((ext_vector_type(8)));
+typedef float float4v __attribute__((ext_vector_type(4)));
 typedef float float16v __attribute__((ext_vector_type(16)));
 typedef __bf16 bf2v __attribute__((ext_vector_type(2)));
 typedef __bf16 bf8v __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) uint32_t lds_u32;
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
 constexpr int kThreads = 512;    // 8 waves: 4 along the weight rows, 2 along the tokens
 constexpr int kRows = 256;       // weight rows of a tile
@@ -47,6 +49,12 @@ __device__ __forceinline__ void load_lds1(const uint8_t* base, uint32_t offset, 
                  :
                  : "s"(to), "v"(offset), "s"(base)
                  : "memory", "m0");
+}
+
+__device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
+    const uint64_t u = reinterpret_cast<uint64_t>(p);
+    return reinterpret_cast<const uint8_t*>(uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(u)))) |
+                                            uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(u >> 32)))) << 32);
 }
 
 // One 32 x 32 tile of a lane's sums to y: register r of lane (q, c) is weight row
@@ -314,7 +322,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 #pragma unroll
             for (int j = 0; j < IT; ++j)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) mine[((i * IT + j) * 16 + r) * kThreads + tid] = acc[i][j][r];
+                for (int r = 0; r < 16; r += 4)
+                    *reinterpret_cast<float4v*>(mine + (wt + 32 * j + c) * kRows + wn + 32 * i + 2 * r + 4 * q) =
+                        float4v{acc[i][j][r], acc[i][j][r + 1], acc[i][j][r + 2], acc[i][j][r + 3]};
         return;
     }
 #pragma unroll
@@ -329,7 +339,6 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 constexpr int kScalePitch = 52;      // LDS bytes of a row's scales: 48, and 4 so that rows meet different banks
 constexpr int kSegment = 48;         // groups whose scales are in LDS at a time
 constexpr int kBigLds = 2 * 32768 + 4 * 16384 + 512 * kScalePitch;
-
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void f8_gemm_big_kernel(const Args a) {
     constexpr int kTokens = 256;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -359,8 +368,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wn = 64 * (wave & 3), half = wave >> 2, wt = 128 * half;
 
-    const uint8_t* const wb = a.w + n0 * a.k + int64_t(g0) * 128;
-    const uint8_t* const xb = a.x + m0 * a.k + int64_t(g0) * 128;
+    const uint8_t* const wb = uniform(a.w + n0 * a.k + int64_t(g0) * 128);
+    const uint8_t* const xb = uniform(a.x + m0 * a.k + int64_t(g0) * 128);
     const uint32_t k32 = uint32_t(a.k);
     const int64_t left_n = a.n - n0, left_m = a.m - m0;
     const auto row_n = [&](int r) { return uint32_t(r < left_n ? r : left_n - 1); };   // rows past the end: the last
@@ -368,36 +377,34 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     uint32_t w_off[4], x_off[2][2];
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-        w_off[u] = row_n(32 * wave + 8 * u + (l >> 3)) * k32 + 16u * uint32_t((l & 7) ^ (4 * (u & 1) + (l >> 4)));
+        w_off[u] = row_n(8 * (4 * wave + u) + (l >> 3)) * k32 + 16u * uint32_t((l & 7) ^ (4 * (u & 1) + (l >> 4)));
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int r = 16 * wave + 8 * u + (l >> 3);
+            const int r = 8 * (2 * wave + u) + (l >> 3);
             x_off[p][u] = row_m(128 * (r >> 6) + 64 * p + (r & 63)) * k32 + 16u * uint32_t((l & 7) ^ (4 * (u & 1) + (l >> 4)));
         }
-    const auto load_w = [&](int b, int s, int u) {
-        load_lds16(wb + 128u * uint32_t(b < blocks ? b : blocks - 1), w_off[u], lds + uint32_t(s) * 32768u + uint32_t(32 * wave + 8 * u) * 128u);
+    const auto load_w = [&](int b, uint32_t s, int u) {
+        load_lds16(wb + 128u * uint32_t(b < blocks ? b : blocks - 1), w_off[u], lds + s * 32768u + uint32_t(4 * wave + u) * 1024u);
     };
-    const auto load_x = [&](int b, int p, int s, int u) {
-        load_lds16(xb + 128u * uint32_t(b < blocks ? b : blocks - 1), x_off[p][u], x_lds + uint32_t(s) * 16384u + uint32_t(16 * wave + 8 * u) * 128u);
+    const auto load_x = [&](int b, int p, uint32_t s, int u) {
+        load_lds16(xb + 128u * uint32_t(b < blocks ? b : blocks - 1), x_off[p][u], x_lds + s * 16384u + uint32_t(2 * wave + u) * 1024u);
     };
     // scales of groups [s0, s0 + 48) of the tile's rows, a row a lane
     const auto stage_scales = [&](int s0) {
-        const bool is_w = tid < 256;
-        const uint8_t* from = (is_w ? a.ws + (n0 + row_n(tid)) * a.groups : a.xs + (m0 + row_m(tid - 256)) * a.groups) + g0 + s0;
+        const uint8_t* from =
+            (tid < 256 ? a.ws + (n0 + row_n(tid)) * a.groups : a.xs + (m0 + row_m(tid - 256)) * a.groups) + g0 + s0;
         const int left = blocks - s0;
-        uint32_t v[12] = {};
-#pragma unroll
-        for (int j = 0; j < 12; ++j) {
-            if (4 * j + 4 <= left) __builtin_memcpy(&v[j], from + 4 * j, 4);
-            else
-                for (int e = 0; e < 3; ++e)
-                    if (4 * j + e < left) v[j] |= uint32_t(from[4 * j + e]) << (8 * e);
-        }
         lds_u32* to = reinterpret_cast<lds_u32*>(scale_lds + uint32_t(tid) * kScalePitch);
+        uint32_t v[kSegment / 4] = {};
 #pragma unroll
-        for (int j = 0; j < 12; ++j) to[j] = v[j];
+        for (int j = 0; j < kSegment / 4; ++j)
+            if (4 * j + 4 <= left) __builtin_memcpy(&v[j], from + 4 * j, 4);
+#pragma unroll
+        for (int j = 0; j < kSegment / 4; ++j) to[j] = v[j];
+        if (left < kSegment)
+            for (int e = left & ~3; e < left; ++e) reinterpret_cast<lds_u8*>(to)[e] = from[e];
     };
 
     const uint32_t f = uint32_t(c) * 128u + 16u * uint32_t((2 * q) ^ ((c >> 1) & 7));
@@ -413,25 +420,25 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
         const u32x4 lo = *reinterpret_cast<lds_u32x4*>(lo_at), hi = *reinterpret_cast<lds_u32x4*>(hi_at);
         return int8v{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]), int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])};
     };
-    int8v w0[2], w10, w11[2], xf[2][2];     // weights of K half 0, of half 1; tokens [jj][h]
-    int wsc[2][2], xsc[2][2];
-    const auto read_w = [&](int s, int h, int i) {
-        const uint32_t at = uint32_t(s) * 32768u + uint32_t(i) * 4096u;
-        return fragment(w_at[h][0] + at, w_at[h][1] + at);
+    int8v wf[2][2], xf[2][2];     // [h][i], [h][jj]
+    int wsc[2], wsn[2], xsc[2][2];
+    // (flip: 32768 where the block after the current one's is meant, whose stages lie there)
+    const auto read_w = [&](uint32_t flip, int h, int i) {
+        const uint32_t at = uint32_t(i) * 4096u;
+        return fragment((w_at[h][0] ^ flip) + at, (w_at[h][1] ^ flip) + at);
     };
-    const auto read_x = [&](int s, int h, int jj) {
-        const uint32_t at = uint32_t(s) * 16384u + uint32_t(jj) * 4096u;
-        return fragment(x_at[h][0] + at, x_at[h][1] + at);
+    const auto read_x = [&](uint32_t flip, int p, int h, int jj) {
+        const uint32_t at = uint32_t(p) * 16384u + uint32_t(jj) * 4096u;
+        return fragment((x_at[h][0] ^ flip) + at, (x_at[h][1] ^ flip) + at);
     };
-    typedef __attribute__((address_space(3))) uint8_t lds_u8;
     uint32_t ws_at = scale_lds + uint32_t(wn + c) * kScalePitch, xs_at = scale_lds + uint32_t(256 + wt + c) * kScalePitch;
-    const auto read_ws = [&](int buf, uint32_t g) {
+    const auto read_ws = [&](int (&v)[2], uint32_t g) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) wsc[buf][i] = *reinterpret_cast<lds_u8*>(ws_at + g + 32u * kScalePitch * uint32_t(i));
+        for (int i = 0; i < 2; ++i) v[i] = *reinterpret_cast<lds_u8*>(ws_at + g + 32u * kScalePitch * uint32_t(i));
     };
-    const auto read_xs = [&](int buf, uint32_t g, int p) {
+    const auto read_xs = [&](uint32_t g, int p) {
 #pragma unroll
-        for (int jj = 0; jj < 2; ++jj) xsc[buf][jj] = *reinterpret_cast<lds_u8*>(xs_at + g + 32u * kScalePitch * uint32_t(2 * p + jj));
+        for (int jj = 0; jj < 2; ++jj) xsc[p][jj] = *reinterpret_cast<lds_u8*>(xs_at + g + 32u * kScalePitch * uint32_t(2 * p + jj));
     };
 
     float16v acc[2][4];
@@ -454,87 +461,67 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-    w0[0] = read_w(0, 0, 0);
-    w0[1] = read_w(0, 0, 1);
-    xf[0][0] = read_x(0, 0, 0);
-    xf[1][0] = read_x(0, 0, 1);
-    w10 = read_w(0, 1, 0);
-    w11[0] = read_w(0, 1, 1);
-    read_ws(0, 0);
-    read_xs(0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) wf[0][i] = read_w(0, 0, i);
+#pragma unroll
+    for (int jj = 0; jj < 2; ++jj) xf[0][jj] = read_x(0, 0, 0, jj);
+    read_ws(wsc, 0);
+    read_xs(0, 0);
 
-#define FENCE_ __builtin_amdgcn_sched_barrier(0)
-    const auto phase = [&](int b, auto p_c) {
-        constexpr int P = decltype(p_c)::value, bp = P >> 1, p = P & 1, nx = p ^ 1;
-        const auto mfma = [&](const int8v& w, int i, int jj, int h) {
-            acc[i][2 * p + jj] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                w, xf[jj][h], acc[i][2 * p + jj], 0, 0, 0, wsc[bp][i], 0, xsc[p][jj]);
-        };
-        mfma(w0[0], 0, 0, 0);
-        xf[0][1] = read_x(P, 1, 0);
-        FENCE_;
-        mfma(w0[0], 0, 1, 0);
-        xf[1][1] = read_x(P, 1, 1);
-        load_x(p ? b + 2 : b + 1, nx, (P + 3) & 3, 0);
-        FENCE_;
-        if (p) w0[0] = read_w(bp ^ 1, 0, 0);
-        mfma(w0[1], 1, 0, 0);
-        FENCE_;
-        xf[0][0] = read_x((P + 1) & 3, 0, 0);
-        mfma(w0[1], 1, 1, 0);
-        load_x(p ? b + 2 : b + 1, nx, (P + 3) & 3, 1);
-        FENCE_;
-        xf[1][0] = read_x((P + 1) & 3, 0, 1);
-        mfma(w10, 0, 0, 1);
-        if (p) w0[1] = read_w(bp ^ 1, 0, 1);
-        FENCE_;
-        if (p) w11[bp ^ 1] = read_w(bp ^ 1, 1, 1);
-        mfma(w10, 0, 1, 1);
-        load_w(b + 2, bp, 2 * p);
-        FENCE_;
-        if (p) w10 = read_w(bp ^ 1, 1, 0);
-        if (p) {
-            ws_at += 1;
-            xs_at += 1;
-            read_ws(bp ^ 1, 0);
-        }
-        read_xs(nx, 0, nx);
-        mfma(w11[bp], 1, 0, 1);
-        FENCE_;
-        mfma(w11[bp], 1, 1, 1);
-        load_w(b + 2, bp, 2 * p + 1);
-        FENCE_;
-        // all but this phase's own loads are there: what the next phase reads
-        if (p) asm volatile("s_waitcnt vmcnt(4) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        else asm volatile("s_waitcnt vmcnt(4)\n\ts_barrier" ::: "memory");
-        FENCE_;
-    };
-    using C0 = std::integral_constant<int, 0>;
-    using C1 = std::integral_constant<int, 1>;
-    using C2 = std::integral_constant<int, 2>;
-    using C3 = std::integral_constant<int, 3>;
     for (int s0 = 0;;) {
-        const int end = blocks < s0 + kSegment ? blocks : s0 + kSegment;
-        int b = s0;
-        for (; b + 2 <= end; b += 2) {
-            phase(b, C0{});
-            phase(b, C1{});
-            phase(b + 1, C2{});
-            phase(b + 1, C3{});
+    const int end = blocks < s0 + kSegment ? blocks : s0 + kSegment;
+#pragma unroll 1
+    for (int b = s0; b < end; ++b) {
+        const uint32_t par = uint32_t(b) & 1;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            // K half 0, then 1: what a half no longer needs is read for its next use
+            constexpr int E = 4;        // matrix instructions of a half
+#pragma unroll
+            for (int e = 0; e < 2 * E; ++e) {
+                const int h = e / E, i = (e % E) >> 1, jj = e & 1;
+                acc[i][2 * p + jj] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    wf[h][i], xf[h][jj], acc[i][2 * p + jj], 0, 0, 0, wsc[i], 0, xsc[p][jj]);
+                if (e < 2) xf[1][e] = read_x(0, p, 1, e);
+                if (p == 0 && e < E) {
+                    if (e == 1 || e == 2) wf[1][e - 1] = read_w(0, 1, e - 1);
+                }
+                if (p == 0 && e == E) read_xs(0, 1);
+                if (e >= E && e < E + 2) xf[0][e - E] = read_x(p ? 32768u : 0u, p ^ 1, 0, e - E);
+                if (p == 1 && (e == E + 1 || e == E + 2)) wf[0][e - E - 1] = read_w(32768u, 0, e - E - 1);
+                if (p == 1 && e == E) read_ws(wsn, 1);
+                if (p == 1 && e == E + 1) read_xs(1, 0);
+                if (p == 0) {
+                    if (e % 4 == 1) load_x(b + 1, 1, (2 * (par ^ 1)) + 1, e / 4);
+                } else {
+                    if (e % 4 == 1) load_x(b + 2, 0, 2 * par, e / 4);
+                    else if (e % 4 != 3) load_w(b + 2, par, 2 * (e / 4) + (e % 4 == 2));
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            // all but this phase's own loads are there: what the next phase reads
+            if (p) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(6) : "memory");
+            else asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(2) : "memory");
+            __builtin_amdgcn_sched_barrier(0);
         }
-        if (b < end) {
-            phase(b, C0{});
-            phase(b, C1{});
-        }
-        s0 = end;
-        if (s0 >= blocks) break;
-        // (all waves are past the barrier behind their last read of a scale)
-        stage_scales(s0);
-        __syncthreads();
-        ws_at -= kSegment;
-        xs_at -= kSegment;
-        read_ws(0, 0);
-        read_xs(0, 0, 0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) w_at[h][e] ^= 32768u, x_at[h][e] ^= 32768u;
+        ws_at += 1;
+        xs_at += 1;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) wsc[i] = wsn[i];
+    }
+    s0 = end;
+    if (s0 >= blocks) break;
+    __syncthreads();    // (the last reads of scales)
+    stage_scales(s0);
+    __syncthreads();
+    ws_at -= kSegment;
+    xs_at -= kSegment;
+    read_ws(wsc, 0);
+    read_xs(0, 0);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
@@ -545,34 +532,87 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) mine[((i * 4 + j) * 16 + r) * kThreads + tid] = acc[i][j][r];
+                for (int r = 0; r < 16; r += 4)
+                    *reinterpret_cast<float4v*>(mine + (wt + 32 * j + c) * kRows + wn + 32 * i + 2 * r + 4 * q) =
+                        float4v{acc[i][j][r], acc[i][j][r + 1], acc[i][j][r + 2], acc[i][j][r + 3]};
         return;
     }
+    // through LDS, 128 tokens by 64 weight rows a wave, so that a store writes whole
+    // cache lines: chunk e of 8 weight rows of a token in another place for each token
+    asm volatile("s_barrier" ::: "memory");
+        const auto place = [&](int token, int e) { return uint32_t(token) * 128u + 16u * uint32_t(e ^ ((token >> 1) & 7)); };
+    const uint32_t mine = lds + 16384u * uint32_t(wave);
+    const auto pair = [&](float u, float v) {
+        return a.y_dtype == TL_F16 ? f16_bits(u) | f16_bits(v) << 16 : bf16_pair(u, v);
+    };
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            store_tile(acc[i][j], a, n0 + wn + 32 * i, m0 + wt + 32 * j + c, q);
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; g += 2) {
+                const float16v& v = acc[i][j];
+                const auto s0 = __builtin_amdgcn_permlane32_swap(pair(v[4 * g], v[4 * g + 1]), pair(v[4 * g + 4], v[4 * g + 5]), false, false);
+                const auto s1 = __builtin_amdgcn_permlane32_swap(pair(v[4 * g + 2], v[4 * g + 3]), pair(v[4 * g + 6], v[4 * g + 7]), false, false);
+                *reinterpret_cast<lds_u32x4*>(mine + place(32 * j + c, 4 * i + g + q)) = u32x4{s0[0], s1[0], s0[1], s1[1]};
+            }
+    const int64_t n = n0 + wn + 8 * ((l & 7));
+    const bool whole_lines = a.n % 64 == 0;
+#pragma unroll
+    for (int z = 0; z < 16; ++z) {
+        const int r = (8) * z + (l >> 3);
+        const u32x4 v = *reinterpret_cast<lds_u32x4*>(mine + place(r, l & 7));
+        const int64_t token = m0 + wt + r;
+        if (token >= a.m) continue;
+        uint16_t* y = static_cast<uint16_t*>(a.y) + token * a.n + n;
+        if (n + 8 <= a.n) {
+            if (whole_lines) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(y));
+            else __builtin_memcpy(y, &v, 16);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (n + k < a.n) y[k] = uint16_t(v[k >> 1] >> (16 * (k & 1)));
+        }
+    }
 }
 
 // The parts of a tile's sums added in their order
 template <int IT>
-__global__ __launch_bounds__(kThreads) void f8_join_kernel(const Args a) {
+__global__ __launch_bounds__(256) void f8_join_kernel(const Args a) {
     constexpr int kTokens = 64 * IT;
-    const int t = int(blockIdx.x) / (2 * IT), e = int(blockIdx.x) % (2 * IT);
+    // 8 weight rows of a token a lane
+    const int t = int(blockIdx.x) / (kTokens / 8), e = 8 * (int(blockIdx.x) % (kTokens / 8)) + int(threadIdx.x >> 5);
     int64_t m0, n0;
     tile_origin(a, a.whole + t, kTokens, n0, m0);
-    const int tid = threadIdx.x, l = tid & 63, wave = tid >> 6;
-    const float* parts = a.sums + size_t(t) * a.splits * (kRows * kTokens) + size_t(e) * 16 * kThreads + tid;
-    float16v sum;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) sum[r] = parts[r * kThreads];
+    const int64_t token = m0 + e, n = n0 + 8 * (threadIdx.x & 31);
+    if (token >= a.m) return;
+    const float4v* parts = reinterpret_cast<const float4v*>(a.sums + size_t(t) * a.splits * (kRows * kTokens) + e * kRows) + 2 * (threadIdx.x & 31);
+    float4v lo = parts[0], hi = parts[1];
     for (int p = 1; p < a.splits; ++p) {
-        parts += kRows * kTokens;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) sum[r] += parts[r * kThreads];
+        parts += kRows * kTokens / 4;
+        lo += parts[0];
+        hi += parts[1];
     }
-    store_tile(sum, a, n0 + 64 * (wave & 3) + 32 * (e / IT), m0 + 32 * IT * (wave >> 2) + 32 * (e % IT) + (l & 31), l >> 5);
+    const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    if (a.y_dtype == TL_F32) {
+        float* y = static_cast<float*>(a.y) + token * a.n + n;
+        if (n + 8 <= a.n) __builtin_memcpy(y, v, 32);
+        else
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (n + k < a.n) y[k] = v[k];
+        return;
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        w[k] = a.y_dtype == TL_F16 ? f16_bits(v[2 * k]) | f16_bits(v[2 * k + 1]) << 16 : bf16_pair(v[2 * k], v[2 * k + 1]);
+    uint16_t* y = static_cast<uint16_t*>(a.y) + token * a.n + n;
+    if (n + 8 <= a.n) __builtin_memcpy(y, w, 16);
+    else
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (n + k < a.n) y[k] = uint16_t(w[k >> 1] >> (16 * (k & 1)));
 }
 
 struct Plan {
@@ -621,7 +661,7 @@ hipError_t launch(Args a, const Plan& p, hipStream_t stream) {
     hipLaunchKernelGGL(kernel, dim3(unsigned(8 * (a.chunk_a + a.chunk_b))), dim3(kThreads), lds, stream, a);
     if (p.splits > 1) {
         if ((e = hipGetLastError()) != hipSuccess) return e;
-        hipLaunchKernelGGL(f8_join_kernel<IT>, dim3(unsigned(2 * IT * (p.tiles - p.whole))), dim3(kThreads), 0, stream, a);
+        hipLaunchKernelGGL(f8_join_kernel<IT>, dim3(unsigned(8 * IT * (p.tiles - p.whole))), dim3(256), 0, stream, a);
     }
     return hipGetLastError();
 }
