@@ -2,8 +2,34 @@
 //
 //   y[m, n] = sum_k X[m, k] * W[n, k],   X, W = e4m3 code * 2^(scale of its 128)
 //
-// v_mfma_scale_f32_32x32x64_f8f6f4 takes both operands' codes and scales as they
-// are: weights are the A rows, tokens the B columns.
+// Weights are the A rows, tokens the B columns.  binary16 and bfloat16 outputs:
+// v_mfma_scale_f32_32x32x64_f8f6f4 takes codes and scales of both as they are; a
+// scale covers 128 of K, so the two halves of a block of 128 give it twice.  float32
+// outputs: codes times scales widen exactly to bfloat16 and
+// v_mfma_f32_32x32x16_bf16 sums exact products.  (The 8-bit instructions align the
+// products of 8 neighbouring k to the largest exponent among them and keep 14 bits
+// of them, then add in fp32: on normal activations, one in a hundred 20 times
+// larger, sums of 5120 are off by 4.3e-5 of their root mean square, within a tenth
+// of binary16's rounding but 700 times float32's.)
+//
+// Operands go from memory straight into LDS (global_load_lds), 128 bytes of each of
+// 8 rows a load: whole cache lines (half lines cost the address path twice the time,
+// 8192 x 8192 x 8192 438 us against 399).  A row's 128 bytes of a block lie together,
+// its 16-byte pieces exchanged by bits 1 .. 3 of the row, so that 16 rows read at one
+// piece meet all banks.  Waits and barriers are written out: the compiler would make
+// every LDS read wait for every load in flight.  Scales come as they lie in memory,
+// some groups of each row at a time.
+//
+// Two kernels:
+//  - some tokens: 128 weight rows by 32, 64 or 128 tokens, 4 waves, two workgroups on
+//    a compute unit.  Bound by the weights' bytes.
+//  - many: 256 by 256, 8 waves, one workgroup.  Bound by the matrix cores' power: with
+//    zeros for data 8192 x 8192 x 8192 takes 284 us at 2.4 GHz, with random data 405 us
+//    at 1.7 GHz, 72 % of the cycles issuing matrix instructions.
+// Either is cut along K where tiles are few, into parts whose sums a second kernel
+// adds in order.
+#include <cmath>
+
 #include "elem.h"
 #include "f8.h"
 #include "tl_internal.h"
@@ -12,19 +38,14 @@ namespace tl {
 namespace {
 
 using namespace elem;
+using namespace f8;
 
 typedef int int8v __attribute__((ext_vector_type(8)));
 typedef float float4v __attribute__((ext_vector_type(4)));
 typedef float float16v __attribute__((ext_vector_type(16)));
-typedef __bf16 bf2v __attribute__((ext_vector_type(2)));
-typedef __bf16 bf8v __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) uint32_t lds_u32;
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
-
-constexpr int kThreads = 512;    // 8 waves: 4 along the weight rows, 2 along the tokens
-constexpr int kRows = 256;       // weight rows of a tile
-constexpr int kStep = 64;        // K of a step
 
 struct Args {
     const uint8_t *w, *ws, *x, *xs;
@@ -32,22 +53,14 @@ struct Args {
     float* sums;
     int64_t m, n, k;
     int y_dtype, groups;             // groups: K / 128
+    // tiles [0, whole) are computed whole, each later one in `splits` parts; an XCD
+    // (blockIdx % 8) takes runs of chunk_a tiles and chunk_b parts
     int tiles_m, tiles_n, tiles, whole, splits, chunk_a, chunk_b;
 };
 
-// 16 (1) bytes a lane from base + offset to LDS, lane i at `to` + 16 (4) i.
-// Written out, with the waits of the loop: the compiler would make every LDS
-// read wait for every load on the way into LDS.
+// 16 bytes a lane from base + offset to LDS, lane i at `to` + 16 i
 __device__ __forceinline__ void load_lds16(const uint8_t* base, uint32_t offset, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :
-                 : "s"(to), "v"(offset), "s"(base)
-                 : "memory", "m0");
-}
-__device__ __forceinline__ void load_lds1(const uint8_t* base, uint32_t offset, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, %2"
-                 :
-                 : "s"(to), "v"(offset), "s"(base)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base)
                  : "memory", "m0");
 }
 
@@ -57,356 +70,313 @@ __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
                                             uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(u >> 32)))) << 32);
 }
 
-// One 32 x 32 tile of a lane's sums to y: register r of lane (q, c) is weight row
-// 8 (r / 4) + 4 q + r % 4 and token c of the tile
-__device__ __forceinline__ void store_tile(const float16v& acc, const Args& a, int64_t n0, int64_t token, int q) {
-    if (a.y_dtype == TL_F32) {
-        float* y = static_cast<float*>(a.y) + token * a.n;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int64_t n = n0 + 8 * g + 4 * q;
-            const float v[4] = {acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]};
-            if (token >= a.m) continue;
-            if (n + 4 <= a.n) {
-                __builtin_memcpy(y + n, v, 16);
-            } else {
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (n + r < a.n) y[n + r] = v[r];
-            }
-        }
-        return;
+// The work item of a workgroup; false where it has none
+struct Item {
+    int tile, part, slot;   // slot: its place among the parts' sums, or -1
+};
+__device__ __forceinline__ bool find_item(const Args& a, Item& it) {
+    if (int(blockIdx.x) < 8 * a.chunk_a) {
+        it = {int(blockIdx.x & 7) * a.chunk_a + int(blockIdx.x >> 3), 0, -1};
+        return it.tile < a.whole;
     }
-    uint16_t* y = static_cast<uint16_t*>(a.y) + token * a.n;
-    const auto pair = [&](float u, float v) {
-        return a.y_dtype == TL_F16 ? f16_bits(u) | f16_bits(v) << 16 : bf16_pair(u, v);
-    };
-    // the halves of the wave exchange rows, so that each lane has 8 in a row
+    const int u = int(blockIdx.x) - 8 * a.chunk_a;
+    it.slot = (u & 7) * a.chunk_b + (u >> 3);
+    it.tile = a.whole + it.slot / a.splits;
+    it.part = it.slot % a.splits;
+    return it.slot < (a.tiles - a.whole) * a.splits;
+}
+
+// Tiles in bands of four rows of tokens' tiles, those fastest: the 32 that run on an
+// XCD at a time share operands in its L2 (2, 8 and 16 rows: within 1 %)
+template <int ROWS, int TOKENS>
+__device__ __forceinline__ void tile_origin(const Args& a, int tile, int64_t& n0, int64_t& m0) {
+    const int per = 4 * a.tiles_n, band = tile / per, in = tile - band * per;
+    const int high = a.tiles_m - 4 * band < 4 ? a.tiles_m - 4 * band : 4;
+    m0 = int64_t(4 * band + in % high) * TOKENS;
+    n0 = int64_t(in / high) * ROWS;
+}
+
+// Scales of groups [s0, s0 + SEG) of a row (`from`: group s0's; `left` of them are the
+// item's) to LDS
+template <int SEG>
+__device__ __forceinline__ void stage_scales(const uint8_t* from, int left, uint32_t to) {
+    lds_u32* const p = reinterpret_cast<lds_u32*>(to);
+    uint32_t v[SEG / 4] = {};
 #pragma unroll
-    for (int g = 0; g < 4; g += 2) {
-        const auto s0 = __builtin_amdgcn_permlane32_swap(pair(acc[4 * g], acc[4 * g + 1]),
-                                                         pair(acc[4 * g + 4], acc[4 * g + 5]), false, false);
-        const auto s1 = __builtin_amdgcn_permlane32_swap(pair(acc[4 * g + 2], acc[4 * g + 3]),
-                                                         pair(acc[4 * g + 6], acc[4 * g + 7]), false, false);
-        const uint32_t v[4] = {s0[0], s1[0], s0[1], s1[1]};
-        const int64_t n = n0 + 8 * (g + q);
-        if (token >= a.m) continue;
+    for (int j = 0; j < SEG / 4; ++j)
+        if (4 * j + 4 <= left) __builtin_memcpy(&v[j], from + 4 * j, 4);
+#pragma unroll
+    for (int j = 0; j < SEG / 4; ++j) p[j] = v[j];
+    if (left < SEG)
+        for (int e = left & ~3; e < left; ++e) reinterpret_cast<lds_u8*>(p)[e] = from[e];
+}
+
+__device__ __forceinline__ int8v fragment(uint32_t lo_at, uint32_t hi_at) {
+    const u32x4 lo = *reinterpret_cast<lds_u32x4*>(lo_at), hi = *reinterpret_cast<lds_u32x4*>(hi_at);
+    return int8v{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]), int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])};
+}
+
+__device__ __forceinline__ uint32_t pair(int type, float u, float v) {
+    return type == TL_F16 ? f16_bits(u) | f16_bits(v) << 16 : bf16_pair(u, v);
+}
+
+// 8 weight rows of a token to y
+__device__ __forceinline__ void store8_rows(const Args& a, int64_t token, int64_t n, const float (&v)[8]) {
+    if (a.y_dtype == TL_F32) {
+        float* y = static_cast<float*>(a.y) + token * a.n + n;
         if (n + 8 <= a.n) {
-            __builtin_memcpy(y + n, v, 16);
+            __builtin_memcpy(y, v, 32);
         } else {
 #pragma unroll
             for (int r = 0; r < 8; ++r)
-                if (n + r < a.n) y[n + r] = uint16_t(v[r >> 1] >> (16 * (r & 1)));
+                if (n + r < a.n) y[r] = v[r];
         }
+        return;
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) w[r] = pair(a.y_dtype, v[2 * r], v[2 * r + 1]);
+    uint16_t* y = static_cast<uint16_t*>(a.y) + token * a.n + n;
+    if (n + 8 <= a.n) {
+        __builtin_memcpy(y, w, 16);
+    } else {
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            if (n + r < a.n) y[r] = uint16_t(w[r >> 1] >> (16 * (r & 1)));
     }
 }
 
-__device__ __forceinline__ void tile_origin(const Args& a, int tile, int tokens, int64_t& n0, int64_t& m0) {
-    // four rows of tokens' tiles at a time, those fastest
-    const int per = 4 * a.tiles_n, band = tile / per, in = tile - band * per;
-    const int high = a.tiles_m - 4 * band < 4 ? a.tiles_m - 4 * band : 4;
-    m0 = int64_t(4 * band + in % high) * tokens;
-    n0 = int64_t(in / high) * kRows;
+// A 32 x 32 tile of a lane's sums to y: register r of lane (q, c) is weight row
+// 8 (r / 4) + 4 q + r % 4 and token c; the halves of the wave exchange rows so that
+// each lane has 8 in a row
+__device__ __forceinline__ void store_tile(const float16v& acc, const Args& a, int64_t n0, int64_t token, int q) {
+#pragma unroll
+    for (int g = 0; g < 4; g += 2) {
+        float v[8];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            // (copies: a bit cast of a vector's element takes the vector's first)
+            const float lo = acc[4 * g + r], hi = acc[4 * g + 4 + r];
+            const auto s = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi), false, false);
+            const uint32_t s0 = s[0], s1 = s[1];
+            v[r] = __builtin_bit_cast(float, s0);
+            v[4 + r] = __builtin_bit_cast(float, s1);
+        }
+        const int64_t n = n0 + 8 * (g + q);
+        if (token < a.m && n < a.n) store8_rows(a, token, n, v);
+    }
 }
 
-__device__ __forceinline__ bf8v widen(uint32_t a, uint32_t b, float s) {
-    const bf2v p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, s, false);
-    const bf2v p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, s, true);
-    const bf2v p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, s, false);
-    const bf2v p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, s, true);
-    return bf8v{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+// The same to a part's sums: [token][weight row] of a tile of ROWS weight rows
+template <int ROWS>
+__device__ __forceinline__ void store_sums(const float16v& acc, float* sums, int row, int token, int q) {
+#pragma unroll
+    for (int r = 0; r < 16; r += 4)
+        *reinterpret_cast<float4v*>(sums + token * ROWS + row + 2 * r + 4 * q) =
+            float4v{acc[r], acc[r + 1], acc[r + 2], acc[r + 3]};
 }
+
+// The parts of a tile's sums added in their order, 8 weight rows of a token a lane
+template <int ROWS, int TOKENS>
+__global__ __launch_bounds__(256) void f8_join_kernel(const Args a) {
+    constexpr int kPerBlock = 256 / (ROWS / 8), kBlocks = TOKENS / kPerBlock;
+    const int t = int(blockIdx.x) / kBlocks, row = 8 * (int(threadIdx.x) % (ROWS / 8));
+    const int e = kPerBlock * (int(blockIdx.x) % kBlocks) + int(threadIdx.x) / (ROWS / 8);
+    int64_t m0, n0;
+    tile_origin<ROWS, TOKENS>(a, a.whole + t, n0, m0);
+    if (m0 + e >= a.m || n0 + row >= a.n) return;
+    const float* parts = a.sums + size_t(t) * a.splits * (ROWS * TOKENS) + e * ROWS + row;
+    float4v lo = *reinterpret_cast<const float4v*>(parts), hi = *reinterpret_cast<const float4v*>(parts + 4);
+#pragma unroll 4
+    for (int p = 1; p < a.splits; ++p) {
+        lo += *reinterpret_cast<const float4v*>(parts + size_t(p) * (ROWS * TOKENS));
+        hi += *reinterpret_cast<const float4v*>(parts + size_t(p) * (ROWS * TOKENS) + 4);
+    }
+    const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    store8_rows(a, m0 + e, n0 + row, v);
+}
+
+// ---- some tokens: 128 weight rows by 32 IT tokens, a wave 32 of the rows ----
+
+constexpr int kMidThreads = 256, kMidRows = 128;
+constexpr int kMidSegment = 24, kMidPitch = 28;     // groups of scales in LDS, and their bytes a row
+
+// blocks of K in LDS: as many as leave room for two workgroups
+template <int IT>
+constexpr int mid_stages() { return IT == 4 ? 2 : 3; }
+template <int IT>
+constexpr int mid_lds() { return (kMidRows + 32 * IT) * (128 * mid_stages<IT>() + kMidPitch); }
+static_assert(mid_lds<1>() <= 80 * 1024 && mid_lds<2>() <= 80 * 1024 && mid_lds<4>() <= 80 * 1024, "LDS");
 
 template <int IT, bool WIDE>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void f8_gemm_kernel(const Args a) {
-    constexpr int kTokens = 64 * IT;
-    constexpr int kStage = (kRows + kTokens) * kStep, kScaleStage = (kRows + kTokens) * 4;
-    constexpr int kTokenLoads = kTokens / 16, kPerWave = kTokenLoads < 8 ? 1 : kTokenLoads / 8;
-    constexpr int kLoads = 2 + kPerWave;        // of a wave in a step, and one of scales every other step
+__global__ __launch_bounds__(kMidThreads) __attribute__((amdgpu_waves_per_eu(2))) void f8_gemm_mid_kernel(const Args a) {
+    constexpr int kTokens = 32 * IT, kAll = kMidRows + kTokens, kStage = kAll * 128, S = mid_stages<IT>(), kLoads = 4 + IT;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    const uint32_t lds = uint32_t(uintptr_t((__attribute__((address_space(3))) uint8_t*)(smem)));
-    constexpr uint32_t kXStages = 4 * kRows * kStep;
-    const uint32_t scale_lds = lds + 4 * kStage;
-
-    int tile, sp = 0, slot = 0;
-    bool split = false;
-    if (int(blockIdx.x) < 8 * a.chunk_a) {
-        tile = int(blockIdx.x & 7) * a.chunk_a + int(blockIdx.x >> 3);
-        if (tile >= a.whole) return;
-    } else {
-        const int u = int(blockIdx.x) - 8 * a.chunk_a;
-        slot = (u & 7) * a.chunk_b + (u >> 3);
-        if (slot >= (a.tiles - a.whole) * a.splits) return;
-        tile = a.whole + slot / a.splits;
-        sp = slot % a.splits;
-        split = a.splits > 1;
-    }
+    const uint32_t lds = lds_address(smem), scale_lds = lds + S * kStage;
+    Item it;
+    if (!find_item(a, it)) return;
     int64_t m0, n0;
-    tile_origin(a, tile, kTokens, n0, m0);
-    const int g0 = split ? int(int64_t(sp) * a.groups / a.splits) : 0;
-    const int g1 = split ? int(int64_t(sp + 1) * a.groups / a.splits) : a.groups;
-    const int steps = 2 * (g1 - g0);
+    tile_origin<kMidRows, kTokens>(a, it.tile, n0, m0);
+    const int g0 = it.slot < 0 ? 0 : int(int64_t(it.part) * a.groups / a.splits);
+    const int blocks = (it.slot < 0 ? a.groups : int(int64_t(it.part + 1) * a.groups / a.splits)) - g0;
 
     const int tid = threadIdx.x, l = tid & 63, q = l >> 5, c = l & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wn = 64 * (wave & 3), wt = 32 * IT * (wave >> 2);
-
-    // lane i of a load of 1 KB brings 16 bytes of row i / 4 to place i % 4, those
-    // of chunk (i % 4) ^ ((row / 4) % 4): 16 rows read at one chunk meet all banks
-    const uint8_t* const wb = a.w + n0 * a.k + int64_t(g0) * 128;
-    const uint8_t* const xb = a.x + m0 * a.k + int64_t(g0) * 128;
-    const uint8_t* const wsb = a.ws + n0 * a.groups + g0;
-    const uint8_t* const xsb = a.xs + m0 * a.groups + g0;
-    const uint32_t k32 = uint32_t(a.k);
+    const uint8_t* const wb = uniform(a.w + n0 * a.k + int64_t(g0) * 128);
+    const uint8_t* const xb = uniform(a.x + m0 * a.k + int64_t(g0) * 128);
     const int64_t left_n = a.n - n0, left_m = a.m - m0;
     const auto row_n = [&](int r) { return uint32_t(r < left_n ? r : left_n - 1); };   // rows past the end: the last
     const auto row_m = [&](int r) { return uint32_t(r < left_m ? r : left_m - 1); };
-    const uint32_t chunk = 16u * uint32_t((l & 3) ^ ((l >> 4) & 3));
-    uint32_t w_off[2], x_off[kPerWave];
-    uint32_t w_to[2], x_to[kPerWave];
+    uint32_t off[kLoads];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        w_off[u] = row_n(32 * wave + 16 * u + (l >> 2)) * k32 + chunk;
-        w_to[u] = uint32_t(32 * wave + 16 * u) * kStep;
+    for (int u = 0; u < kLoads; ++u) {
+        const int r = 8 * (u < 4 ? 4 * wave + u : IT * wave + u - 4) + (l >> 3);
+        off[u] = (u < 4 ? row_n(r) : row_m(r)) * uint32_t(a.k) + 16u * uint32_t((l & 7) ^ ((r >> 1) & 7));
     }
+    const auto load = [&](int b, uint32_t stage) {      // (past the last block: that one again)
+        const uint32_t at = 128u * uint32_t(b < blocks ? b : blocks - 1), to = lds + stage * kStage;
 #pragma unroll
-    for (int u = 0; u < kPerWave; ++u) {
-        const int first = 16 * ((kPerWave * wave + u) % kTokenLoads);
-        x_off[u] = row_m(first + (l >> 2)) * k32 + chunk;
-        x_to[u] = kXStages + uint32_t(first) * kStep;
-    }
-    const int sw = wave % (4 + IT);     // 64 rows' scales
-    const bool s_w = sw < 4;
-    const uint8_t* const sb = s_w ? wsb : xsb;
-    const uint32_t s_off = (s_w ? row_n(64 * sw + l) : row_m(64 * (sw - 4) + l)) * uint32_t(a.groups);
-    const uint32_t s_to = scale_lds + 256u * uint32_t(sw);
+        for (int u = 0; u < kLoads; ++u)
+            load_lds16((u < 4 ? wb : xb) + at, off[u], to + 1024u * uint32_t(u < 4 ? 4 * wave + u : 16 + IT * wave + u - 4));
+    };
+    const auto all_scales = [&](int s0) {
+        const int r = tid - kMidRows;
+        if (tid < kAll)
+            stage_scales<kMidSegment>((r < 0 ? a.ws + (n0 + row_n(tid)) * a.groups : a.xs + (m0 + row_m(r)) * a.groups) + g0 + s0,
+                                      blocks - s0, scale_lds + uint32_t(tid) * kMidPitch);
+    };
+    static_assert(kAll <= kMidThreads, "a row of scales a lane");
+    const uint32_t f = uint32_t(c) * 128u + 16u * uint32_t((2 * q) ^ ((c >> 1) & 7));
+    const auto half = [&](uint32_t at, int h) { return fragment(at + (f ^ (64u * h)), at + (f ^ (64u * h) ^ 16u)); };
 
-    // load u of step t (past the end: of the last one again)
-    const auto load_w = [&](int t, int stage, int u) {
-        const uint32_t at = uint32_t(t < steps ? t : steps - 1) * kStep;
-        load_lds16(wb + at, w_off[u], lds + uint32_t(stage) * kRows * kStep + w_to[u]);
-    };
-    const auto load_x = [&](int t, int stage, int u) {
-        const uint32_t at = uint32_t(t < steps ? t : steps - 1) * kStep;
-        load_lds16(xb + at, x_off[u], lds + uint32_t(stage) * kTokens * kStep + x_to[u]);
-    };
-    const auto load_scales = [&](int t, int stage) {
-        const uint32_t g = uint32_t(t < steps ? t : steps - 1) >> 1;
-        load_lds1(sb + g, s_off, s_to + uint32_t(stage) * kScaleStage);
-    };
-
-    // a lane's fragment of a 32-row tile: 32 bytes of row c, at 32 q
-    const uint32_t f0 = uint32_t(c) * kStep + 16u * uint32_t((2 * q) ^ ((c >> 2) & 3));
-    const uint32_t w_at = lds + uint32_t(wn) * kStep + f0, x_at = lds + kXStages + uint32_t(wt) * kStep + f0;
-    const uint32_t w_at1 = w_at ^ 16u, x_at1 = x_at ^ 16u;
-    const uint32_t ws_at = scale_lds + 4u * uint32_t(wn + c), xs_at = scale_lds + 4u * uint32_t(kRows + wt + c);
-    const auto fragment = [&](uint32_t lo_at, uint32_t hi_at) {
-        const u32x4 lo = *reinterpret_cast<lds_u32x4*>(lo_at), hi = *reinterpret_cast<lds_u32x4*>(hi_at);
-        return int8v{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]), int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])};
-    };
-
-    int8v wf[2][2], xf[IT];
-    int wsc[2][2], xsc[IT];
-    const auto read_w = [&](int buf, int stage, int i) {
-        const uint32_t at = uint32_t(stage) * kRows * kStep + 32u * kStep * uint32_t(i);
-        wf[buf][i] = fragment(w_at + at, w_at1 + at);
-    };
-    const auto read_x = [&](int stage, int j) {
-        const uint32_t at = uint32_t(stage) * kTokens * kStep + 32u * kStep * uint32_t(j);
-        xf[j] = fragment(x_at + at, x_at1 + at);
-    };
-    const auto read_ws = [&](int buf, int stage) {
-        const uint32_t at = uint32_t(stage) * kScaleStage;
+    float16v acc[IT];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) wsc[buf][i] = int(*reinterpret_cast<lds_u32*>(ws_at + at + 128u * uint32_t(i)));
-    };
-    const auto read_xs = [&](int stage, int j) {
-        const uint32_t at = uint32_t(stage) * kScaleStage;
-        xsc[j] = int(*reinterpret_cast<lds_u32*>(xs_at + at + 128u * uint32_t(j)));
-    };
-
-    float16v acc[2][IT];
+    for (int j = 0; j < IT; ++j)
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+        for (int r = 0; r < 16; ++r) acc[j][r] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < IT; ++j)
+    for (int b = 0; b < S - 1; ++b) load(b, b);
+    all_scales(0);
+    uint32_t stage = 0, fill = S - 1;
+    for (int s0 = 0;;) {
+        const int end = blocks < s0 + kMidSegment ? blocks : s0 + kMidSegment;
+        uint32_t sc = scale_lds + uint32_t(c) * kMidPitch;
+#pragma unroll 1
+        for (int b = s0; b < end; ++b, ++sc) {
+            // this wave's loads of block b are there and its reads of b - 1 done; then everyone's
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLoads * (S - 2)) : "memory");
+            __builtin_amdgcn_sched_barrier(0);
+            load(b + S - 1, fill);
+            fill = fill == S - 1 ? 0 : fill + 1;
+            const uint32_t at = lds + stage * kStage;
+            stage = stage == S - 1 ? 0 : stage + 1;
+            const int ws = *reinterpret_cast<lds_u8*>(sc + 32u * uint32_t(wave) * kMidPitch);
+            int xs[IT];
 #pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-
-    load_scales(0, 0);
+            for (int j = 0; j < IT; ++j) xs[j] = *reinterpret_cast<lds_u8*>(sc + uint32_t(kMidRows + 32 * j) * kMidPitch);
 #pragma unroll
-    for (int t = 0; t < 3; ++t) {
+            for (int h = 0; h < 2; ++h) {
+                const int8v wf = half(at + 4096u * uint32_t(wave), h);
+                bf8v wv[4];
+                if constexpr (WIDE) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) load_w(t, t, u);
+                    for (int e = 0; e < 4; ++e) wv[e] = widen(uint32_t(wf[2 * e]), uint32_t(wf[2 * e + 1]), uint32_t(ws));
+                }
 #pragma unroll
-        for (int u = 0; u < kPerWave; ++u) load_x(t, t, u);
-    }
-    load_scales(2, 1);
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-    read_ws(0, 0);
+                for (int j = 0; j < IT; ++j) {
+                    const int8v xf = half(at + 128u * uint32_t(kMidRows + 32 * j), h);
+                    if constexpr (WIDE) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) read_w(0, 0, i);
-#pragma unroll
-    for (int j = 0; j < IT; ++j) read_xs(0, j), read_x(0, j);
-
-    const auto step = [&](int t, auto s_c) {
-        constexpr int S = decltype(s_c)::value, cur = S & 1, nxt = cur ^ 1, group = S >> 1;
-#pragma unroll
-        for (int j = 0; j < IT; ++j) {
-            if constexpr (WIDE) {
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const bf8v xv = widen(uint32_t(xf[j][2 * h]), uint32_t(xf[j][2 * h + 1]),
-                                          __builtin_bit_cast(float, xsc[j] << 23));
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                    const bf8v wv = widen(uint32_t(wf[cur][i][2 * h]), uint32_t(wf[cur][i][2 * h + 1]),
-                                  __builtin_bit_cast(float, wsc[group][i] << 23));
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wv, xv, acc[i][j], 0, 0, 0);
+                        for (int e = 0; e < 4; ++e)
+                            acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                                wv[e], widen(uint32_t(xf[2 * e]), uint32_t(xf[2 * e + 1]), uint32_t(xs[j])), acc[j], 0, 0, 0);
+                    } else {
+                        acc[j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf, xf, acc[j], 0, 0, 0, ws, 0, xs[j]);
                     }
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                        wf[cur][i], xf[j], acc[i][j], 0, 0, 0, wsc[group][i], 0, xsc[j]);
             }
-            if (j == 0) {
-                if (S & 1) read_ws(group ^ 1, group ^ 1);
-                read_w(nxt, (S + 1) & 3, 0);
-                read_w(nxt, (S + 1) & 3, 1);
-            }
-            if (S & 1) read_xs(group ^ 1, j);
-            read_x((S + 1) & 3, j);
-            constexpr int D = IT == 4 ? 0 : 0;
-            if (j == D || IT == 1) load_w(t + 3, (S + 3) & 3, 0), load_w(t + 3, (S + 3) & 3, 1);
-            if (IT == 1) load_x(t + 3, (S + 3) & 3, 0);
-            if (IT > 1 && j == D + 1) {
-#pragma unroll
-                for (int u = 0; u < kPerWave; ++u) load_x(t + 3, (S + 3) & 3, u);
-            }
-            if (S & 1 && j == IT - 1) load_scales(t + 3, ((S + 3) >> 1) & 1);
-            __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
-        // all but this step's own loads are there: what the next step reads
-        if (S & 1) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kLoads + 1) : "memory");
-        else asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kLoads) : "memory");
-        __builtin_amdgcn_sched_barrier(0);
-    };
-    using C0 = std::integral_constant<int, 0>;
-    using C1 = std::integral_constant<int, 1>;
-    using C2 = std::integral_constant<int, 2>;
-    using C3 = std::integral_constant<int, 3>;
-    int t = 0;
-    for (; t + 4 <= steps; t += 4) {
-        step(t, C0{});
-        step(t + 1, C1{});
-        step(t + 2, C2{});
-        step(t + 3, C3{});
+        s0 = end;
+        if (s0 >= blocks) break;
+        __syncthreads();    // (the last reads of scales; the next block's barrier follows their writes)
+        all_scales(s0);
     }
-    if (t < steps) {
-        step(t, C0{});
-        step(t + 1, C1{});
-    }
-    // loads into stages nobody reads may still be on the way: wait for them before
-    // the workgroup's LDS goes to another
+    // no load may write LDS that belongs to another workgroup
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-
-    if (split) {
-        float* mine = a.sums + size_t(slot) * (kRows * kTokens);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < IT; ++j)
-#pragma unroll
-                for (int r = 0; r < 16; r += 4)
-                    *reinterpret_cast<float4v*>(mine + (wt + 32 * j + c) * kRows + wn + 32 * i + 2 * r + 4 * q) =
-                        float4v{acc[i][j][r], acc[i][j][r + 1], acc[i][j][r + 2], acc[i][j][r + 3]};
-        return;
+    for (int j = 0; j < IT; ++j) {
+        if (it.slot >= 0) store_sums<kMidRows>(acc[j], a.sums + size_t(it.slot) * (kMidRows * kTokens), 32 * wave, 32 * j + c, q);
+        else store_tile(acc[j], a, n0 + 32 * wave, m0 + 32 * j + c, q);
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < IT; ++j)
-            store_tile(acc[i][j], a, n0 + wn + 32 * i, m0 + wt + 32 * j + c, q);
 }
 
-// ---- many tokens: 256 x 256 tiles, 8-bit matrix instructions ----
+// ---- many tokens: 256 x 256, a wave 64 weight rows by 128 tokens ----
+//
+// K goes in blocks of 128, each in two phases of 64 of the wave's 128 tokens; a phase
+// is 8 matrix instructions (2 x 2 tiles of 32 x 32, two halves of the block).  LDS
+// holds two blocks of weights and four phases' tokens; a phase requests the tokens of
+// the third phase after it, a block's second phase the weights of the block after the
+// next, into the stages whose last readers are behind the barrier before.  Fragments
+// are single: what a half of the block no longer needs is read for its next use, half
+// a phase ahead, so that matrix instructions wait for no LDS latency.  (Four waves of
+// 128 x 128 read a third less from LDS and take as long; 16 x 16 x 128 instructions
+// draw less power and take as long too.)
 
-constexpr int kScalePitch = 52;      // LDS bytes of a row's scales: 48, and 4 so that rows meet different banks
-constexpr int kSegment = 48;         // groups whose scales are in LDS at a time
-constexpr int kBigLds = 2 * 32768 + 4 * 16384 + 512 * kScalePitch;
+constexpr int kThreads = 512, kRows = 256, kTokens = 256;
+constexpr int kSegment = 48, kPitch = 52;       // groups of scales in LDS, and their bytes a row
+constexpr int kBigLds = 2 * 32768 + 4 * 16384 + 512 * kPitch;
+
+template <bool WIDE>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void f8_gemm_big_kernel(const Args a) {
-    constexpr int kTokens = 256;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    const uint32_t lds = uint32_t(uintptr_t((__attribute__((address_space(3))) uint8_t*)(smem)));
-    const uint32_t x_lds = lds + 65536, scale_lds = lds + 131072;
-
-    int tile, sp = 0, slot = 0;
-    bool split = false;
-    if (int(blockIdx.x) < 8 * a.chunk_a) {
-        tile = int(blockIdx.x & 7) * a.chunk_a + int(blockIdx.x >> 3);
-        if (tile >= a.whole) return;
-    } else {
-        const int u = int(blockIdx.x) - 8 * a.chunk_a;
-        slot = (u & 7) * a.chunk_b + (u >> 3);
-        if (slot >= (a.tiles - a.whole) * a.splits) return;
-        tile = a.whole + slot / a.splits;
-        sp = slot % a.splits;
-        split = a.splits > 1;
-    }
+    const uint32_t lds = lds_address(smem), x_lds = lds + 65536, scale_lds = lds + 131072;
+    Item it;
+    if (!find_item(a, it)) return;
     int64_t m0, n0;
-    tile_origin(a, tile, kTokens, n0, m0);
-    const int g0 = split ? int(int64_t(sp) * a.groups / a.splits) : 0;
-    const int g1 = split ? int(int64_t(sp + 1) * a.groups / a.splits) : a.groups;
-    const int blocks = g1 - g0;
+    tile_origin<kRows, kTokens>(a, it.tile, n0, m0);
+    const int g0 = it.slot < 0 ? 0 : int(int64_t(it.part) * a.groups / a.splits);
+    const int blocks = (it.slot < 0 ? a.groups : int(int64_t(it.part + 1) * a.groups / a.splits)) - g0;
 
     const int tid = threadIdx.x, l = tid & 63, q = l >> 5, c = l & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wn = 64 * (wave & 3), half = wave >> 2, wt = 128 * half;
-
+    const int wn = 64 * (wave & 3), side = wave >> 2, wt = 128 * side;
     const uint8_t* const wb = uniform(a.w + n0 * a.k + int64_t(g0) * 128);
     const uint8_t* const xb = uniform(a.x + m0 * a.k + int64_t(g0) * 128);
     const uint32_t k32 = uint32_t(a.k);
     const int64_t left_n = a.n - n0, left_m = a.m - m0;
     const auto row_n = [&](int r) { return uint32_t(r < left_n ? r : left_n - 1); };   // rows past the end: the last
     const auto row_m = [&](int r) { return uint32_t(r < left_m ? r : left_m - 1); };
+
+    // loads: the weights' 256 rows of a block four a wave, a phase's 2 x 64 tokens two
     uint32_t w_off[4], x_off[2][2];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-        w_off[u] = row_n(8 * (4 * wave + u) + (l >> 3)) * k32 + 16u * uint32_t((l & 7) ^ (4 * (u & 1) + (l >> 4)));
+    for (int u = 0; u < 4; ++u) {
+        const int r = 8 * (4 * wave + u) + (l >> 3);
+        w_off[u] = row_n(r) * k32 + 16u * uint32_t((l & 7) ^ ((r >> 1) & 7));
+    }
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int r = 8 * (2 * wave + u) + (l >> 3);
-            x_off[p][u] = row_m(128 * (r >> 6) + 64 * p + (r & 63)) * k32 + 16u * uint32_t((l & 7) ^ (4 * (u & 1) + (l >> 4)));
+            x_off[p][u] = row_m(128 * (r >> 6) + 64 * p + (r & 63)) * k32 + 16u * uint32_t((l & 7) ^ ((r >> 1) & 7));
         }
-    const auto load_w = [&](int b, uint32_t s, int u) {
+    const auto load_w = [&](int b, uint32_t s, int u) {     // (past the last block: that one again)
         load_lds16(wb + 128u * uint32_t(b < blocks ? b : blocks - 1), w_off[u], lds + s * 32768u + uint32_t(4 * wave + u) * 1024u);
     };
     const auto load_x = [&](int b, int p, uint32_t s, int u) {
         load_lds16(xb + 128u * uint32_t(b < blocks ? b : blocks - 1), x_off[p][u], x_lds + s * 16384u + uint32_t(2 * wave + u) * 1024u);
     };
-    // scales of groups [s0, s0 + 48) of the tile's rows, a row a lane
-    const auto stage_scales = [&](int s0) {
-        const uint8_t* from =
-            (tid < 256 ? a.ws + (n0 + row_n(tid)) * a.groups : a.xs + (m0 + row_m(tid - 256)) * a.groups) + g0 + s0;
-        const int left = blocks - s0;
-        lds_u32* to = reinterpret_cast<lds_u32*>(scale_lds + uint32_t(tid) * kScalePitch);
-        uint32_t v[kSegment / 4] = {};
-#pragma unroll
-        for (int j = 0; j < kSegment / 4; ++j)
-            if (4 * j + 4 <= left) __builtin_memcpy(&v[j], from + 4 * j, 4);
-#pragma unroll
-        for (int j = 0; j < kSegment / 4; ++j) to[j] = v[j];
-        if (left < kSegment)
-            for (int e = left & ~3; e < left; ++e) reinterpret_cast<lds_u8*>(to)[e] = from[e];
+    const auto all_scales = [&](int s0) {
+        const int r = tid - kRows;
+        stage_scales<kSegment>((r < 0 ? a.ws + (n0 + row_n(tid)) * a.groups : a.xs + (m0 + row_m(r)) * a.groups) + g0 + s0,
+                               blocks - s0, scale_lds + uint32_t(tid) * kPitch);
     };
 
+    // a lane's fragment of 32 rows and half a block: 32 bytes of row c, at 64 h + 32 q.
+    // Stages of odd blocks lie 32768 further; the addresses are turned over each block,
+    // and `next` reads the other ones.
     const uint32_t f = uint32_t(c) * 128u + 16u * uint32_t((2 * q) ^ ((c >> 1) & 7));
     uint32_t w_at[2][2], x_at[2][2];
 #pragma unroll
@@ -414,31 +384,26 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             w_at[h][e] = lds + uint32_t(wn) * 128u + (f ^ (64u * h) ^ (16u * e));
-            x_at[h][e] = x_lds + uint32_t(half) * 8192u + (f ^ (64u * h) ^ (16u * e));
+            x_at[h][e] = x_lds + uint32_t(side) * 8192u + (f ^ (64u * h) ^ (16u * e));
         }
-    const auto fragment = [&](uint32_t lo_at, uint32_t hi_at) {
-        const u32x4 lo = *reinterpret_cast<lds_u32x4*>(lo_at), hi = *reinterpret_cast<lds_u32x4*>(hi_at);
-        return int8v{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]), int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])};
+    int8v wf[2][2], xf[2][2];       // [half of the block][tile]
+    int wsc[2], wsn[2], xsc[2][2];  // scales: weights, of the next block, tokens of each phase
+    const auto read_w = [&](bool next, int h, int i) {
+        const uint32_t at = uint32_t(i) * 4096u, x = next ? 32768u : 0u;
+        wf[h][i] = fragment((w_at[h][0] ^ x) + at, (w_at[h][1] ^ x) + at);
     };
-    int8v wf[2][2], xf[2][2];     // [h][i], [h][jj]
-    int wsc[2], wsn[2], xsc[2][2];
-    // (flip: 32768 where the block after the current one's is meant, whose stages lie there)
-    const auto read_w = [&](uint32_t flip, int h, int i) {
-        const uint32_t at = uint32_t(i) * 4096u;
-        return fragment((w_at[h][0] ^ flip) + at, (w_at[h][1] ^ flip) + at);
+    const auto read_x = [&](bool next, int p, int h, int j) {
+        const uint32_t at = uint32_t(p) * 16384u + uint32_t(j) * 4096u, x = next ? 32768u : 0u;
+        xf[h][j] = fragment((x_at[h][0] ^ x) + at, (x_at[h][1] ^ x) + at);
     };
-    const auto read_x = [&](uint32_t flip, int p, int h, int jj) {
-        const uint32_t at = uint32_t(p) * 16384u + uint32_t(jj) * 4096u;
-        return fragment((x_at[h][0] ^ flip) + at, (x_at[h][1] ^ flip) + at);
-    };
-    uint32_t ws_at = scale_lds + uint32_t(wn + c) * kScalePitch, xs_at = scale_lds + uint32_t(256 + wt + c) * kScalePitch;
+    uint32_t ws_at = scale_lds + uint32_t(wn + c) * kPitch, xs_at = scale_lds + uint32_t(kRows + wt + c) * kPitch;
     const auto read_ws = [&](int (&v)[2], uint32_t g) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) v[i] = *reinterpret_cast<lds_u8*>(ws_at + g + 32u * kScalePitch * uint32_t(i));
+        for (int i = 0; i < 2; ++i) v[i] = *reinterpret_cast<lds_u8*>(ws_at + g + 32u * kPitch * uint32_t(i));
     };
     const auto read_xs = [&](uint32_t g, int p) {
 #pragma unroll
-        for (int jj = 0; jj < 2; ++jj) xsc[p][jj] = *reinterpret_cast<lds_u8*>(xs_at + g + 32u * kScalePitch * uint32_t(2 * p + jj));
+        for (int j = 0; j < 2; ++j) xsc[p][j] = *reinterpret_cast<lds_u8*>(xs_at + g + 32u * kPitch * uint32_t(2 * p + j));
     };
 
     float16v acc[2][4];
@@ -457,94 +422,114 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
         for (int u = 0; u < 2; ++u) load_x(t >> 1, t & 1, t, u);
 #pragma unroll
     for (int u = 0; u < 4; ++u) load_w(1, 1, u);
-    stage_scales(0);
+    all_scales(0);
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) wf[0][i] = read_w(0, 0, i);
-#pragma unroll
-    for (int jj = 0; jj < 2; ++jj) xf[0][jj] = read_x(0, 0, 0, jj);
+    for (int i = 0; i < 2; ++i) read_w(false, 0, i), read_x(false, 0, 0, i);
     read_ws(wsc, 0);
     read_xs(0, 0);
 
     for (int s0 = 0;;) {
-    const int end = blocks < s0 + kSegment ? blocks : s0 + kSegment;
+        const int end = blocks < s0 + kSegment ? blocks : s0 + kSegment;
 #pragma unroll 1
-    for (int b = s0; b < end; ++b) {
-        const uint32_t par = uint32_t(b) & 1;
+        for (int b = s0; b < end; ++b) {
+            const uint32_t odd = uint32_t(b) & 1;
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            // K half 0, then 1: what a half no longer needs is read for its next use
-            constexpr int E = 4;        // matrix instructions of a half
+            for (int p = 0; p < 2; ++p) {
 #pragma unroll
-            for (int e = 0; e < 2 * E; ++e) {
-                const int h = e / E, i = (e % E) >> 1, jj = e & 1;
-                acc[i][2 * p + jj] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    wf[h][i], xf[h][jj], acc[i][2 * p + jj], 0, 0, 0, wsc[i], 0, xsc[p][jj]);
-                if (e < 2) xf[1][e] = read_x(0, p, 1, e);
-                if (p == 0 && e < E) {
-                    if (e == 1 || e == 2) wf[1][e - 1] = read_w(0, 1, e - 1);
+                for (int e = 0; e < 8; ++e) {
+                    const int h = e >> 2;
+                    if constexpr (WIDE) {       // the half in four slices of 16, all four tiles of each
+                        bf8v wv[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            wv[i] = widen(uint32_t(wf[h][i][2 * (e & 3)]), uint32_t(wf[h][i][2 * (e & 3) + 1]), uint32_t(wsc[i]));
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const bf8v xv = widen(uint32_t(xf[h][j][2 * (e & 3)]), uint32_t(xf[h][j][2 * (e & 3) + 1]), uint32_t(xsc[p][j]));
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                acc[i][2 * p + j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wv[i], xv, acc[i][2 * p + j], 0, 0, 0);
+                        }
+                    } else {
+                        const int i = (e >> 1) & 1, j = e & 1;
+                        acc[i][2 * p + j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                            wf[h][i], xf[h][j], acc[i][2 * p + j], 0, 0, 0, wsc[i], 0, xsc[p][j]);
+                    }
+                    // reads, of registers that are free and stages that are full: the
+                    // block's second half early in a phase, the next phase's (and block's)
+                    // first half once this one's is done
+                    if (e < 2) read_x(false, p, 1, e);
+                    if (p == 0) {
+                        if (e == 1 || e == 2) read_w(false, 1, e - 1);
+                        if (e == 4) read_xs(0, 1);
+                        if (e == 4 || e == 5) read_x(false, 1, 0, e - 4);
+                    } else {
+                        if (e == 4) read_ws(wsn, 1);
+                        if (e == 4 || e == 5) read_x(true, 0, 0, e - 4);
+                        if (e == 5 || e == 6) read_w(true, 0, e - 5);
+                        if (e == 5) read_xs(1, 0);
+                    }
+                    // loads: tokens three phases ahead, weights two blocks
+                    if (p == 0) {
+                        if (e % 4 == 1) load_x(b + 1, 1, 2 * (odd ^ 1) + 1, e / 4);
+                    } else {
+                        if (e % 4 == 1) load_x(b + 2, 0, 2 * odd, e / 4);
+                        else if (e % 4 != 3) load_w(b + 2, odd, 2 * (e / 4) + (e % 4 == 2));
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                if (p == 0 && e == E) read_xs(0, 1);
-                if (e >= E && e < E + 2) xf[0][e - E] = read_x(p ? 32768u : 0u, p ^ 1, 0, e - E);
-                if (p == 1 && (e == E + 1 || e == E + 2)) wf[0][e - E - 1] = read_w(32768u, 0, e - E - 1);
-                if (p == 1 && e == E) read_ws(wsn, 1);
-                if (p == 1 && e == E + 1) read_xs(1, 0);
-                if (p == 0) {
-                    if (e % 4 == 1) load_x(b + 1, 1, (2 * (par ^ 1)) + 1, e / 4);
-                } else {
-                    if (e % 4 == 1) load_x(b + 2, 0, 2 * par, e / 4);
-                    else if (e % 4 != 3) load_w(b + 2, par, 2 * (e / 4) + (e % 4 == 2));
-                }
+                // all but this phase's own loads are there: what the next phase reads
+                if (p) asm volatile("s_waitcnt vmcnt(6)\n\ts_barrier" ::: "memory");
+                else asm volatile("s_waitcnt vmcnt(2)\n\ts_barrier" ::: "memory");
                 __builtin_amdgcn_sched_barrier(0);
             }
-            // all but this phase's own loads are there: what the next phase reads
-            if (p) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(6) : "memory");
-            else asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(2) : "memory");
-            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) w_at[h][e] ^= 32768u, x_at[h][e] ^= 32768u;
+            ws_at += 1;
+            xs_at += 1;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) wsc[i] = wsn[i];
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) w_at[h][e] ^= 32768u, x_at[h][e] ^= 32768u;
-        ws_at += 1;
-        xs_at += 1;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) wsc[i] = wsn[i];
-    }
-    s0 = end;
-    if (s0 >= blocks) break;
-    __syncthreads();    // (the last reads of scales)
-    stage_scales(s0);
-    __syncthreads();
-    ws_at -= kSegment;
-    xs_at -= kSegment;
-    read_ws(wsc, 0);
-    read_xs(0, 0);
+        s0 = end;
+        if (s0 >= blocks) break;
+        __syncthreads();    // (the last reads of scales)
+        all_scales(s0);
+        __syncthreads();
+        ws_at -= kSegment;
+        xs_at -= kSegment;
+        read_ws(wsc, 0);
+        read_xs(0, 0);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
-    if (split) {
-        float* mine = a.sums + size_t(slot) * (kRows * kTokens);
+    if (it.slot >= 0) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int r = 0; r < 16; r += 4)
-                    *reinterpret_cast<float4v*>(mine + (wt + 32 * j + c) * kRows + wn + 32 * i + 2 * r + 4 * q) =
-                        float4v{acc[i][j][r], acc[i][j][r + 1], acc[i][j][r + 2], acc[i][j][r + 3]};
+                store_sums<kRows>(acc[i][j], a.sums + size_t(it.slot) * (kRows * kTokens), wn + 32 * i, wt + 32 * j + c, q);
         return;
     }
-    // through LDS, 128 tokens by 64 weight rows a wave, so that a store writes whole
-    // cache lines: chunk e of 8 weight rows of a token in another place for each token
+    if constexpr (WIDE) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) store_tile(acc[i][j], a, n0 + wn + 32 * i, m0 + wt + 32 * j + c, q);
+        return;
+    }
+    // through LDS, 128 tokens by 64 weight rows a wave, so that a store writes whole cache
+    // lines: piece e of 8 weight rows of a token in place e ^ (token / 2) % 8.  Straight
+    // from the registers, 32 bytes of a token a store, 4096 x 17408 x 5120 takes 328 us
+    // instead of 309; lines that are whole are stored past the caches' replacement order
+    // (304; rows of 32003 are slower that way, 144 against 138 for 1000 tokens).
     asm volatile("s_barrier" ::: "memory");
-        const auto place = [&](int token, int e) { return uint32_t(token) * 128u + 16u * uint32_t(e ^ ((token >> 1) & 7)); };
+    const auto place = [&](int token, int e) { return uint32_t(token) * 128u + 16u * uint32_t(e ^ ((token >> 1) & 7)); };
     const uint32_t mine = lds + 16384u * uint32_t(wave);
-    const auto pair = [&](float u, float v) {
-        return a.y_dtype == TL_F16 ? f16_bits(u) | f16_bits(v) << 16 : bf16_pair(u, v);
-    };
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -552,15 +537,16 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 #pragma unroll
             for (int g = 0; g < 4; g += 2) {
                 const float16v& v = acc[i][j];
-                const auto s0 = __builtin_amdgcn_permlane32_swap(pair(v[4 * g], v[4 * g + 1]), pair(v[4 * g + 4], v[4 * g + 5]), false, false);
-                const auto s1 = __builtin_amdgcn_permlane32_swap(pair(v[4 * g + 2], v[4 * g + 3]), pair(v[4 * g + 6], v[4 * g + 7]), false, false);
+                const int t = a.y_dtype;
+                const auto s0 = __builtin_amdgcn_permlane32_swap(pair(t, v[4 * g], v[4 * g + 1]), pair(t, v[4 * g + 4], v[4 * g + 5]), false, false);
+                const auto s1 = __builtin_amdgcn_permlane32_swap(pair(t, v[4 * g + 2], v[4 * g + 3]), pair(t, v[4 * g + 6], v[4 * g + 7]), false, false);
                 *reinterpret_cast<lds_u32x4*>(mine + place(32 * j + c, 4 * i + g + q)) = u32x4{s0[0], s1[0], s0[1], s1[1]};
             }
-    const int64_t n = n0 + wn + 8 * ((l & 7));
+    const int64_t n = n0 + wn + 8 * (l & 7);
     const bool whole_lines = a.n % 64 == 0;
 #pragma unroll
     for (int z = 0; z < 16; ++z) {
-        const int r = (8) * z + (l >> 3);
+        const int r = 8 * z + (l >> 3);
         const u32x4 v = *reinterpret_cast<lds_u32x4*>(mine + place(r, l & 7));
         const int64_t token = m0 + wt + r;
         if (token >= a.m) continue;
@@ -576,114 +562,105 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     }
 }
 
-// The parts of a tile's sums added in their order
-template <int IT>
-__global__ __launch_bounds__(256) void f8_join_kernel(const Args a) {
-    constexpr int kTokens = 64 * IT;
-    // 8 weight rows of a token a lane
-    const int t = int(blockIdx.x) / (kTokens / 8), e = 8 * (int(blockIdx.x) % (kTokens / 8)) + int(threadIdx.x >> 5);
-    int64_t m0, n0;
-    tile_origin(a, a.whole + t, kTokens, n0, m0);
-    const int64_t token = m0 + e, n = n0 + 8 * (threadIdx.x & 31);
-    if (token >= a.m) return;
-    const float4v* parts = reinterpret_cast<const float4v*>(a.sums + size_t(t) * a.splits * (kRows * kTokens) + e * kRows) + 2 * (threadIdx.x & 31);
-    float4v lo = parts[0], hi = parts[1];
-    for (int p = 1; p < a.splits; ++p) {
-        parts += kRows * kTokens / 4;
-        lo += parts[0];
-        hi += parts[1];
-    }
-    const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-    if (a.y_dtype == TL_F32) {
-        float* y = static_cast<float*>(a.y) + token * a.n + n;
-        if (n + 8 <= a.n) __builtin_memcpy(y, v, 32);
-        else
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (n + k < a.n) y[k] = v[k];
-        return;
-    }
-    uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        w[k] = a.y_dtype == TL_F16 ? f16_bits(v[2 * k]) | f16_bits(v[2 * k + 1]) << 16 : bf16_pair(v[2 * k], v[2 * k + 1]);
-    uint16_t* y = static_cast<uint16_t*>(a.y) + token * a.n + n;
-    if (n + 8 <= a.n) __builtin_memcpy(y, w, 16);
-    else
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (n + k < a.n) y[k] = uint16_t(w[k >> 1] >> (16 * (k & 1)));
-}
+// ---- which kernel, and how K is cut ----
 
 struct Plan {
-    int it, splits;
+    int it;             // 32 it tokens a tile of 128 weight rows; 8: the 256 x 256 kernel
+    int splits;
     int64_t tiles_m, tiles_n, tiles, whole;
+    int64_t sums() const { return splits > 1 ? (tiles - whole) * splits * (it == 8 ? 65536 : 4096 * it) * 4 : 0; }
 };
 
-constexpr int64_t kMaxParts = 512;
+constexpr int64_t kMostSums = int64_t(1) << 28;
 
-Plan make_plan(int64_t m, int64_t n, int64_t k) {
-    Plan p;
-    p.it = m <= 64 ? 1 : m <= 128 ? 2 : 4;
-    p.tiles_m = (m + 64 * p.it - 1) / (64 * p.it);
-    p.tiles_n = (n + kRows - 1) / kRows;
-    p.tiles = p.tiles_m * p.tiles_n;
-    const int64_t cus = cu_count(), rem = p.tiles % cus, groups = k / 128;
-    p.whole = p.tiles;
-    p.splits = 1;
-    double best = double(groups);
-    for (int s = 2; rem && s <= 32 && s <= groups / 2 && rem * s <= kMaxParts; ++s) {
-        const double cost = double((rem * s + cus - 1) / cus) * (double((groups + s - 1) / s) + 1.0) + 0.02 * double(rem * s) + 2.0;
-        if (cost < best - 1.0) {
-            best = cost;
-            p.whole = p.tiles - rem;
-            p.splits = s;
+// The plan with the least estimated time, in us: MODEL
+Plan make_plan(int64_t m, int64_t n, int64_t k, bool wide) {
+    static const double kEach[2][4] = {{0.42, 0.50, 0.65, 1.6}, {0.50, 0.65, 1.0, 2.9}};
+    static const double kAlone[2][4] = {{0.60, 0.68, 1.0, 1.6}, {0.65, 0.85, 1.4, 2.9}};
+    const int64_t cus = cu_count(), groups = k / 128;
+    Plan best = {};
+    double least = 0;
+    for (const int it : {1, 2, 4, 8}) {
+        const bool big = it == 8;
+        Plan p;
+        p.it = it;
+        p.tiles_m = (m + 32 * it - 1) / (32 * it);
+        p.tiles_n = big ? (n + kRows - 1) / kRows : (n + kMidRows - 1) / kMidRows;
+        p.tiles = p.tiles_m * p.tiles_n;
+        if (it > 1 && 16 * it >= m) break;      // (half the tokens or more of every tile absent)
+        const int i = it == 1 ? 0 : it == 2 ? 1 : it == 4 ? 2 : 3, rows = big ? kRows : kMidRows;
+        for (p.splits = 1; p.splits <= 16 && p.splits <= groups; ++p.splits) {
+            // the large kernel cuts only the tiles of the last, partial round
+            p.whole = p.splits == 1 ? p.tiles : big ? p.tiles / cus * cus : 0;
+            if (p.sums() > kMostSums) break;
+            const double whole = double(p.splits > 1 ? p.whole : p.tiles), cut = double(p.tiles * p.splits) - whole * p.splits;
+            const double part = std::ceil(double(groups) / p.splits);
+            const double each = kEach[wide][i], alone = kAlone[wide][i];
+            const double in_whole = std::ceil(whole / cus), in_cut = p.splits > 1 ? std::ceil(cut / cus) : 0.0;
+            // blocks of the busiest compute unit, one workgroup after the other or side by side
+            double us = in_whole + in_cut == 1 ? (in_whole * groups + in_cut * part) * alone
+                                               : (in_whole * groups + in_cut * part) * each;
+            // operands from memory, and to the compute units from the caches
+            const double mean = (whole * groups + (p.splits > 1 ? cut * part : 0.0)) / cus;
+            const double uneven = 0.5 + 0.5 * (in_whole * groups + in_cut * part) / mean;
+            us = std::fmax(us, double(n + m) * k / 5.2e6 * uneven);
+            us = std::fmax(us, double(p.tiles) * (rows + 32 * it) * k / 10e6);
+            if (p.splits > 1) us += 3.0 + 0.2 * p.splits + 2 * double(p.sums()) / 5e6;
+            if (least == 0 || us < least) {
+                least = us;
+                best = p;
+            }
         }
     }
-    return p;
+    return best;
 }
 
-template <int IT, bool WIDE>
-hipError_t launch(Args a, const Plan& p, hipStream_t stream) {
-    constexpr bool kBig = IT == 4 && !WIDE;
-    const auto kernel = kBig ? f8_gemm_big_kernel : f8_gemm_kernel<IT, kBig || WIDE>;
-    constexpr int lds = kBig ? kBigLds : 4 * (kRows + 64 * IT) * kStep + 2 * (kRows + 64 * IT) * 4;
+template <int ROWS, int TOKENS>
+hipError_t run(void (*kernel)(const Args), int threads, int lds, Args a, const Plan& p, hipStream_t stream) {
     hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), lds);
     if (e != hipSuccess) return e;
-    const int64_t items = (p.tiles - p.whole) * p.splits;
+    const int64_t cut = p.tiles - p.whole;
     a.tiles_m = int(p.tiles_m);
     a.tiles_n = int(p.tiles_n);
     a.tiles = int(p.tiles);
     a.whole = int(p.whole);
     a.splits = p.splits;
     a.chunk_a = int((p.whole + 7) / 8);
-    a.chunk_b = int((items + 7) / 8);
-    hipLaunchKernelGGL(kernel, dim3(unsigned(8 * (a.chunk_a + a.chunk_b))), dim3(kThreads), lds, stream, a);
-    if (p.splits > 1) {
+    a.chunk_b = int((cut * p.splits + 7) / 8);
+    hipLaunchKernelGGL(kernel, dim3(unsigned(8 * (a.chunk_a + a.chunk_b))), dim3(threads), lds, stream, a);
+    if (cut) {
         if ((e = hipGetLastError()) != hipSuccess) return e;
-        hipLaunchKernelGGL(f8_join_kernel<IT>, dim3(unsigned(8 * IT * (p.tiles - p.whole))), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((f8_join_kernel<ROWS, TOKENS>), dim3(unsigned(cut * (ROWS * TOKENS / 2048))), dim3(256), 0, stream, a);
     }
     return hipGetLastError();
 }
 
-constexpr int64_t kFewTokens = 64;
+template <bool WIDE>
+hipError_t run(const Args& a, const Plan& p, hipStream_t stream) {
+    switch (p.it) {
+        case 1: return run<kMidRows, 32>(f8_gemm_mid_kernel<1, WIDE>, kMidThreads, mid_lds<1>(), a, p, stream);
+        case 2: return run<kMidRows, 64>(f8_gemm_mid_kernel<2, WIDE>, kMidThreads, mid_lds<2>(), a, p, stream);
+        case 4: return run<kMidRows, 128>(f8_gemm_mid_kernel<4, WIDE>, kMidThreads, mid_lds<4>(), a, p, stream);
+    }
+    return run<kRows, kTokens>(f8_gemm_big_kernel<WIDE>, kThreads, kBigLds, a, p, stream);
+}
 
 }  // namespace
 
 int64_t f8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-    if (m <= kFewTokens) return 0;
-    const Plan p = make_plan(m, n, k);
-    return p.splits > 1 ? (p.tiles - p.whole) * p.splits * kRows * 64 * p.it * 4 : 0;
+    if (f8_gemv_fits(m)) return 0;
+    const int64_t a = make_plan(m, n, k, false).sums(), b = make_plan(m, n, k, true).sums();
+    return a > b ? a : b;
 }
 
 hipError_t launch_f8_gemm(const uint8_t* codes, const uint8_t* scales, const uint8_t* x, const uint8_t* x_scales,
                           int64_t m, int64_t n, int64_t k, void* y, int y_dtype, void* ws, hipStream_t stream) {
-    if (m <= kFewTokens) return launch_f8_gemv(codes, scales, x, x_scales, m, n, k, y, y_dtype, stream);
-    const Plan p = make_plan(m, n, k);
-    const Args a = {codes, scales, x, x_scales, y, static_cast<float*>(ws), m, n, k, y_dtype, int(k / 128), 0, 0, 0, 0, 0, 0, 0};
-    if (y_dtype == TL_F32)
-        return p.it == 1 ? launch<1, true>(a, p, stream) : p.it == 2 ? launch<2, true>(a, p, stream) : launch<4, true>(a, p, stream);
-    return p.it == 1 ? launch<1, false>(a, p, stream) : p.it == 2 ? launch<2, false>(a, p, stream) : launch<4, false>(a, p, stream);
+    if (f8_gemv_fits(m)) return launch_f8_gemv(codes, scales, x, x_scales, m, n, k, y, y_dtype, stream);
+    const bool wide = y_dtype == TL_F32;
+    const Plan p = make_plan(m, n, k, wide);
+    const Args a = {codes, scales, x, x_scales, y, static_cast<float*>(ws), m, n, k, y_dtype, int(k / 128),
+                    0, 0, 0, 0, 0, 0, 0};
+    return wide ? run<true>(a, p, stream) : run<false>(a, p, stream);
 }
 
 }  // namespace tl

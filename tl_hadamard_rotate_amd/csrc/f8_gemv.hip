@@ -2,22 +2,29 @@
 //
 //   y[m, n] = sum_k X[m, k] * W[n, k],   X, W = e4m3 code * 2^(scale of its 128)
 //
-// A code has 4 significant bits, so code * scale is a bfloat16 number (while it
-// lies within bfloat16's range): one conversion instruction makes two of them,
-// scale included, and v_mfma_f32_16x16x32_bf16 multiplies them exactly and sums
-// in fp32.  (The 8-bit matrix instructions sum 8 products at a time with 14 bits
-// below the largest of them; few tokens are bound by the weights' bytes, so
-// nothing is gained by them here.)
+// code * scale is a bfloat16 number: one instruction makes two of them, and
+// v_mfma_f32_16x16x32_bf16 multiplies them exactly and sums in fp32.  (The 8-bit
+// matrix instructions sum 8 products at a time with 14 bits below the largest of
+// them; few tokens are bound by the weights' bytes, so they gain nothing here.)
 //
-// 16 weight rows are the A rows, 16 tokens the B columns (absent tokens repeat
-// the last).  Lane (q, c) = (lane / 16, lane % 16) holds 32 bytes of row c of a
-// chunk of 128, at 32 q: which of the chunk's places a matrix instruction sums is
-// free as long as both operands agree.
+// 16 weight rows are the A rows, 16 tokens the B columns (absent tokens repeat the
+// last).  Lane (q, c) = (lane / 16, lane % 16) takes 32 bytes of row c of a chunk
+// of 128, at 32 q: which of the chunk's places a matrix instruction sums is free as
+// long as both operands agree.
 //
-// A wave goes through the chunks of one tile of 16 rows, the next kDepth of them
-// on the way to registers; where rows are few, ks waves share a tile, each a run
-// of the chunks, and add their sums in LDS in a fixed order.  Scales, one byte of
-// each of 16 rows a chunk, come 64 chunks at a time through the wave's own LDS.
+// Every wave works on its own: R tiles of 16 weight rows, a run of K's chunks, and
+// a ring of D of them in its own LDS, filled by loads that write LDS directly and
+// whose waits are counted by hand (through registers, with the compiler's waits, a
+// wave had hardly more than one chunk on the way: 17408 x 5120 of one token 43 us,
+// now 20).  A load takes whole cache lines, 128 bytes of each of 8 rows.  The
+// activations of a chunk come through the same ring.  A workgroup is the `ks` waves
+// that share a tile, each a run of the chunks; their sums meet in LDS in order.
+// Scales, one byte of each row a chunk, come 32 chunks at a time.
+//
+// Bound: the weights' bytes from HBM.  In a graph, weights not in the caches: 131072
+// x 5120 of one token 108 us (6.2 TB/s), 17408 x 5120 of one 20 us, of sixteen 24,
+// 5120 x 17408 of one 21, 1024 x 5120 of one 6.0 (bound by one wave's loads, one
+// after another).
 #include "elem.h"
 #include "f8.h"
 #include "tl_internal.h"
@@ -26,15 +33,17 @@ namespace tl {
 namespace {
 
 using namespace elem;
+using namespace f8;
 
-typedef __bf16 bf2v __attribute__((ext_vector_type(2)));
-typedef __bf16 bf8v __attribute__((ext_vector_type(8)));
 typedef float float4v __attribute__((ext_vector_type(4)));
-typedef unsigned int uint4v __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef __attribute__((address_space(3))) float4v lds_float4;
 
-constexpr int kWaves = 8;        // of a workgroup
-constexpr int kSegment = 64;     // chunks whose scales a wave holds at a time
-constexpr int kScaleRow = 80;    // bytes of a row of them in LDS: 16-byte aligned, 16 rows on different banks
+constexpr int kDepth = 3;        // chunks of the ring
+constexpr int kSegment = 32;     // chunks whose scales a wave holds at a time
+constexpr int kScaleRow = 48;    // LDS bytes of a row of them: 8-byte aligned, 16 rows on different banks
 
 struct Args {
     const uint8_t *codes, *scales, *x, *xs;
@@ -43,147 +52,173 @@ struct Args {
     int m, y_dtype, chunks, ks;
 };
 
-// 8 codes times the scale whose biased exponent is in s's exponent field
-__device__ __forceinline__ bf8v widen(uint32_t a, uint32_t b, float s) {
-    const bf2v p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, s, false);
-    const bf2v p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, s, true);
-    const bf2v p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, s, false);
-    const bf2v p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, s, true);
-    return bf8v{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+// 16 bytes a lane from its address to LDS, lane i at `to` + 16 i.  Written out: the
+// compiler would make every read of LDS wait for every load on the way there.
+template <bool NT>
+__device__ __forceinline__ void load_lds16(const uint8_t* from, uint32_t to) {
+    if (NT) asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt" ::"s"(to), "v"(from) : "memory", "m0");
+    else asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory", "m0");
 }
 
-// scales [s0, s0 + 64) of 16 rows to the wave's LDS: lane 4 r + p brings 16 of row
-// r (row pointer `from`, of this lane's row), as a whole where the row has them
-__device__ __forceinline__ void stage_scales(const uint8_t* from, int s0, int chunks, uint8_t* lds, int l) {
-    const int i = s0 + 16 * (l & 3);
-    uint32_t w[4] = {};
-    if (i + 16 <= chunks) {
-        __builtin_memcpy(w, from + i, 16);
+// scales [s0, s0 + 32) of 16 rows to LDS: lane 4 r + p brings 8 of row r, `from`
+// being that row's; where the row ends in a word, the row's last word is shifted
+__device__ __forceinline__ void stage_scales(const uint8_t* from, int s0, int chunks, uint32_t lds, int l) {
+    const int i = s0 + 8 * (l & 3);
+    uint32_t w[2] = {};
+    if (chunks >= 4) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int at = i + 4 * j, in = at < chunks - 4 ? at : chunks - 4, off = at - in < 3 ? at - in : 3;
+            uint32_t v;
+            __builtin_memcpy(&v, from + in, 4);
+            w[j] = v >> (8 * off);
+        }
     } else {
-        for (int j = 0; j < 16; ++j)
-            if (i + j < chunks) w[j >> 2] |= uint32_t(from[i + j]) << (8 * (j & 3));
+        for (int j = 0; j < 3; ++j)
+            if (i + j < chunks) w[0] |= uint32_t(from[i + j]) << (8 * j);
     }
-    *reinterpret_cast<uint4v*>(lds + kScaleRow * (l >> 2) + 16 * (l & 3)) = uint4v{w[0], w[1], w[2], w[3]};
+    *reinterpret_cast<lds_u32x2*>(lds + kScaleRow * uint32_t(l >> 2) + 8u * uint32_t(l & 3)) = u32x2{w[0], w[1]};
 }
 
-template <int MT, int D>
-__global__ __launch_bounds__(64 * kWaves) void f8_gemv_kernel(const Args a) {
-    constexpr int kScaleBytes = 16 * kScaleRow;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[kWaves * (1 + MT) * kScaleBytes];
-    static_assert(kWaves * MT * 1024 <= int(sizeof(smem)), "the sums of the waves take the scales' place");
+template <int R, int XI>
+constexpr int wave_bytes() { return kDepth * (2 * R + XI) * 1024 + 16 * kScaleRow * (R + 1); }
+
+// R tiles of 16 weight rows a wave, XI loads of 8 tokens
+template <int R, int XI>
+__global__ __launch_bounds__(512) void f8_gemv_kernel(const Args a) {
+    constexpr int kLoads = 2 * R + XI, kSlot = kLoads * 1024, kWave = wave_bytes<R, XI>();
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const int l = threadIdx.x & 63, q = l >> 4, c = l & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int part = wave % a.ks;
-    const int64_t n0 = 16 * (int64_t(blockIdx.x) * (kWaves / a.ks) + wave / a.ks);
-    const int m0 = 16 * MT * blockIdx.y;
-
+    const uint32_t ring = lds_address(smem) + uint32_t(wave) * kWave, scales = ring + kDepth * kSlot;
+    const int64_t n0 = 16 * R * int64_t(blockIdx.x);
     const auto row = [&](int i) { return n0 + i < a.n ? n0 + i : a.n - 1; };
-    const auto token = [&](int i) { return m0 + i < a.m ? m0 + i : a.m - 1; };
-    const uint8_t* wp = a.codes + row(c) * a.k + 32 * q;
-    const uint8_t* xp[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) xp[t] = a.x + token(16 * t + c) * a.k + 32 * q;
+    const auto token = [&](int i) { return int64_t(i < a.m ? i : a.m - 1); };
 
-    float4v acc[MT] = {};
-    uint4v wr[D][2], xr[D][MT][2];
-    const auto load = [&](int i, int64_t chunk) {
-        wr[i][0] = __builtin_nontemporal_load(reinterpret_cast<const uint4v*>(wp + 128 * chunk));
-        wr[i][1] = __builtin_nontemporal_load(reinterpret_cast<const uint4v*>(wp + 128 * chunk + 16));
+    // lane i of a load brings the piece of row i / 8 that belongs in place i % 8, piece
+    // (i % 8) ^ (row / 2) % 8: 16 rows read at one piece meet all banks
+    const int c0 = int(int64_t(wave) * a.chunks / a.ks), c1 = int(int64_t(wave + 1) * a.chunks / a.ks);
+    const uint8_t* wp[2 * R];
+    const uint8_t* xp[XI];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            xr[i][t][0] = *reinterpret_cast<const uint4v*>(xp[t] + 128 * chunk);
-            xr[i][t][1] = *reinterpret_cast<const uint4v*>(xp[t] + 128 * chunk + 16);
-        }
+    for (int u = 0; u < 2 * R; ++u)
+        wp[u] = a.codes + row(8 * u + (l >> 3)) * a.k + 16 * ((l & 7) ^ (4 * (u & 1) + (l >> 4))) + 128 * int64_t(c0);
+#pragma unroll
+    for (int u = 0; u < XI; ++u)
+        xp[u] = a.x + token(8 * u + (l >> 3)) * a.k + 16 * ((l & 7) ^ (4 * (u & 1) + (l >> 4))) + 128 * int64_t(c0);
+    const auto load = [&](int t, uint32_t slot) {       // chunk t of the wave's (past them: the last again)
+        const int64_t at = 128 * int64_t(t < c1 - c0 ? t : c1 - c0 - 1);
+#pragma unroll
+        for (int u = 0; u < 2 * R; ++u) load_lds16<true>(wp[u] + at, slot + 1024u * u);
+#pragma unroll
+        for (int u = 0; u < XI; ++u) load_lds16<false>(xp[u] + at, slot + 1024u * (2 * R + u));
     };
+    // (of 8 tokens the lanes from 8 on read the first again, and drop what they get)
+    const int ct = XI == 1 ? c & 7 : c;
+    const uint32_t fw = uint32_t(c) * 128u + 16u * uint32_t((2 * q) ^ ((c >> 1) & 7));
+    const uint32_t fx = uint32_t(ct) * 128u + 16u * uint32_t((2 * q) ^ ((ct >> 1) & 7)) + 2048u * R;
 
-    uint8_t* const scales = smem + wave * (1 + MT) * kScaleBytes;
-    const int c0 = int(int64_t(part) * a.chunks / a.ks), c1 = int(int64_t(part + 1) * a.chunks / a.ks);
+    float4v acc[R] = {};
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i) load(i, ring + uint32_t(i) * kSlot);
+    uint32_t slot = ring;
     for (int s0 = c0; s0 < c1; s0 += kSegment) {
         const int s1 = s0 + kSegment < c1 ? s0 + kSegment : c1;
-        stage_scales(a.scales + row(l >> 2) * a.chunks, s0, a.chunks, scales, l);
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-            stage_scales(a.xs + int64_t(token(16 * t + (l >> 2))) * a.chunks, s0, a.chunks, scales + (1 + t) * kScaleBytes, l);
+        for (int r = 0; r < R; ++r)
+            stage_scales(a.scales + row(16 * r + (l >> 2)) * a.chunks, s0, a.chunks, scales + 16 * kScaleRow * r, l);
+        stage_scales(a.xs + token(l >> 2) * a.chunks, s0, a.chunks, scales + 16 * kScaleRow * R, l);
+        uint32_t sw_at = scales + kScaleRow * uint32_t(c), sx_at = scales + kScaleRow * uint32_t(16 * R + ct);
+#pragma unroll 1
+        for (int t = s0; t < s1; ++t, ++sw_at, ++sx_at) {
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads * (kDepth - 1)) : "memory");
+            u32x4 w[R][2], x[2];
+            uint32_t sw[R];
 #pragma unroll
-        for (int i = 0; i < D; ++i) load(i, s0 + i < s1 ? s0 + i : s1 - 1);
-        for (int b = s0; b < s1; b += D) {
+            for (int e = 0; e < 2; ++e) {
 #pragma unroll
-            for (int i = 0; i < D; ++i) {
-                if (b + i < s1) {
-                    const uint8_t* s = scales + kScaleRow * c + (b + i - s0);
-                    const float sw = __builtin_bit_cast(float, uint32_t(*s) << 23);
-                    bf8v w[4];
+                for (int r = 0; r < R; ++r) w[r][e] = *reinterpret_cast<lds_u32x4*>(slot + (fw ^ (16u * e)) + 2048u * r);
+                x[e] = *reinterpret_cast<lds_u32x4*>(slot + (fx ^ (16u * e)));
+            }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) w[j] = widen(wr[i][j >> 1][2 * (j & 1)], wr[i][j >> 1][2 * (j & 1) + 1], sw);
+            for (int r = 0; r < R; ++r) sw[r] = *reinterpret_cast<lds_u8*>(sw_at + 16 * kScaleRow * r);
+            const uint32_t sx = *reinterpret_cast<lds_u8*>(sx_at);
+            // what the slot held is in registers before the ring's next chunk takes its place
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+            load(t - c0 + kDepth, slot);
+            slot = slot == ring + (kDepth - 1) * kSlot ? ring : slot + kSlot;
 #pragma unroll
-                    for (int t = 0; t < MT; ++t) {
-                        const float sx = __builtin_bit_cast(float, uint32_t(s[(1 + t) * kScaleBytes]) << 23);
+            for (int h = 0; h < 4; ++h) {
+                const bf8v xv = widen(x[h >> 1][2 * (h & 1)], x[h >> 1][2 * (h & 1) + 1], sx);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                w[j], widen(xr[i][t][j >> 1][2 * (j & 1)], xr[i][t][j >> 1][2 * (j & 1) + 1], sx), acc[t],
-                                0, 0, 0);
-                    }
-                }
-                load(i, b + i + D < s1 ? b + i + D : s1 - 1);
+                for (int r = 0; r < R; ++r)
+                    acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        widen(w[r][h >> 1][2 * (h & 1)], w[r][h >> 1][2 * (h & 1) + 1], sw[r]), xv, acc[r], 0, 0, 0);
             }
         }
     }
+    // no load may write LDS once its place is used otherwise, or another workgroup's
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
-    // lane (q, c) holds rows 4 q .. 4 q + 3 of the tile for token c
     if (a.ks > 1) {
-        float4v* sums = reinterpret_cast<float4v*>(smem);
         __syncthreads();
 #pragma unroll
-        for (int t = 0; t < MT; ++t) sums[(wave * MT + t) * 64 + l] = acc[t];
+        for (int r = 0; r < R; ++r) *reinterpret_cast<lds_float4*>(ring + 1024u * r + 16u * l) = acc[r];
         __syncthreads();
-        if (part) return;
+        if (wave) return;
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-            for (int p = 1; p < a.ks; ++p) acc[t] += sums[((wave + p) * MT + t) * 64 + l];
+        for (int r = 0; r < R; ++r)
+            for (int p = 1; p < a.ks; ++p) acc[r] += *reinterpret_cast<lds_float4*>(ring + p * kWave + 1024u * r + 16u * l);
     }
+    // lane (q, c) holds rows 4 q .. 4 q + 3 of a tile for token c
+    const int64_t m = c;
+    if (m >= a.m) return;
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-        const int64_t m = m0 + 16 * t + c;
-        if (m >= a.m) continue;
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int64_t n = n0 + 4 * q + r;
+        for (int e = 0; e < 4; ++e) {
+            const int64_t n = n0 + 16 * r + 4 * q + e;
             if (n >= a.n) continue;
-            if (a.y_dtype == TL_F32) static_cast<float*>(a.y)[m * a.n + n] = acc[t][r];
+            if (a.y_dtype == TL_F32) static_cast<float*>(a.y)[m * a.n + n] = acc[r][e];
             else
                 static_cast<uint16_t*>(a.y)[m * a.n + n] =
-                    uint16_t(a.y_dtype == TL_F16 ? f16_bits(acc[t][r]) : bf16_bits(acc[t][r]));
+                    uint16_t(a.y_dtype == TL_F16 ? f16_bits(acc[r][e]) : bf16_bits(acc[r][e]));
         }
-    }
 }
 
-template <int MT, int D>
-void launch(const Args& all, int64_t m, hipStream_t stream) {
-    const int64_t tiles = (all.n + 15) / 16, step = 65535 * 16 * MT;
-    for (int64_t m0 = 0; m0 < m; m0 += step) {   // (the grid's second dimension ends at 65535)
-        Args a = all;
-        a.m = int(m - m0 < step ? m - m0 : step);
-        a.x += m0 * a.k;
-        a.xs += m0 * a.chunks;
-        a.y = static_cast<uint8_t*>(a.y) + m0 * a.n * (a.y_dtype == TL_F32 ? 4 : 2);
-        const int64_t per = kWaves / a.ks;
-        hipLaunchKernelGGL((f8_gemv_kernel<MT, D>), dim3(unsigned((tiles + per - 1) / per), unsigned((a.m + 16 * MT - 1) / (16 * MT))),
-                           dim3(64 * kWaves), 0, stream, a);
-    }
+template <int R, int XI>
+hipError_t launch(Args a, int64_t waves, hipStream_t stream) {
+    const auto kernel = f8_gemv_kernel<R, XI>;
+    const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), 160 * 1024);
+    if (e != hipSuccess) return e;
+    const int64_t tiles = (a.n + 16 * R - 1) / (16 * R);
+    constexpr int most = 160 * 1024 / wave_bytes<R, XI>();
+    int64_t ks = (waves + tiles / 2) / tiles;
+    ks = ks > 8 ? 8 : ks;
+    ks = ks > most ? most : ks;
+    ks = ks > a.chunks ? a.chunks : ks;
+    a.ks = ks < 1 ? 1 : int(ks);
+    hipLaunchKernelGGL(kernel, dim3(unsigned(tiles)), dim3(64 * a.ks), unsigned(a.ks * wave_bytes<R, XI>()), stream, a);
+    return hipGetLastError();
 }
 
 }  // namespace
 
+bool f8_gemv_fits(int64_t m) { return m <= 16; }
+
+// Waves share a tile until there are about 1024 (512 where each brings 16 tokens'
+// activations too); from 320 tiles on, two tiles a wave share those.  Measured, us in
+// a graph with 1 .. 8 waves a tile: 17408 x 5120 of one token 19.7 20.4 21.0 20.3
+// .. 24, 5120 x 17408 36 25 21.1 21.3 .. 23, 1024 x 5120 14 8.6 7.0 6.2 6.0 6.2 ..;
+// sixteen tokens, one and two tiles: 32003 x 5120 36.9 and 34.6, 5120 x 17408 27 and
+// 25.4, 1024 x 5120 7.3 and 8.5.
 hipError_t launch_f8_gemv(const uint8_t* codes, const uint8_t* scales, const uint8_t* x, const uint8_t* x_scales,
                           int64_t m, int64_t n, int64_t k, void* y, int y_dtype, hipStream_t stream) {
-    Args a = {codes, scales, x, x_scales, y, n, k, 0, y_dtype, int(k / 128), 1};
-    const int64_t tiles = (n + 15) / 16;
-    while (a.ks < kWaves && tiles * a.ks < 8 * cu_count() && 2 * a.ks <= a.chunks) a.ks *= 2;
-    if (m <= 16) launch<1, 4>(a, m, stream);
-    else if (m <= 32) launch<2, 3>(a, m, stream);
-    else launch<4, 2>(a, m, stream);
-    return hipGetLastError();
+    if (!f8_gemv_fits(m)) return hipErrorInvalidValue;
+    const Args a = {codes, scales, x, x_scales, y, n, k, int(m), y_dtype, int(k / 128), 1};
+    if (m <= 8) return launch<1, 1>(a, 1024, stream);
+    return n >= 16 * 320 ? launch<2, 2>(a, 512, stream) : launch<1, 2>(a, 512, stream);
 }
 
 }  // namespace tl
