@@ -773,34 +773,57 @@ def adjust_logits(logits, history=None, history_lens=None, prompt_lens=None, rep
     Ids outside the vocabulary are padding.  ``out`` may be logits itself."""
     dt, shape, index = _rows(logits, "logits")
     m, v = shape
-    od = dt if out_dtype is None else _out_type(out_dtype)
+    if out_dtype is None:
+        out_dtype, od = logits.dtype, dt
+    else:
+        od = _out_type(out_dtype)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or logits.dtype, device=logits.device)
-    elif not (isinstance(out, torch.Tensor) and out.dtype is (out_dtype or logits.dtype) and out.shape == shape and
+        out = torch.empty(shape, dtype=out_dtype, device=logits.device)
+    elif not (isinstance(out, torch.Tensor) and out.dtype is out_dtype and out.shape == shape and
               out.get_device() == index and out.is_contiguous()):
-        _refuse(out, "out", out_dtype or logits.dtype, shape, index)
-    row = (m,)
+        _refuse(out, "out", out_dtype, shape, index)
     h = b = 0
-    hp = ip = vp = mp = None
-    each = []
+    hp = lp = pp = rp = ep = fp = ip = vp = mp = None
     if history is not None:
         if not (isinstance(history, torch.Tensor) and history.dtype is _I32 and history.dim() == 2 and
                 history.shape[0] == m and history.get_device() == index and history.is_contiguous()):
             _refuse(history, "history", _I32, (m, "H"), index)
         h = history.shape[1]
-        hp = history.data_ptr()
-    for name, t, dtype in (("history_lens", history_lens, _I32), ("prompt_lens", prompt_lens, _I32),
-                           ("repetition", repetition, _F32), ("presence", presence, _F32),
-                           ("frequency", frequency, _F32)):
-        if t is None:
-            each.append(None)
-            continue
-        if history is None:
-            raise ValueError(f"{name} needs a history")
-        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == row and t.get_device() == index and
-                t.is_contiguous()):
-            _refuse(t, name, dtype, row, index)
-        each.append(t.data_ptr() if h else None)    # (an empty history has no address)
+        row = (m,)
+        if history_lens is not None:
+            if not (isinstance(history_lens, torch.Tensor) and history_lens.dtype is _I32 and
+                    history_lens.shape == row and history_lens.get_device() == index and
+                    history_lens.is_contiguous()):
+                _refuse(history_lens, "history_lens", _I32, row, index)
+            lp = history_lens.data_ptr()
+        if prompt_lens is not None:
+            if not (isinstance(prompt_lens, torch.Tensor) and prompt_lens.dtype is _I32 and
+                    prompt_lens.shape == row and prompt_lens.get_device() == index and
+                    prompt_lens.is_contiguous()):
+                _refuse(prompt_lens, "prompt_lens", _I32, row, index)
+            pp = prompt_lens.data_ptr()
+        if repetition is not None:
+            if not (isinstance(repetition, torch.Tensor) and repetition.dtype is _F32 and
+                    repetition.shape == row and repetition.get_device() == index and
+                    repetition.is_contiguous()):
+                _refuse(repetition, "repetition", _F32, row, index)
+            rp = repetition.data_ptr()
+        if presence is not None:
+            if not (isinstance(presence, torch.Tensor) and presence.dtype is _F32 and presence.shape == row and
+                    presence.get_device() == index and presence.is_contiguous()):
+                _refuse(presence, "presence", _F32, row, index)
+            ep = presence.data_ptr()
+        if frequency is not None:
+            if not (isinstance(frequency, torch.Tensor) and frequency.dtype is _F32 and frequency.shape == row and
+                    frequency.get_device() == index and frequency.is_contiguous()):
+                _refuse(frequency, "frequency", _F32, row, index)
+            fp = frequency.data_ptr()
+        if h:
+            hp = history.data_ptr()
+        else:       # (an empty history has no address, and nothing to penalise)
+            lp = pp = rp = ep = fp = None
+    elif not (history_lens is prompt_lens is repetition is presence is frequency is None):
+        raise ValueError("history_lens, prompt_lens and penalties need a history")
     if bias_ids is not None or bias_values is not None:
         if not (isinstance(bias_ids, torch.Tensor) and bias_ids.dtype is _I32 and bias_ids.dim() == 2 and
                 bias_ids.shape[0] == m and bias_ids.get_device() == index and bias_ids.is_contiguous()):
@@ -818,7 +841,7 @@ def adjust_logits(logits, history=None, history_lens=None, prompt_lens=None, rep
                 mask.get_device() == index and mask.is_contiguous()):
             _refuse(mask, "mask", _I32, words, index)
         mp = mask.data_ptr()
-    _call("tl_adjust_logits", index, (logits.data_ptr(), m, v, dt, hp if h else None, h, *each, ip, vp, b, mp,
+    _call("tl_adjust_logits", index, (logits.data_ptr(), m, v, dt, hp, h, lp, pp, rp, ep, fp, ip, vp, b, mp,
                                       out.data_ptr(), od))
     return out
 
