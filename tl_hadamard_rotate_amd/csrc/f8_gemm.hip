@@ -28,8 +28,6 @@
 //    at 1.7 GHz, 72 % of the cycles issuing matrix instructions.
 // Either is cut along K where tiles are few, into parts whose sums a second kernel
 // adds in order.
-#include <cmath>
-
 #include "elem.h"
 #include "f8.h"
 #include "tl_internal.h"
@@ -573,38 +571,44 @@ struct Plan {
 
 constexpr int64_t kMostSums = int64_t(1) << 28;
 
-// The plan with the least estimated time, in us: MODEL
+// The plan with the least estimated time.  What it weighs was measured over 500 x 640
+// to 131072 x 5120 by 17 to 4096 tokens, weights not in the caches, and picks within a
+// few per cent of the best cut of nearly every one: a block of 128 K takes the busiest
+// compute unit `each` us for every workgroup on it, `alone` where it has one; weights
+// and activations arrive at 5.2 bytes per ps, longer by half of what an uneven load
+// leaves idle; operands at 10 from the caches; the second kernel costs 3 us, 0.2 a
+// part, and its sums, written and read, 5 bytes per ps.  (17408 x 5120 by 64 tokens
+// takes 30 us in tiles of 64 tokens, 36 in tiles of 32, 112 with a ring of chunks a
+// wave; by 512 66 us in tiles of 256 x 256, 87 in tiles of 128 x 128.)
 Plan make_plan(int64_t m, int64_t n, int64_t k, bool wide) {
     static const double kEach[2][4] = {{0.42, 0.50, 0.65, 1.6}, {0.50, 0.65, 1.0, 2.9}};
     static const double kAlone[2][4] = {{0.60, 0.68, 1.0, 1.6}, {0.65, 0.85, 1.4, 2.9}};
     const int64_t cus = cu_count(), groups = k / 128;
     Plan best = {};
     double least = 0;
-    for (const int it : {1, 2, 4, 8}) {
-        const bool big = it == 8;
+    for (int i = 0; i < 4; ++i) {
         Plan p;
-        p.it = it;
-        p.tiles_m = (m + 32 * it - 1) / (32 * it);
-        p.tiles_n = big ? (n + kRows - 1) / kRows : (n + kMidRows - 1) / kMidRows;
+        p.it = 1 << i;
+        if (i > 0 && 16 * p.it >= m) break;      // (half the tokens or more of every tile absent)
+        const bool big = p.it == 8;
+        const int64_t rows = big ? kRows : kMidRows;
+        p.tiles_m = (m + 32 * p.it - 1) / (32 * p.it);
+        p.tiles_n = (n + rows - 1) / rows;
         p.tiles = p.tiles_m * p.tiles_n;
-        if (it > 1 && 16 * it >= m) break;      // (half the tokens or more of every tile absent)
-        const int i = it == 1 ? 0 : it == 2 ? 1 : it == 4 ? 2 : 3, rows = big ? kRows : kMidRows;
+        const double bytes = double(n + m) * k / 5.2e6, caches = double(p.tiles) * (rows + 32 * p.it) * k / 10e6;
         for (p.splits = 1; p.splits <= 16 && p.splits <= groups; ++p.splits) {
             // the large kernel cuts only the tiles of the last, partial round
             p.whole = p.splits == 1 ? p.tiles : big ? p.tiles / cus * cus : 0;
-            if (p.sums() > kMostSums) break;
-            const double whole = double(p.splits > 1 ? p.whole : p.tiles), cut = double(p.tiles * p.splits) - whole * p.splits;
-            const double part = std::ceil(double(groups) / p.splits);
-            const double each = kEach[wide][i], alone = kAlone[wide][i];
-            const double in_whole = std::ceil(whole / cus), in_cut = p.splits > 1 ? std::ceil(cut / cus) : 0.0;
-            // blocks of the busiest compute unit, one workgroup after the other or side by side
-            double us = in_whole + in_cut == 1 ? (in_whole * groups + in_cut * part) * alone
-                                               : (in_whole * groups + in_cut * part) * each;
-            // operands from memory, and to the compute units from the caches
-            const double mean = (whole * groups + (p.splits > 1 ? cut * part : 0.0)) / cus;
-            const double uneven = 0.5 + 0.5 * (in_whole * groups + in_cut * part) / mean;
-            us = std::fmax(us, double(n + m) * k / 5.2e6 * uneven);
-            us = std::fmax(us, double(p.tiles) * (rows + 32 * it) * k / 10e6);
+            const int64_t cut = (p.tiles - p.whole) * p.splits;
+            if (p.splits > 1 && (cut == 0 || cut > 8 * cus || p.sums() > kMostSums)) break;
+            const int64_t part = (groups + p.splits - 1) / p.splits;
+            const int64_t in_whole = (p.whole + cus - 1) / cus, in_cut = (cut + cus - 1) / cus;
+            const double busiest = double(in_whole * groups + in_cut * part);     // blocks of a compute unit
+            const double mean = double(p.whole * groups + cut * part) / cus;
+            double us = busiest * (in_whole + in_cut == 1 ? kAlone : kEach)[wide][i];
+            const double memory = bytes * (0.5 + 0.5 * busiest / mean);
+            us = us > memory ? us : memory;
+            us = us > caches ? us : caches;
             if (p.splits > 1) us += 3.0 + 0.2 * p.splits + 2 * double(p.sums()) / 5e6;
             if (least == 0 || us < least) {
                 least = us;
