@@ -26,7 +26,7 @@ def _dequant(x=B[0], m=4, k=1024, xd=1, codes=B[1], scales=B[2]):
 def test_f8_weight_refusals(call):
     for name in ("x", "codes", "scales"):
         assert call(**{name: NULL}) == 1
-        assert call(**{name: B[7] + 8}) == 4
+    assert call(x=B[7] + 8) == 4 and call(codes=B[7] + 8) == 4
     for k in (0, 64, 192, (1 << 20) + 128, -128):
         assert call(k=k) == 2
     assert call(m=0) == 2 and call(m=(1 << 24) + 1) == 2 and call(m=1 << 24, k=8192) == 2
@@ -45,6 +45,7 @@ def _gemm(codes=B[0], scales=B[1], x=B[2], xs=B[3], m=4, n=64, k=1024, y=B[4], y
 def test_f8_gemm_refusals():
     for name in ("codes", "scales", "x", "xs", "y"):
         assert _gemm(**{name: NULL}) == 1
+    for name in ("codes", "x", "y"):
         assert _gemm(**{name: B[7] + 8}) == 4
     assert _gemm(m=0) == 2 and _gemm(n=0) == 2 and _gemm(k=64) == 2 and _gemm(k=200) == 2
     assert _gemm(m=1 << 24, k=8192) == 2 and _gemm(n=1 << 24, k=8192) == 2 and _gemm(m=1 << 20, n=1 << 20, k=128) == 2
@@ -84,7 +85,8 @@ def _f8(codes=B[0], scales=B[1], ids=B[2], m=4, n=64, k=1024, factor=1.0, out=B[
 def test_rows_refusals(call):
     for name in ("codes", "scales", "ids", "out"):
         assert call(**{name: NULL}) == 1
-        assert call(**{name: B[7] + (2 if name == "ids" else 8)}) == 4
+        if (call, name) != (_f8, "scales"):
+            assert call(**{name: B[7] + (2 if name == "ids" else 8)}) == 4
     assert call(m=0) == 2 and call(n=0) == 2 and call(k=64) == 2 and call(k=192) == 2
     assert call(m=1 << 24, k=8192) == 2 and call(n=1 << 24, k=8192) == 2
     assert call(od=3) == 7 and call(od=5) == 7

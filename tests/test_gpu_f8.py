@@ -267,6 +267,91 @@ def test_workspace_contents_do_not_matter(gpu):
         assert torch.equal(got, call(x, w, torch.float16, gpu, workspace=ws))
 
 
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("m,n,k", [(9, 40, 17408), (40, 150, 7040), (130, 130, 9984), (300, 300, 12800),
+                                   (600, 5200, 7040), (520, 700, 17408)])
+def test_long_sums_of_whole_numbers(gpu, m, n, k, out):
+    """Every place of long rows counts, in whole and in cut tiles: codes of -1, 0 and
+    1, sparse enough that sums stay exact in every type, under scales whose product
+    is 1 and which differ from block to block."""
+    rng = np.random.default_rng(k)
+    xv, wv = rng.integers(-1, 2, (m, k)), rng.integers(-1, 2, (n, k))
+    xv[rng.random((m, k)) < 0.9] = 0
+    e = rng.integers(-20, 21, k // 128)
+    code = np.array([0xB8, 0, 0x38], np.uint8)
+    xs, ws = np.tile((127 + e).astype(np.uint8), (m, 1)), np.tile((127 - e).astype(np.uint8), (n, 1))
+    got = host(call((code[xv + 1], xs), (code[wv + 1], ws), TYPES[out], gpu))
+    want = torch.from_numpy(xv).float() @ torch.from_numpy(wv).float().T        # whole numbers below 2^24
+    assert np.array_equal(got, want.to(TYPES[out]).double().numpy())
+
+
+@pytest.mark.parametrize("m", [1, 16, 40, 100, 300])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_scales_far_from_one(gpu, m, out):
+    """Blocks of 2^-117 times 2^110 and the like: products stay ordinary numbers."""
+    n, k = 140, 1280
+    x, w = make(m, n, k, seed=m, outliers=False)
+    for e in (-108, 117):
+        xs = (x[1].astype(int) + e).clip(10, 245).astype(np.uint8)      # (codes of 2^-9 .. 448: within 2^-126 .. 2^127)
+        ws = (w[1].astype(int) - e).clip(10, 245).astype(np.uint8)
+        check((x[0], xs), (w[0], ws), TYPES[out], gpu)
+
+
+@pytest.mark.parametrize("m", [1, 12, 40, 300])
+def test_rows_cut_out_of_others(gpu, m):
+    """Any run of rows is rows again: scales then start at odd addresses."""
+    n, k = 50, 640
+    x, w = make(m + 3, n + 3, k, seed=m)
+    xc, xs, wc, ws = e4(x[0], gpu), e8(x[1], gpu), e4(w[0], gpu), e8(w[1], gpu)
+    for out in (torch.float32, torch.float16):
+        got = tl.f8_gemm(wc[3:], ws[3:], xc[3:], xs[3:], out_dtype=out)
+        want = tl.f8_gemm(wc[3:].clone(), ws[3:].clone(), xc[3:].clone(), xs[3:].clone(), out_dtype=out)
+        assert torch.equal(got, want)
+    v = tl.f8_dequantize(wc, ws, out_dtype=torch.float32)
+    assert torch.equal(tl.f8_dequantize(wc[3:], ws[3:], out_dtype=torch.float32), v[3:])
+    ids = torch.arange(n, dtype=torch.int32, device=gpu)
+    assert torch.equal(tl.f8_rows(wc[3:], ws[3:], ids, out_dtype=torch.float32), v[3:])
+    c2, s2 = torch.full_like(wc.view(torch.uint8), 9), torch.full_like(ws.view(torch.uint8), 9)
+    tl.f8_quantize(v[3:], c2.view(torch.float8_e4m3fn)[3:], s2.view(torch.float8_e8m0fnu)[3:])
+    c1, s1 = tl.f8_quantize(v)
+    assert bool((c2[:3] == 9).all() and (s2[:3] == 9).all())
+    assert torch.equal(c2[3:], c1.view(torch.uint8)[3:]) and torch.equal(s2[3:], s1.view(torch.uint8)[3:])
+
+
+def test_quantize_past_32_bits(gpu):
+    """The last rows of more than 2^32 values."""
+    m, k = 32800, 131072
+    x = torch.zeros(m, k, dtype=torch.bfloat16, device=gpu)
+    x[m - 2] = 3.0
+    x[m - 1, -1] = -448.0
+    codes, scales = tl.f8_quantize(x)
+    del x
+    assert not codes[:m - 2].view(torch.uint8).any() and not scales[:m - 2].view(torch.uint8).any()
+    back = tl.f8_dequantize(codes, scales)
+    assert bool((back[m - 2] == 3).all()) and float(back[m - 1, -1]) == -448 and not back[m - 1, :-1].any()
+    assert not back[:m - 2].any()
+
+
+@pytest.mark.parametrize("m", [1, 16, 40, 300, 1100])
+def test_weights_past_32_bits(gpu, m):
+    """The last of more than 2^32 weights (and, for 1100 tokens, of as many outputs)."""
+    n, k = (1 << 22) + 37, 1024
+    codes = torch.zeros(n, k, dtype=torch.uint8, device=gpu)
+    scales = torch.full((n, k // 128), 127, dtype=torch.uint8, device=gpu)
+    rows = torch.tensor([0, 5, 1 << 21, n - 300, n - 38, n - 2, n - 1], device=gpu)
+    g = torch.Generator().manual_seed(m)
+    wv, xv = torch.randint(-1, 2, (len(rows), k), generator=g), torch.randint(-1, 2, (m, k), generator=g)
+    code = torch.tensor([0xB8, 0, 0x38], dtype=torch.uint8)
+    codes[rows] = code[wv + 1].to(gpu)
+    xs = torch.full((m, k // 128), 127, dtype=torch.uint8, device=gpu)
+    for out in (torch.float16, torch.float32) if m < 1100 else (torch.float16,):
+        y = tl.f8_gemm(codes.view(torch.float8_e4m3fn), scales.view(torch.float8_e8m0fnu),
+                       code[xv + 1].to(gpu).view(torch.float8_e4m3fn), xs.view(torch.float8_e8m0fnu), out_dtype=out)
+        assert torch.equal(y[:, rows].float().cpu(), xv.float() @ wv.float().T)
+        y[:, rows] = 0
+        assert not y[0].any() and not y[m - 1].any() and not y[m // 2].any()
+
+
 def test_linear_rounds_and_multiplies(gpu):
     g = torch.Generator().manual_seed(5)
     wf, xf = 0.02 * torch.randn(300, 1280, generator=g), torch.randn(9, 1280, generator=g)

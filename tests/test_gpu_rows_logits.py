@@ -197,6 +197,40 @@ def test_many_rows(gpu):
     assert torch.equal(got, torch.zeros_like(x).scatter_(1, ids.long(), 1))
 
 
+def test_as_many_rows_as_may_be(gpu):
+    """A lane or more for each of 2^24 rows, and more lanes than one launch has."""
+    m = 1 << 24
+    x = torch.arange(m, dtype=torch.float32, device=gpu)[:, None]
+    ids = (torch.arange(m, dtype=torch.int32, device=gpu) % 2)[:, None].contiguous()
+    got = tl.adjust_logits(x, bias_ids=ids, bias_values=torch.ones(m, 1, device=gpu))
+    assert torch.equal(got[:, 0], x[:, 0] + (ids[:, 0] == 0))
+
+
+def test_logits_past_32_bits(gpu):
+    m, v = 4100, 1 << 20
+    x = torch.zeros(m, v, dtype=torch.float16, device=gpu)
+    ids = torch.full((m, 2), v - 1, dtype=torch.int32, device=gpu)
+    ids[:, 0] = torch.arange(m, device=gpu)
+    mask = torch.full((m, v // 32), -1, dtype=torch.int32, device=gpu)
+    mask[m - 1, 7] = ~1
+    tl.adjust_logits(x, bias_ids=ids, bias_values=torch.tensor([[1.0, 2.0]], device=gpu).repeat(m, 1), mask=mask, out=x)
+    at = torch.arange(m, device=gpu)
+    assert bool((x[:, v - 1] == 2).all()) and bool((x[at, at] == 1).all()) and float(x[m - 1, 224]) == -float("inf")
+    x[:, v - 1], x[at, at], x[m - 1, 224] = 0, 0, 0
+    assert not any(bool(x[i:i + 512].any()) for i in range(0, m, 512))
+
+
+def test_rows_past_one_launch(gpu):
+    """More lanes of 8 values than a launch has."""
+    m, n, k = 1 << 24, 1000, 1152
+    args, _ = table("f8", n, k, gpu)
+    ids = torch.arange(m, dtype=torch.int32, device=gpu) % (n + 1)
+    got = tl.f8_rows(*args, ids)
+    want = torch.cat([tl.f8_dequantize(*args), torch.zeros(1, k, dtype=torch.float16, device=gpu)])
+    for at in list(range(0, m, m // 7)) + [m - 4096, (1 << 31) // (k // 8) - 2048]:
+        assert torch.equal(got[at:at + 4096], want[ids[at:at + 4096].long()]), at
+
+
 # ------------------------------------------------------------ the run
 
 def run_of_calls(embedding, head, gain, ids, history, mask, bufs=None):

@@ -11,7 +11,7 @@
 // history and biases and marks in LDS what falls into its slice: occurrences after
 // the prompt counted, the prompt's in the top bit; the largest place of a bias that
 // names the token.  Integer additions and maxima, whose order does not show.
-#include <cmath>
+#include <type_traits>
 
 #include "elem.h"
 #include "tl_internal.h"
@@ -29,7 +29,7 @@ struct Args {
     const float* bias_values;
     const uint8_t* mask;
     void* out;
-    int64_t v, h, b;
+    int64_t v, h, b, row0;       // row0: the launch's first row
     uint32_t slices;
 };
 
@@ -116,8 +116,9 @@ template <typename T, typename U, int I, bool WIDE>
 __global__ __launch_bounds__(1024) void adjust_logits_kernel(const Args a) {
     extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
     const uint32_t tid = threadIdx.x, threads = blockDim.x, width = 4 * I * threads;
-    const int64_t row = blockIdx.x / a.slices;
-    const uint32_t first = (blockIdx.x - uint32_t(row) * a.slices) * width;      // token of the slice
+    const uint32_t at_row = blockIdx.x / a.slices;
+    const int64_t row = a.row0 + at_row;
+    const uint32_t first = (blockIdx.x - at_row * a.slices) * width;     // token of the slice
     const uint32_t v = uint32_t(a.v);
     const Elem<T>* in = static_cast<const Elem<T>*>(a.logits) + row * a.v;
     Elem<U>* out = static_cast<Elem<U>*>(a.out) + row * a.v;
@@ -248,13 +249,16 @@ hipError_t launch(Args a, int64_t m, unsigned threads, hipStream_t stream) {
     const auto kernel = adjust_logits_kernel<T, U, I, WIDE>;
     const unsigned width = 4 * I * threads;
     const unsigned lds = Table<WIDE>::kBytes * width * unsigned((a.history ? 1 : 0) + (a.bias_ids ? 1 : 0));
-    if (lds > 64 * 1024) {
-        const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), 160 * 1024);
+    static_assert(Table<WIDE>::kBytes * 4 * I * 1024 * 2 <= 64 * 1024, "LDS");
+    a.slices = unsigned((a.v + width - 1) / width);
+    const int64_t most = (int64_t(1) << 31) / threads / a.slices;   // rows of a launch, whose lanes count in 32 bits
+    for (a.row0 = 0; a.row0 < m; a.row0 += most) {
+        const int64_t left = m - a.row0 < most ? m - a.row0 : most;
+        hipLaunchKernelGGL(kernel, dim3(unsigned(left * a.slices)), dim3(threads), lds, stream, a);
+        const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    a.slices = unsigned((a.v + width - 1) / width);
-    hipLaunchKernelGGL(kernel, dim3(unsigned(m * a.slices)), dim3(threads), lds, stream, a);
-    return hipGetLastError();
+    return hipSuccess;
 }
 
 // 16 bits hold a count below 32768 and a place below 65536.  Every workgroup goes
@@ -288,7 +292,7 @@ hipError_t launch_adjust_logits(const void* logits, int64_t m, int64_t v, int dt
                                 void* out, int out_dtype, hipStream_t stream) {
     // (a history of no tokens, or biases of none, are as good as absent)
     const Args a = {logits, h ? history : nullptr, history_lens, prompt_lens, repetition, presence, frequency,
-                    b ? bias_ids : nullptr, bias_values, reinterpret_cast<const uint8_t*>(mask), out, v, h, b, 0};
+                    b ? bias_ids : nullptr, bias_values, reinterpret_cast<const uint8_t*>(mask), out, v, h, b, 0, 0};
     return dtype == TL_F32   ? launch_out<F32>(a, m, out_dtype, stream)
            : dtype == TL_F16 ? launch_out<F16>(a, m, out_dtype, stream)
                              : launch_out<BF16>(a, m, out_dtype, stream);

@@ -63,15 +63,20 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(const uint8_t* __restric
 template <typename W>
 hipError_t rows(const uint8_t* codes, const void* scales, const int32_t* ids, int64_t m, int64_t n, int64_t k,
                 float factor, void* out, int out_dtype, hipStream_t stream) {
+    const auto kernel = out_dtype == TL_F32   ? rows_kernel<W, F32>
+                        : out_dtype == TL_F16 ? rows_kernel<W, F16>
+                                              : rows_kernel<W, BF16>;
     const uint32_t eights = uint32_t(k / 8);
-    const dim3 grid(unsigned((m * eights + kThreads - 1) / kThreads)), block(kThreads);
-    if (out_dtype == TL_F32)
-        hipLaunchKernelGGL((rows_kernel<W, F32>), grid, block, 0, stream, codes, scales, ids, m, n, eights, factor, out);
-    else if (out_dtype == TL_F16)
-        hipLaunchKernelGGL((rows_kernel<W, F16>), grid, block, 0, stream, codes, scales, ids, m, n, eights, factor, out);
-    else
-        hipLaunchKernelGGL((rows_kernel<W, BF16>), grid, block, 0, stream, codes, scales, ids, m, n, eights, factor, out);
-    return hipGetLastError();
+    const int64_t most = (int64_t(1) << 31) / eights;       // rows of a launch, whose lanes count in 32 bits
+    for (int64_t at = 0; at < m; at += most) {
+        const int64_t left = m - at < most ? m - at : most;
+        hipLaunchKernelGGL(kernel, dim3(unsigned((left * eights + kThreads - 1) / kThreads)), dim3(kThreads), 0, stream,
+                           codes, scales, ids + at, left, n, eights, factor,
+                           static_cast<uint8_t*>(out) + at * k * (out_dtype == TL_F32 ? 4 : 2));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace

@@ -103,7 +103,7 @@ tl_status check_rows(const void* codes, int64_t code_bytes, const void* scales, 
                      const int32_t* ids, int64_t m, int64_t k, float factor, const void* out, int32_t out_dtype) {
     if (!real_dtype(out_dtype)) return TL_ERR_DTYPE;
     if (!std::isfinite(factor)) return TL_ERR_VALUE;
-    if (!aligned16(codes) || !aligned16(scales) || !aligned4(ids) || !aligned16(out)) return TL_ERR_ALIGN;
+    if (!aligned16(codes) || !aligned4(ids) || !aligned16(out)) return TL_ERR_ALIGN;
     const int64_t ob = m * k * dtype_bytes(out_dtype);
     if (overlap(out, ob, codes, code_bytes) || overlap(out, ob, scales, scale_bytes) || overlap(out, ob, ids, m * 4))
         return TL_ERR_ALIAS;
@@ -466,7 +466,7 @@ tl_status tl_f8_quantize(const void* x, int64_t M, int64_t K, int32_t x_dtype, u
     if (!x || !codes || !scales) return TL_ERR_NULL;
     if (!q4_shape_ok(M, K)) return TL_ERR_SHAPE;
     if (!real_dtype(x_dtype)) return TL_ERR_DTYPE;
-    if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return TL_ERR_ALIGN;
+    if (!aligned16(x) || !aligned16(codes)) return TL_ERR_ALIGN;
     const int64_t xb = M * K * dtype_bytes(x_dtype), cb = M * K, sb = M * (K / TL_GROUP);
     if (overlap(codes, cb, x, xb) || overlap(scales, sb, x, xb) || overlap(codes, cb, scales, sb))
         return TL_ERR_ALIAS;
@@ -478,7 +478,7 @@ tl_status tl_f8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t 
     if (!codes || !scales || !out) return TL_ERR_NULL;
     if (!q4_shape_ok(M, K)) return TL_ERR_SHAPE;
     if (!real_dtype(out_dtype)) return TL_ERR_DTYPE;
-    if (!aligned16(codes) || !aligned16(scales) || !aligned16(out)) return TL_ERR_ALIGN;
+    if (!aligned16(codes) || !aligned16(out)) return TL_ERR_ALIGN;
     const int64_t ob = M * K * dtype_bytes(out_dtype);
     if (overlap(out, ob, codes, M * K) || overlap(out, ob, scales, M * (K / TL_GROUP))) return TL_ERR_ALIAS;
     return launched(tl::launch_f8_dequantize(codes, scales, M, K, out, out_dtype, stream));
@@ -494,8 +494,7 @@ tl_status tl_f8_gemm(const uint8_t* codes, const uint8_t* scales, const uint8_t*
     if (!codes || !scales || !x || !x_scales || !y) return TL_ERR_NULL;
     if (!q4_product_shape_ok(M, N, K)) return TL_ERR_SHAPE;
     if (!real_dtype(y_dtype)) return TL_ERR_DTYPE;
-    if (!aligned16(codes) || !aligned16(scales) || !aligned16(x) || !aligned16(x_scales) || !aligned16(y))
-        return TL_ERR_ALIGN;
+    if (!aligned16(codes) || !aligned16(x) || !aligned16(y)) return TL_ERR_ALIGN;
     const int64_t cb = N * K, sb = N * (K / TL_GROUP), xb = M * K, xsb = M * (K / TL_GROUP);
     const int64_t yb = M * N * dtype_bytes(y_dtype);
     if (overlap(y, yb, codes, cb) || overlap(y, yb, scales, sb) || overlap(y, yb, x, xb) ||
@@ -514,6 +513,7 @@ tl_status tl_q4_rows(const uint8_t* packed, const uint16_t* scales, int32_t grou
     if (!packed || !scales || !ids || !out) return TL_ERR_NULL;
     if (!q4_shape_ok(N, K) || !q4_shape_ok(M, K)) return TL_ERR_SHAPE;
     if (!q4_group_ok(group)) return TL_ERR_FORMAT;
+    if (!aligned16(scales)) return TL_ERR_ALIGN;
     const tl_status st = check_rows(packed, N * (K / 2), scales, N * (K / group) * 2, ids, M, K, factor, out, out_dtype);
     if (st != TL_OK) return st;
     return launched(tl::launch_q4_rows(packed, scales, group, ids, M, N, K, factor, out, out_dtype, stream));
