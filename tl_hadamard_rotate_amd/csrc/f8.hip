@@ -32,49 +32,40 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t a) {
     return a;
 }
 
-// One lane per 8 values, a block being a row of 16 lanes; U such pieces of a lane are
-// loaded before the first is rounded
-template <typename T, int U>
+// One lane per 8 values, a block being a row of 16 lanes
+template <typename T>
 __global__ __launch_bounds__(kThreads) void f8_quantize_kernel(const void* __restrict__ x, int64_t items,
-                                                               u32x2* __restrict__ codes,
+                                                               uint2* __restrict__ codes,
                                                                uint8_t* __restrict__ scales) {
     // items is a multiple of 16 (K % 128 == 0): a block's lanes leave together
-    const int64_t stride = int64_t(gridDim.x) * (kThreads * U);
-    for (int64_t base = int64_t(blockIdx.x) * (kThreads * U) + threadIdx.x; base < items; base += stride) {
-        float values[U][8];
+    const int64_t stride = int64_t(gridDim.x) * kThreads;
+    for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < items; i += stride) {
+        float v[8];
+        load8<T>(x, 8 * i, v);
+        uint32_t a = 0, top = 0;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (base + u * kThreads < items) load8<T>(x, 8 * (base + u * kThreads), values[u]);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t i = base + u * kThreads;
-            if (i >= items) return;
-            const float(&v)[8] = values[u];
-            uint32_t a = 0, top = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t b = abs_bits(v[j]);
-                top = max(top, b);
-                a = max(a, b < kInf ? b : 0u);
-            }
-            a = row16_max(a);
-            const uint32_t s = scale_of(a);
-            const float inv = __builtin_bit_cast(float, (254u - s) << 23);   // s <= 247
-            uint32_t c[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h] * inv, v[4 * h + 1] * inv, 0, false);
-                w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h + 2] * inv, v[4 * h + 3] * inv, w, true);
-                c[h] = uint32_t(w);
-            }
-            if (top >= kInf) {      // e4m3 has no infinity: both become its NaN
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (abs_bits(v[j]) >= kInf) c[j >> 2] = (c[j >> 2] & ~(0xFFu << (8 * (j & 3)))) | 0x7Fu << (8 * (j & 3));
-            }
-            put<false>(codes + i, u32x2{c[0], c[1]});
-            if ((i & 15) == 0) scales[i >> 4] = uint8_t(s);
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t b = abs_bits(v[j]);
+            top = max(top, b);
+            a = max(a, b < kInf ? b : 0u);
         }
+        a = row16_max(a);
+        const uint32_t s = scale_of(a);
+        const float inv = __builtin_bit_cast(float, (254u - s) << 23);   // s <= 247
+        uint32_t c[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h] * inv, v[4 * h + 1] * inv, 0, false);
+            w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h + 2] * inv, v[4 * h + 3] * inv, w, true);
+            c[h] = uint32_t(w);
+        }
+        if (top >= kInf) {      // e4m3 has no infinity: both become its NaN
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (abs_bits(v[j]) >= kInf) c[j >> 2] = (c[j >> 2] & ~(0xFFu << (8 * (j & 3)))) | 0x7Fu << (8 * (j & 3));
+        }
+        codes[i] = uint2{c[0], c[1]};
+        if ((i & 15) == 0) scales[i >> 4] = uint8_t(s);
     }
 }
 
@@ -95,25 +86,16 @@ unsigned grid_for(int64_t items) {
     return unsigned(g < (1 << 20) ? g : (1 << 20));
 }
 
-template <int U>
-void quantize(const void* x, int64_t items, int x_dtype, u32x2* codes, uint8_t* scales, hipStream_t stream) {
-    const auto kernel = x_dtype == TL_F32   ? f8_quantize_kernel<F32, U>
-                        : x_dtype == TL_F16 ? f8_quantize_kernel<F16, U>
-                                            : f8_quantize_kernel<BF16, U>;
-    hipLaunchKernelGGL(kernel, dim3(grid_for((items + U - 1) / U)), dim3(kThreads), 0, stream, x, items, codes, scales);
-}
-
 }  // namespace
 
-// Two pieces a lane where there are many: us in a graph with one and two, 5120 x 17408
-// bfloat16 48.0 and 45.9, 17408 x 5120 float32 76.8 and 75.5, 1024 x 5120 binary16 4.9
-// and 4.7, 64 x 5120 bfloat16 3.1 and 3.3 (four: 49.1, 78.3, 5.4, 4.0).
 hipError_t launch_f8_quantize(const void* x, int64_t m, int64_t k, int x_dtype, uint8_t* codes, uint8_t* scales,
                               hipStream_t stream) {
     const int64_t items = m * k / 8;
-    u32x2* c = reinterpret_cast<u32x2*>(codes);
-    if (items >= 1 << 18) quantize<2>(x, items, x_dtype, c, scales, stream);
-    else quantize<1>(x, items, x_dtype, c, scales, stream);
+    uint2* c = reinterpret_cast<uint2*>(codes);
+    const dim3 grid(grid_for(items)), block(kThreads);
+    if (x_dtype == TL_F32) hipLaunchKernelGGL(f8_quantize_kernel<F32>, grid, block, 0, stream, x, items, c, scales);
+    else if (x_dtype == TL_F16) hipLaunchKernelGGL(f8_quantize_kernel<F16>, grid, block, 0, stream, x, items, c, scales);
+    else hipLaunchKernelGGL(f8_quantize_kernel<BF16>, grid, block, 0, stream, x, items, c, scales);
     return hipGetLastError();
 }
 

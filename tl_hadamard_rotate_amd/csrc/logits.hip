@@ -112,17 +112,6 @@ struct Table {
     }
 };
 
-// 4 elements past the caches' replacement order: nothing here reads them again, and
-// stores that are kept take longer (64 x 131072 to float32 17.4 us against 15.2)
-template <typename U>
-__device__ __forceinline__ void put4(Elem<U>* p, const Raw<U>& r) {
-    typedef uint32_t vec __attribute__((ext_vector_type(U::kBytes), aligned(U::kBytes)));
-    vec v;
-#pragma unroll
-    for (int j = 0; j < U::kBytes; ++j) v[j] = r.w[j];
-    __builtin_nontemporal_store(v, reinterpret_cast<vec*>(p));
-}
-
 template <typename T, typename U, int I, bool WIDE>
 __global__ __launch_bounds__(1024) void adjust_logits_kernel(const Args a) {
     extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
@@ -244,7 +233,7 @@ __global__ __launch_bounds__(1024) void adjust_logits_kernel(const Args a) {
         Raw<U> res;
         pack<U>(x, res);
         if (at + 4 <= v) {
-            put4<U>(out + at, res);
+            __builtin_memcpy(out + at, &res, sizeof(res));
         } else {
             Elem<U> e[4];
             __builtin_memcpy(e, &res, sizeof(res));
@@ -276,10 +265,9 @@ hipError_t launch(Args a, int64_t m, unsigned threads, hipStream_t stream) {
 // through the whole history, so slices are long (16384 tokens) where that leaves two
 // workgroups a compute unit, short where there are few rows and little history.  us in
 // a graph, slices of 2048, 8192, 16384, 32768 tokens: 64 rows of 131072 bfloat16 to
-// float32 logits, 8192 ids, 300 biases 21.7 17.0 14.8 15.9; 16 rows of float32, 4096
-// ids 7.3 6.6 8.3 12.2; one row, 2048 ids, 16 biases 4.6 5.4 7.2 10.7.  The first moves
-// 52 MB, 8.8 us without history and biases: its workgroups all run at once, and their
-// stores begin when the ids are done.
+// float32 logits, 8192 ids, 300 biases 22.7 18.3 16.8 17.9; one row of float32, 2048
+// ids, 16 biases 4.6 5.3 7.2 10.7.  The first moves 52 MB: the reads overlap the ids
+// of the history, the stores (33 MB, 6 us) begin when those are done.
 template <typename T, typename U>
 hipError_t launch_sized(const Args& a, int64_t m, hipStream_t stream) {
     const int64_t cus = cu_count(), slots = m * ((a.v + 8191) / 8192);
