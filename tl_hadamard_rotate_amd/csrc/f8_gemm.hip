@@ -24,7 +24,7 @@
 //  - some tokens: 128 weight rows by 32, 64 or 128 tokens, 4 waves, two workgroups on
 //    a compute unit.  Bound by the weights' bytes.
 //  - many: 256 by 256, 8 waves, one workgroup.  Bound by the matrix cores' power: with
-//    zeros for data 8192 x 8192 x 8192 takes 284 us at 2.4 GHz, with random data 405 us
+//    zeros for data 8192 x 8192 x 8192 takes 295 us at 2.4 GHz, with random data 405 us
 //    at 1.7 GHz, 72 % of the cycles issuing matrix instructions.
 // Either is cut along K where tiles are few, into parts whose sums a second kernel
 // adds in order.
@@ -523,8 +523,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     // through LDS, 128 tokens by 64 weight rows a wave, so that a store writes whole cache
     // lines: piece e of 8 weight rows of a token in place e ^ (token / 2) % 8.  Straight
     // from the registers, 32 bytes of a token a store, 4096 x 17408 x 5120 takes 328 us
-    // instead of 309; lines that are whole are stored past the caches' replacement order
-    // (304; rows of 32003 are slower that way, 144 against 138 for 1000 tokens).
+    // instead of 309.  (Stores past the caches' replacement order: the same time here,
+    // and 1 to 3 us more for what reads y next.)
     asm volatile("s_barrier" ::: "memory");
     const auto place = [&](int token, int e) { return uint32_t(token) * 128u + 16u * uint32_t(e ^ ((token >> 1) & 7)); };
     const uint32_t mine = lds + 16384u * uint32_t(wave);
@@ -541,7 +541,6 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
                 *reinterpret_cast<lds_u32x4*>(mine + place(32 * j + c, 4 * i + g + q)) = u32x4{s0[0], s1[0], s0[1], s1[1]};
             }
     const int64_t n = n0 + wn + 8 * (l & 7);
-    const bool whole_lines = a.n % 64 == 0;
 #pragma unroll
     for (int z = 0; z < 16; ++z) {
         const int r = 8 * z + (l >> 3);
@@ -550,8 +549,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
         if (token >= a.m) continue;
         uint16_t* y = static_cast<uint16_t*>(a.y) + token * a.n + n;
         if (n + 8 <= a.n) {
-            if (whole_lines) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(y));
-            else __builtin_memcpy(y, &v, 16);
+            __builtin_memcpy(y, &v, 16);
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)

@@ -267,7 +267,9 @@ hipError_t launch(Args a, int64_t m, unsigned threads, hipStream_t stream) {
 // a graph, slices of 2048, 8192, 16384, 32768 tokens: 64 rows of 131072 bfloat16 to
 // float32 logits, 8192 ids, 300 biases 22.7 18.3 16.8 17.9; one row of float32, 2048
 // ids, 16 biases 4.6 5.3 7.2 10.7.  The first moves 52 MB: the reads overlap the ids
-// of the history, the stores (33 MB, 6 us) begin when those are done.
+// of the history, the stores (33 MB, 6 us) begin when those are done.  (Stores past the
+// caches' replacement order: 14.8, but a maximum over each row behind it takes 12 us
+// longer then.)
 template <typename T, typename U>
 hipError_t launch_sized(const Args& a, int64_t m, hipStream_t stream) {
     const int64_t cus = cu_count(), slots = m * ((a.v + 8191) / 8192);
