@@ -469,9 +469,9 @@ TL_API int64_t tl_f8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * entry do not matter, and calls that may run at the same time need separate
  * ones.  codes, x, y and workspace 16-byte aligned; y and workspace overlap
  * nothing else.
- *   TL_F32, and every type up to 16 tokens: products are exact, their sums fp32.
- * Other types, more tokens: the 8-bit matrix instructions, which align the
- * products of 8 neighbouring k to the largest of them, keep 14 bits below its
+ *   TL_F32, every type up to 16 tokens, and the smallest products: products are
+ * exact, their sums fp32.  Otherwise: the 8-bit matrix instructions, which align
+ * the products of 8 neighbouring k to the largest of them, keep 14 bits below its
  * leading one, and add the eights in fp32 (relative to sqrt(sum x^2 w^2), some
  * 1e-5, well below the output's own rounding unless a sum nearly cancels).
  *   code * scale must lie between 2^-126 and 2^127 (below, bits are lost; above,

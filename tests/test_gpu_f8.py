@@ -166,7 +166,8 @@ def test_few_tokens(gpu, m, n, k, out):
 @pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("m,n,k", [(65, 17, 128), (66, 300, 256), (128, 128, 384), (129, 257, 640), (200, 1, 896),
                                    (255, 511, 1152), (256, 256, 512), (257, 259, 2176), (300, 1030, 1280),
-                                   (513, 70, 5120)])
+                                   (513, 70, 5120), (20, 4200, 640), (33, 9000, 384), (64, 5003, 1152),
+                                   (100, 2100, 896), (128, 4100, 256), (200, 1500, 5248), (40, 40, 5376)])
 def test_many_tokens(gpu, m, n, k, out):
     x, w = make(m, n, k, seed=m + n + k, spread=4)
     check(x, w, TYPES[out], gpu)
@@ -178,18 +179,18 @@ def test_long_rows(gpu, m, n, k):
     check(x, w, torch.float32, gpu)
 
 
+@pytest.mark.parametrize("n,k", [(270, 1408), (4130, 1408), (270, 5248)])
 @pytest.mark.parametrize("m", [1, 20, 64, 100, 300])
-def test_codes_count_and_none_is_missed(gpu, m):
+def test_codes_count_and_none_is_missed(gpu, m, n, k):
     """Small whole numbers: every sum is exact, so one product lost, counted
     twice or taken from another place shows."""
     rng = np.random.default_rng(m)
-    n, k = 270, 1408
     values = np.array([-2, -1, 0, 1, 2])
     xc, wc = rng.integers(0, 5, (m, k)), rng.integers(0, 5, (n, k))
     code = oracle.e4m3_codes(values.astype(float))
     s = np.full((max(m, n), k // 128), 127, np.uint8)
     got = host(call((code[xc], s[:m]), (code[wc], s[:n]), torch.float32, gpu))
-    want = values[xc] @ values[wc].T
+    want = (torch.from_numpy(values[xc]).double() @ torch.from_numpy(values[wc]).double().T).numpy()
     assert np.array_equal(got, want)
     got = host(call((code[xc], s[:m]), (code[wc], s[:n]), torch.float16, gpu))
     assert np.array_equal(got, want)            # |sums| stay below 2048
@@ -197,9 +198,10 @@ def test_codes_count_and_none_is_missed(gpu, m):
 
 @pytest.mark.parametrize("m", [1, 20, 100, 300])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
-def test_every_scale_reaches_its_block(gpu, m, out):
+@pytest.mark.parametrize("k", [1152, 5376])
+def test_every_scale_reaches_its_block(gpu, m, out, k):
     """One block of each row counts, under a scale of its own."""
-    n, k = 130, 1152
+    n = 130
     rng = np.random.default_rng(m)
     xv, wv = np.zeros((m, k)), np.zeros((n, k))
     xs, ws = rng.integers(110, 140, (m, k // 128)).astype(np.uint8), rng.integers(110, 140, (n, k // 128)).astype(np.uint8)
@@ -214,8 +216,9 @@ def test_every_scale_reaches_its_block(gpu, m, out):
 
 @pytest.mark.parametrize("m", [1, 30, 100, 300])
 @pytest.mark.parametrize("out", ["f32", "f16"])
-def test_nan_and_zero_stay_in_their_rows(gpu, m, out):
-    n, k = 150, 512
+@pytest.mark.parametrize("k", [512, 5248])
+def test_nan_and_zero_stay_in_their_rows(gpu, m, out, k):
+    n = 150
     x, w = make(m, n, k, seed=m)
     x, w = (x[0].copy(), x[1].copy()), (w[0].copy(), w[1].copy())
     w[0][3, 300] = 0x7F
@@ -237,7 +240,8 @@ def test_nan_and_zero_stay_in_their_rows(gpu, m, out):
         assert np.all(np.abs(got[np.ix_(check_rows, cols)] - want) <= tol)
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 1000, 5120), (12, 500, 17408), (40, 96, 2048), (100, 300, 1280), (300, 520, 2048)])
+@pytest.mark.parametrize("m,n,k", [(1, 1000, 5120), (12, 500, 17408), (40, 96, 2048), (100, 300, 1280), (300, 520, 2048),
+                                   (40, 96, 6016), (100, 4100, 1280), (300, 520, 6016)])
 def test_same_bits_again_and_alone(gpu, m, n, k):
     """From call to call, and whatever the other tokens hold."""
     x, w = make(m, n, k, seed=m)
@@ -249,9 +253,10 @@ def test_same_bits_again_and_alone(gpu, m, n, k):
         assert torch.equal(got[m - 1], call(other, w, out, gpu)[m - 1])
 
 
+@pytest.mark.parametrize("k", [640, 5248])
 @pytest.mark.parametrize("m", [1, 33, 90, 260])
-def test_nothing_behind_the_rows_is_written(gpu, m):
-    x, w = make(m, 33, 640, seed=m)
+def test_nothing_behind_the_rows_is_written(gpu, m, k):
+    x, w = make(m, 33, k, seed=m)
     for out in (torch.float32, torch.float16):
         big = torch.full((m + 3, 33), 7.0, dtype=out, device=gpu)
         call(x, w, out, gpu, out=big[:m])
@@ -287,9 +292,10 @@ def test_long_sums_of_whole_numbers(gpu, m, n, k, out):
 
 @pytest.mark.parametrize("m", [1, 16, 40, 100, 300])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
-def test_scales_far_from_one(gpu, m, out):
+@pytest.mark.parametrize("k", [1280, 5504])
+def test_scales_far_from_one(gpu, m, out, k):
     """Blocks of 2^-117 times 2^110 and the like: products stay ordinary numbers."""
-    n, k = 140, 1280
+    n = 140
     x, w = make(m, n, k, seed=m, outliers=False)
     for e in (-108, 117):
         xs = (x[1].astype(int) + e).clip(10, 245).astype(np.uint8)      # (codes of 2^-9 .. 448: within 2^-126 .. 2^127)
@@ -297,10 +303,11 @@ def test_scales_far_from_one(gpu, m, out):
         check((x[0], xs), (w[0], ws), TYPES[out], gpu)
 
 
+@pytest.mark.parametrize("k", [640, 5248])
 @pytest.mark.parametrize("m", [1, 12, 40, 300])
-def test_rows_cut_out_of_others(gpu, m):
+def test_rows_cut_out_of_others(gpu, m, k):
     """Any run of rows is rows again: scales then start at odd addresses."""
-    n, k = 50, 640
+    n = 50
     x, w = make(m + 3, n + 3, k, seed=m)
     xc, xs, wc, ws = e4(x[0], gpu), e8(x[1], gpu), e4(w[0], gpu), e8(w[1], gpu)
     for out in (torch.float32, torch.float16):

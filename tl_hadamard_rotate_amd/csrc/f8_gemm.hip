@@ -650,14 +650,14 @@ hipError_t run(const Args& a, const Plan& p, hipStream_t stream) {
 }  // namespace
 
 int64_t f8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-    if (f8_gemv_fits(m)) return 0;
+    if (f8_gemv_fits(m, n, k)) return 0;
     const int64_t a = make_plan(m, n, k, false).sums(), b = make_plan(m, n, k, true).sums();
     return a > b ? a : b;
 }
 
 hipError_t launch_f8_gemm(const uint8_t* codes, const uint8_t* scales, const uint8_t* x, const uint8_t* x_scales,
                           int64_t m, int64_t n, int64_t k, void* y, int y_dtype, void* ws, hipStream_t stream) {
-    if (f8_gemv_fits(m)) return launch_f8_gemv(codes, scales, x, x_scales, m, n, k, y, y_dtype, stream);
+    if (f8_gemv_fits(m, n, k)) return launch_f8_gemv(codes, scales, x, x_scales, m, n, k, y, y_dtype, stream);
     const bool wide = y_dtype == TL_F32;
     const Plan p = make_plan(m, n, k, wide);
     const Args a = {codes, scales, x, x_scales, y, static_cast<float*>(ws), m, n, k, y_dtype, int(k / 128),

@@ -1,4 +1,4 @@
-// Product of few tokens with weights in 8-bit floating point, exact products:
+// Product of few tokens (or few weights) in 8-bit floating point, exact products:
 //
 //   y[m, n] = sum_k X[m, k] * W[n, k],   X, W = e4m3 code * 2^(scale of its 128)
 //
@@ -7,10 +7,10 @@
 // matrix instructions sum 8 products at a time with 14 bits below the largest of
 // them; few tokens are bound by the weights' bytes, so they gain nothing here.)
 //
-// 16 weight rows are the A rows, 16 tokens the B columns (absent tokens repeat the
-// last).  Lane (q, c) = (lane / 16, lane % 16) takes 32 bytes of row c of a chunk
-// of 128, at 32 q: which of the chunk's places a matrix instruction sums is free as
-// long as both operands agree.
+// 16 weight rows are the A rows, 16 tokens (or twice 16) the B columns; absent tokens
+// repeat the last.  Lane (q, c) = (lane / 16, lane % 16) takes 32 bytes of row c of a
+// chunk of 128, at 32 q: which of the chunk's places a matrix instruction sums is free
+// as long as both operands agree.
 //
 // Every wave works on its own: R tiles of 16 weight rows, a run of K's chunks, and
 // a ring of D of them in its own LDS, filled by loads that write LDS directly and
@@ -43,13 +43,13 @@ typedef __attribute__((address_space(3))) float4v lds_float4;
 
 constexpr int kDepth = 3;        // chunks of the ring
 constexpr int kSegment = 32;     // chunks whose scales a wave holds at a time
-constexpr int kScaleRow = 48;    // LDS bytes of a row of them: 8-byte aligned, 16 rows on different banks
+constexpr int kScaleRow = 40;    // LDS bytes of a row of them: 8-byte aligned, 16 rows on different banks
 
 struct Args {
     const uint8_t *codes, *scales, *x, *xs;
     void* y;
-    int64_t n, k;
-    int m, y_dtype, chunks, ks;
+    int64_t m, n, k;
+    int y_dtype, chunks, ks;
 };
 
 // 16 bytes a lane from its address to LDS, lane i at `to` + 16 i.  Written out: the
@@ -81,19 +81,20 @@ __device__ __forceinline__ void stage_scales(const uint8_t* from, int s0, int ch
 }
 
 template <int R, int XI>
-constexpr int wave_bytes() { return kDepth * (2 * R + XI) * 1024 + 16 * kScaleRow * (R + 1); }
+constexpr int wave_bytes() { return kDepth * (2 * R + XI) * 1024 + 16 * kScaleRow * (R + (XI + 1) / 2); }
 
-// R tiles of 16 weight rows a wave, XI loads of 8 tokens
+// R tiles of 16 weight rows a wave, XI loads of 8 tokens, T tiles of 16 of them
 template <int R, int XI>
 __global__ __launch_bounds__(512) void f8_gemv_kernel(const Args a) {
-    constexpr int kLoads = 2 * R + XI, kSlot = kLoads * 1024, kWave = wave_bytes<R, XI>();
+    constexpr int T = (XI + 1) / 2, kLoads = 2 * R + XI, kSlot = kLoads * 1024, kWave = wave_bytes<R, XI>();
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const int l = threadIdx.x & 63, q = l >> 4, c = l & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t ring = lds_address(smem) + uint32_t(wave) * kWave, scales = ring + kDepth * kSlot;
     const int64_t n0 = 16 * R * int64_t(blockIdx.x);
     const auto row = [&](int i) { return n0 + i < a.n ? n0 + i : a.n - 1; };
-    const auto token = [&](int i) { return int64_t(i < a.m ? i : a.m - 1); };
+    const int64_t m0 = 16 * T * int64_t(blockIdx.y);
+    const auto token = [&](int i) { return m0 + i < a.m ? m0 + i : a.m - 1; };
 
     // lane i of a load brings the piece of row i / 8 that belongs in place i % 8, piece
     // (i % 8) ^ (row / 2) % 8: 16 rows read at one piece meet all banks
@@ -118,7 +119,7 @@ __global__ __launch_bounds__(512) void f8_gemv_kernel(const Args a) {
     const uint32_t fw = uint32_t(c) * 128u + 16u * uint32_t((2 * q) ^ ((c >> 1) & 7));
     const uint32_t fx = uint32_t(ct) * 128u + 16u * uint32_t((2 * q) ^ ((ct >> 1) & 7)) + 2048u * R;
 
-    float4v acc[R] = {};
+    float4v acc[R][T] = {};
 #pragma unroll
     for (int i = 0; i < kDepth; ++i) load(i, ring + uint32_t(i) * kSlot);
     uint32_t slot = ring;
@@ -127,22 +128,26 @@ __global__ __launch_bounds__(512) void f8_gemv_kernel(const Args a) {
 #pragma unroll
         for (int r = 0; r < R; ++r)
             stage_scales(a.scales + row(16 * r + (l >> 2)) * a.chunks, s0, a.chunks, scales + 16 * kScaleRow * r, l);
-        stage_scales(a.xs + token(l >> 2) * a.chunks, s0, a.chunks, scales + 16 * kScaleRow * R, l);
+#pragma unroll
+        for (int j = 0; j < T; ++j)
+            stage_scales(a.xs + token(16 * j + (l >> 2)) * a.chunks, s0, a.chunks, scales + 16 * kScaleRow * (R + j), l);
         uint32_t sw_at = scales + kScaleRow * uint32_t(c), sx_at = scales + kScaleRow * uint32_t(16 * R + ct);
 #pragma unroll 1
         for (int t = s0; t < s1; ++t, ++sw_at, ++sx_at) {
             asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads * (kDepth - 1)) : "memory");
-            u32x4 w[R][2], x[2];
-            uint32_t sw[R];
+            u32x4 w[R][2], x[T][2];
+            uint32_t sw[R], sx[T];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
                 for (int r = 0; r < R; ++r) w[r][e] = *reinterpret_cast<lds_u32x4*>(slot + (fw ^ (16u * e)) + 2048u * r);
-                x[e] = *reinterpret_cast<lds_u32x4*>(slot + (fx ^ (16u * e)));
+#pragma unroll
+                for (int j = 0; j < T; ++j) x[j][e] = *reinterpret_cast<lds_u32x4*>(slot + (fx ^ (16u * e)) + 2048u * j);
             }
 #pragma unroll
             for (int r = 0; r < R; ++r) sw[r] = *reinterpret_cast<lds_u8*>(sw_at + 16 * kScaleRow * r);
-            const uint32_t sx = *reinterpret_cast<lds_u8*>(sx_at);
+#pragma unroll
+            for (int j = 0; j < T; ++j) sx[j] = *reinterpret_cast<lds_u8*>(sx_at + 16 * kScaleRow * j);
             // what the slot held is in registers before the ring's next chunk takes its place
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
@@ -150,11 +155,15 @@ __global__ __launch_bounds__(512) void f8_gemv_kernel(const Args a) {
             slot = slot == ring + (kDepth - 1) * kSlot ? ring : slot + kSlot;
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
-                const bf8v xv = widen(x[h >> 1][2 * (h & 1)], x[h >> 1][2 * (h & 1) + 1], sx);
+                bf8v wv[R];
 #pragma unroll
-                for (int r = 0; r < R; ++r)
-                    acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        widen(w[r][h >> 1][2 * (h & 1)], w[r][h >> 1][2 * (h & 1) + 1], sw[r]), xv, acc[r], 0, 0, 0);
+                for (int r = 0; r < R; ++r) wv[r] = widen(w[r][h >> 1][2 * (h & 1)], w[r][h >> 1][2 * (h & 1) + 1], sw[r]);
+#pragma unroll
+                for (int j = 0; j < T; ++j) {
+                    const bf8v xv = widen(x[j][h >> 1][2 * (h & 1)], x[j][h >> 1][2 * (h & 1) + 1], sx[j]);
+#pragma unroll
+                    for (int r = 0; r < R; ++r) acc[r][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[r], xv, acc[r][j], 0, 0, 0);
+                }
             }
         }
     }
@@ -164,27 +173,30 @@ __global__ __launch_bounds__(512) void f8_gemv_kernel(const Args a) {
     if (a.ks > 1) {
         __syncthreads();
 #pragma unroll
-        for (int r = 0; r < R; ++r) *reinterpret_cast<lds_float4*>(ring + 1024u * r + 16u * l) = acc[r];
+        for (int i = 0; i < R * T; ++i) *reinterpret_cast<lds_float4*>(ring + 1024u * i + 16u * l) = acc[i / T][i % T];
         __syncthreads();
         if (wave) return;
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-            for (int p = 1; p < a.ks; ++p) acc[r] += *reinterpret_cast<lds_float4*>(ring + p * kWave + 1024u * r + 16u * l);
+        for (int i = 0; i < R * T; ++i)
+            for (int p = 1; p < a.ks; ++p) acc[i / T][i % T] += *reinterpret_cast<lds_float4*>(ring + p * kWave + 1024u * i + 16u * l);
     }
     // lane (q, c) holds rows 4 q .. 4 q + 3 of a tile for token c
-    const int64_t m = c;
-    if (m >= a.m) return;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int j = 0; j < T; ++j) {
+        const int64_t m = m0 + 16 * j + c;
+        if (m >= a.m) continue;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int64_t n = n0 + 16 * r + 4 * q + e;
-            if (n >= a.n) continue;
-            if (a.y_dtype == TL_F32) static_cast<float*>(a.y)[m * a.n + n] = acc[r][e];
-            else
-                static_cast<uint16_t*>(a.y)[m * a.n + n] =
-                    uint16_t(a.y_dtype == TL_F16 ? f16_bits(acc[r][e]) : bf16_bits(acc[r][e]));
-        }
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int64_t n = n0 + 16 * r + 4 * q + e;
+                if (n >= a.n) continue;
+                if (a.y_dtype == TL_F32) static_cast<float*>(a.y)[m * a.n + n] = acc[r][j][e];
+                else
+                    static_cast<uint16_t*>(a.y)[m * a.n + n] =
+                        uint16_t(a.y_dtype == TL_F16 ? f16_bits(acc[r][j][e]) : bf16_bits(acc[r][j][e]));
+            }
+    }
 }
 
 template <int R, int XI>
@@ -199,13 +211,22 @@ hipError_t launch(Args a, int64_t waves, hipStream_t stream) {
     ks = ks > most ? most : ks;
     ks = ks > a.chunks ? a.chunks : ks;
     a.ks = ks < 1 ? 1 : int(ks);
-    hipLaunchKernelGGL(kernel, dim3(unsigned(tiles)), dim3(64 * a.ks), unsigned(a.ks * wave_bytes<R, XI>()), stream, a);
+    const dim3 grid(unsigned(tiles), unsigned((a.m + 8 * XI - 1) / (8 * XI)));
+    hipLaunchKernelGGL(kernel, grid, dim3(64 * a.ks), unsigned(a.ks * wave_bytes<R, XI>()), stream, a);
     return hipGetLastError();
 }
 
 }  // namespace
 
-bool f8_gemv_fits(int64_t m) { return m <= 16; }
+// More than 16 tokens come in blocks of 32 where the product is so small that the other
+// kernels would cut K and add the parts in a second launch (us in a graph, here and
+// there: 2048 x 2048 by 17, 64, 128 tokens 6.3 7.8, 6.9 8.6, 8.9 9.5; 1024 x 5120 by 17,
+// 32, 64, 128 8.2 8.5, 9.7 8.7, 9.8 9.6, 9.8 10.5; called one by one, with that launch
+// and its workspace, 16 x 2560 by 18 6.4 11.4).  Past 40 chunks, ten a wave, cutting K
+// further wins: 512 x 7168 by 32 tokens 10.4 8.5.
+bool f8_gemv_fits(int64_t m, int64_t n, int64_t k) {
+    return m <= 16 || (k <= 5120 && ((n + 15) / 16) * ((m + 31) / 32) <= 256);
+}
 
 // Waves share a tile until there are about 1024 (512 where each brings 16 tokens'
 // activations too); from 320 tiles on, two tiles a wave share those.  Measured, us in
@@ -215,10 +236,10 @@ bool f8_gemv_fits(int64_t m) { return m <= 16; }
 // 25.4, 1024 x 5120 7.3 and 8.5.
 hipError_t launch_f8_gemv(const uint8_t* codes, const uint8_t* scales, const uint8_t* x, const uint8_t* x_scales,
                           int64_t m, int64_t n, int64_t k, void* y, int y_dtype, hipStream_t stream) {
-    if (!f8_gemv_fits(m)) return hipErrorInvalidValue;
-    const Args a = {codes, scales, x, x_scales, y, n, k, int(m), y_dtype, int(k / 128), 1};
+    const Args a = {codes, scales, x, x_scales, y, m, n, k, y_dtype, int(k / 128), 1};
     if (m <= 8) return launch<1, 1>(a, 1024, stream);
-    return n >= 16 * 320 ? launch<2, 2>(a, 512, stream) : launch<1, 2>(a, 512, stream);
+    if (m <= 16) return n >= 16 * 320 ? launch<2, 2>(a, 512, stream) : launch<1, 2>(a, 512, stream);
+    return launch<1, 4>(a, 4 * ((n + 15) / 16), stream);
 }
 
 }  // namespace tl

@@ -151,12 +151,12 @@ hipError_t launch_q4_gemv(const uint8_t* packed, const uint16_t* scales, int gro
                           int y_dtype, void* ws, hipStream_t stream);
 
 // 8-bit floating point rows with block scales: rounding, values, and the
-// product of rows with weights (few tokens, when f8_gemv_fits; any number)
+// product of rows with weights (when f8_gemv_fits; any number)
 hipError_t launch_f8_quantize(const void* x, int64_t m, int64_t k, int x_dtype, uint8_t* codes, uint8_t* scales,
                               hipStream_t stream);
 hipError_t launch_f8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t n, int64_t k, void* w,
                                 int w_dtype, hipStream_t stream);
-bool f8_gemv_fits(int64_t m);
+bool f8_gemv_fits(int64_t m, int64_t n, int64_t k);
 hipError_t launch_f8_gemv(const uint8_t* codes, const uint8_t* scales, const uint8_t* x, const uint8_t* x_scales,
                           int64_t m, int64_t n, int64_t k, void* y, int y_dtype, hipStream_t stream);
 int64_t f8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k);
