@@ -359,6 +359,36 @@ def test_weights_past_32_bits(gpu, m):
         assert not y[0].any() and not y[m - 1].any() and not y[m // 2].any()
 
 
+@pytest.mark.parametrize("out", ["f32", "f16"])
+@pytest.mark.parametrize("m,n,k", [(3, 515, 1024), (40, 96, 2048), (100, 1024, 7168), (300, 5200, 7040)])
+def test_captured_and_replayed(gpu, m, n, k, out):
+    """Two graphs over one workspace, one after the other, with other calls between."""
+    x, w = make(m, n, k, seed=m)
+    other = make(m, n, k, seed=m + 1)[0]
+    xc, xs, wc, ws = e4(x[0], gpu), e8(x[1], gpu), e4(w[0], gpu), e8(w[1], gpu)
+    room = torch.empty(max(16, tl.f8_gemm_workspace_bytes(m, n, k)), dtype=torch.uint8, device=gpu)
+    run = lambda **kw: tl.f8_gemm(wc, ws, xc, xs, out_dtype=TYPES[out], **kw)  # noqa: E731
+    want = run()
+    graphs, outs = [], []
+    for given in (room, room, None):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y = run(workspace=given)
+        graphs.append(g)
+        outs.append(y)
+    for i in range(3):
+        src = (other if i == 1 else x)
+        xc.view(torch.uint8).copy_(torch.from_numpy(src[0]))
+        xs.view(torch.uint8).copy_(torch.from_numpy(src[1]))
+        now = run()
+        for g, y in zip(graphs, outs):
+            y.zero_()
+            g.replay()
+            room.fill_(0xFF)
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, now) for y in outs) and torch.equal(now, want) == (i != 1)
+
+
 def test_linear_rounds_and_multiplies(gpu):
     g = torch.Generator().manual_seed(5)
     wf, xf = 0.02 * torch.randn(300, 1280, generator=g), torch.randn(9, 1280, generator=g)

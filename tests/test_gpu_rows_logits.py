@@ -162,6 +162,22 @@ def test_a_token_repeated_throughout(gpu):
     assert np.array_equal(got[:, :8999], np.ones((3, 8999)))
 
 
+def test_the_longest_histories_and_bias_lists(gpu):
+    """Counts and places beyond 16 bits."""
+    v, h, b = 20000, 70000, 70000
+    c = case(2, v, h, b, True, seed=9)
+    c["history"][0, ::2], c["history_lens"][0], c["prompt_lens"][0] = 7, h, 11
+    c["frequency"][:] = 2.0 ** -12
+    c["bias_ids"][1, :], c["bias_ids"][1, -1] = 3, 4
+    check(host(tl.adjust_logits(**to_device(c, "f32", gpu))), c, "f32", "f32")
+
+
+@pytest.mark.parametrize("m,v,h,b", [(1100, 501, 50, 3), (260, 30011, 700, 0), (520, 9001, 0, 40), (35, 250007, 300, 20)])
+def test_many_sequences(gpu, m, v, h, b):
+    c = case(m, v, h, b, True, seed=m)
+    check(host(tl.adjust_logits(**to_device(c, "bf16", gpu), out_dtype=torch.float32)), c, "bf16", "f32")
+
+
 def test_what_is_not_finite(gpu):
     inf, nan = float("inf"), float("nan")
     x = torch.tensor([[inf, -inf, nan, 1.0, nan, inf, -inf, -3.4e38]], device=gpu)
