@@ -36,7 +36,8 @@ def table(form, n, k, gpu, seed=0):
 
 @pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("form", ["f8", "q4_32", "q4_64", "q4_128"])
-@pytest.mark.parametrize("m,n,k", [(1, 1, 128), (7, 50, 384), (33, 1000, 1152), (2, 300, 5120), (600, 77, 128)])
+@pytest.mark.parametrize("m,n,k", [(1, 1, 128), (7, 50, 384), (33, 1000, 1152), (2, 300, 5120), (600, 77, 128),
+                                   (4099, 60, 2176)])
 def test_rows(gpu, m, n, k, form, out):
     args, values = table(form, n, k, gpu, seed=n)
     call = tl.f8_rows if form == "f8" else tl.q4_rows

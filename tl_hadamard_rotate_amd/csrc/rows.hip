@@ -6,7 +6,7 @@
 // value is exact in fp32, the product is rounded there and once more to the
 // output's type.  A lane takes 8 values; nothing is shared, so the bound is
 // memory (a prompt) or the latency of two dependent loads, id then row (a token).
-// us traced: 4096 rows of 5120 8-bit codes to bfloat16 12.1 (42 MB written), a row of 4-bit ones
+// us traced: 4096 rows of 5120 8-bit codes to bfloat16 12 (42 MB written), a row of 4-bit ones
 // 1.7.  Outputs are stored to stay in the caches, for the norm that reads them next.
 #include "elem.h"
 #include "f8.h"
@@ -41,44 +41,67 @@ struct E4M3 {
     }
 };
 
-template <typename W, typename T>
+// U pieces of 8 values a lane, all asked for before the first is stored
+template <typename W, typename T, int U>
 __global__ __launch_bounds__(kThreads) void rows_kernel(const uint8_t* __restrict__ codes,
                                                         const void* __restrict__ scales,
                                                         const int32_t* __restrict__ ids, int64_t m, int64_t n,
                                                         uint32_t eights, float factor, void* __restrict__ out) {
     // the workgroup's first item by one division of scalars, a lane's by 32-bit ones
-    const int64_t first = int64_t(blockIdx.x) * kThreads, row0 = first / eights;
-    const uint32_t off = uint32_t(first - row0 * eights) + threadIdx.x;
-    const int64_t row = row0 + off / eights;
-    const uint32_t j = off % eights;
-    if (row >= m) return;
-    const int32_t id = ids[row];
-    float v[8] = {};
-    if (id >= 0 && id < n) {
-        W::load(codes, scales, id, eights, j, v);
+    const int64_t first = int64_t(blockIdx.x) * (kThreads * U), row0 = first / eights;
+    const uint32_t off0 = uint32_t(first - row0 * eights) + threadIdx.x;
+    int64_t row[U];
+    uint32_t j[U];
+    int32_t id[U];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= factor;
+    for (int u = 0; u < U; ++u) {
+        const uint32_t off = off0 + u * kThreads;
+        row[u] = row0 + off / eights;
+        j[u] = off % eights;
+        id[u] = row[u] < m ? ids[row[u]] : -1;
     }
-    store8<T, true>(out, 8 * (row * eights + j), v);
+    float v[U][8] = {};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (id[u] < 0 || id[u] >= n) continue;
+        W::load(codes, scales, id[u], eights, j[u], v[u]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] *= factor;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (row[u] < m) store8<T, true>(out, 8 * (row[u] * eights + j[u]), v[u]);
 }
 
-template <typename W>
+template <typename W, int U>
 hipError_t rows(const uint8_t* codes, const void* scales, const int32_t* ids, int64_t m, int64_t n, int64_t k,
                 float factor, void* out, int out_dtype, hipStream_t stream) {
-    const auto kernel = out_dtype == TL_F32   ? rows_kernel<W, F32>
-                        : out_dtype == TL_F16 ? rows_kernel<W, F16>
-                                              : rows_kernel<W, BF16>;
+    const auto kernel = out_dtype == TL_F32   ? rows_kernel<W, F32, 1>
+                        : out_dtype == TL_F16 ? rows_kernel<W, F16, U>
+                                              : rows_kernel<W, BF16, U>;
+    const int per = kThreads * (out_dtype == TL_F32 ? 1 : U);
     const uint32_t eights = uint32_t(k / 8);
     const int64_t most = (int64_t(1) << 31) / eights;       // rows of a launch, whose lanes count in 32 bits
     for (int64_t at = 0; at < m; at += most) {
         const int64_t left = m - at < most ? m - at : most;
-        hipLaunchKernelGGL(kernel, dim3(unsigned((left * eights + kThreads - 1) / kThreads)), dim3(kThreads), 0, stream,
+        hipLaunchKernelGGL(kernel, dim3(unsigned((left * eights + per - 1) / per)), dim3(kThreads), 0, stream,
                            codes, scales, ids + at, left, n, eights, factor,
                            static_cast<uint8_t*>(out) + at * k * (out_dtype == TL_F32 ? 4 : 2));
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
+}
+
+// Two pieces a lane for outputs of 2 bytes where there are many.  us in a graph with one
+// and two: 4096 rows of 5120 8-bit codes to bfloat16 12.9 12.3 (outputs beyond the cache
+// 18.4 16.9), 16384 of 1024 11.1 10.8, 512 of 5120 4.2 4.4; to float32 4096 of 5120 26.6
+// 27.7.
+template <typename W>
+hipError_t rows(const uint8_t* codes, const void* scales, const int32_t* ids, int64_t m, int64_t n, int64_t k,
+                float factor, void* out, int out_dtype, hipStream_t stream) {
+    return m * k >= int64_t(1) << 23 ? rows<W, 2>(codes, scales, ids, m, n, k, factor, out, out_dtype, stream)
+                                     : rows<W, 1>(codes, scales, ids, m, n, k, factor, out, out_dtype, stream);
 }
 
 }  // namespace
