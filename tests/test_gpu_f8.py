@@ -167,7 +167,8 @@ def test_few_tokens(gpu, m, n, k, out):
 @pytest.mark.parametrize("m,n,k", [(65, 17, 128), (66, 300, 256), (128, 128, 384), (129, 257, 640), (200, 1, 896),
                                    (255, 511, 1152), (256, 256, 512), (257, 259, 2176), (300, 1030, 1280),
                                    (513, 70, 5120), (20, 4200, 640), (33, 9000, 384), (64, 5003, 1152),
-                                   (100, 2100, 896), (128, 4100, 256), (200, 1500, 5248), (40, 40, 5376)])
+                                   (100, 2100, 896), (128, 4100, 256), (200, 1500, 5248), (40, 40, 5376),
+                                   (66, 8371, 256), (90, 2741, 4480)])
 def test_many_tokens(gpu, m, n, k, out):
     x, w = make(m, n, k, seed=m + n + k, spread=4)
     check(x, w, TYPES[out], gpu)
@@ -274,7 +275,13 @@ def test_workspace_contents_do_not_matter(gpu):
 
 @pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("m,n,k", [(9, 40, 17408), (40, 150, 7040), (130, 130, 9984), (300, 300, 12800),
-                                   (600, 5200, 7040), (520, 700, 17408)])
+                                   (600, 5200, 7040), (520, 700, 17408),
+                                   # tiles of every shape, whole and cut
+                                   (33, 2084, 256), (81, 2741, 4480), (101, 2697, 3712), (65, 8371, 256),
+                                   (585, 3219, 256), (18, 5477, 3200), (19, 1241, 5504), (17, 16869, 256),
+                                   (33, 5462, 6400), (34, 5585, 4224), (33, 17109, 256), (67, 10982, 6400),
+                                   (131, 16163, 256), (130, 8329, 9856), (391, 5554, 5504), (389, 16929, 256),
+                                   (1100, 16700, 5248)])
 def test_long_sums_of_whole_numbers(gpu, m, n, k, out):
     """Every place of long rows counts, in whole and in cut tiles: codes of -1, 0 and
     1, sparse enough that sums stay exact in every type, under scales whose product

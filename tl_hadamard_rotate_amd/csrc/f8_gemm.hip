@@ -21,8 +21,8 @@
 // some groups of each row at a time.
 //
 // Two kernels:
-//  - some tokens: 128 weight rows by 32, 64 or 128 tokens, 4 waves, two workgroups on
-//    a compute unit.  Bound by the weights' bytes.
+//  - some tokens: 64 or 128 weight rows by 32, 64 or 128 tokens, 4 waves, two
+//    workgroups on a compute unit.  Bound by the weights' bytes.
 //  - many: 256 by 256, 8 waves, one workgroup.  Bound by the matrix cores' power: with
 //    zeros for data 8192 x 8192 x 8192 takes 295 us at 2.4 GHz, with random data 405 us
 //    at 1.7 GHz, 72 % of the cycles issuing matrix instructions.
@@ -194,27 +194,33 @@ __global__ __launch_bounds__(256) void f8_join_kernel(const Args a) {
     store8_rows(a, m0 + e, n0 + row, v);
 }
 
-// ---- some tokens: 128 weight rows by 32 IT tokens, a wave 32 of the rows ----
+// ---- some tokens: 32 RW weight rows by 32 IT tokens, four waves ----
+//
+// Wave w has 32 of the rows, w % RW, and with two such groups half of the tokens.
 
-constexpr int kMidThreads = 256, kMidRows = 128;
+constexpr int kMidThreads = 256;
 constexpr int kMidSegment = 24, kMidPitch = 28;     // groups of scales in LDS, and their bytes a row
 
-// blocks of K in LDS: as many as leave room for two workgroups
-template <int IT>
-constexpr int mid_stages() { return IT == 4 ? 2 : 3; }
-template <int IT>
-constexpr int mid_lds() { return (kMidRows + 32 * IT) * (128 * mid_stages<IT>() + kMidPitch); }
-static_assert(mid_lds<1>() <= 80 * 1024 && mid_lds<2>() <= 80 * 1024 && mid_lds<4>() <= 80 * 1024, "LDS");
+// blocks of K in LDS: as many as leave room for two workgroups, up to 4
+template <int RW, int IT>
+constexpr int mid_stages() {
+    constexpr int rows = 32 * (RW + IT), fit = (80 * 1024 - rows * kMidPitch) / (rows * 128);
+    return fit < 4 ? fit : 4;
+}
+template <int RW, int IT>
+constexpr int mid_lds() { return 32 * (RW + IT) * (128 * mid_stages<RW, IT>() + kMidPitch); }
 
-template <int IT, bool WIDE>
+template <int RW, int IT, bool WIDE>
 __global__ __launch_bounds__(kMidThreads) __attribute__((amdgpu_waves_per_eu(2))) void f8_gemm_mid_kernel(const Args a) {
-    constexpr int kTokens = 32 * IT, kAll = kMidRows + kTokens, kStage = kAll * 128, S = mid_stages<IT>(), kLoads = 4 + IT;
+    constexpr int kTileRows = 32 * RW, kTileTokens = 32 * IT, kAll = kTileRows + kTileTokens, kStage = kAll * 128;
+    constexpr int S = mid_stages<RW, IT>(), kLoads = RW + IT, J = IT * RW / 4;     // J: a wave's tiles of 32 x 32
+    static_assert((RW == 4 || RW == 2) && J >= 1 && S >= 2, "tiles");
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const uint32_t lds = lds_address(smem), scale_lds = lds + S * kStage;
     Item it;
     if (!find_item(a, it)) return;
     int64_t m0, n0;
-    tile_origin<kMidRows, kTokens>(a, it.tile, n0, m0);
+    tile_origin<kTileRows, kTileTokens>(a, it.tile, n0, m0);
     const int g0 = it.slot < 0 ? 0 : int(int64_t(it.part) * a.groups / a.splits);
     const int blocks = (it.slot < 0 ? a.groups : int(int64_t(it.part + 1) * a.groups / a.splits)) - g0;
 
@@ -228,17 +234,17 @@ __global__ __launch_bounds__(kMidThreads) __attribute__((amdgpu_waves_per_eu(2))
     uint32_t off[kLoads];
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
-        const int r = 8 * (u < 4 ? 4 * wave + u : IT * wave + u - 4) + (l >> 3);
-        off[u] = (u < 4 ? row_n(r) : row_m(r)) * uint32_t(a.k) + 16u * uint32_t((l & 7) ^ ((r >> 1) & 7));
+        const int r = 8 * (u < RW ? RW * wave + u : IT * wave + u - RW) + (l >> 3);
+        off[u] = (u < RW ? row_n(r) : row_m(r)) * uint32_t(a.k) + 16u * uint32_t((l & 7) ^ ((r >> 1) & 7));
     }
     const auto load = [&](int b, uint32_t stage) {      // (past the last block: that one again)
         const uint32_t at = 128u * uint32_t(b < blocks ? b : blocks - 1), to = lds + stage * kStage;
 #pragma unroll
         for (int u = 0; u < kLoads; ++u)
-            load_lds16((u < 4 ? wb : xb) + at, off[u], to + 1024u * uint32_t(u < 4 ? 4 * wave + u : 16 + IT * wave + u - 4));
+            load_lds16((u < RW ? wb : xb) + at, off[u], to + 1024u * uint32_t(u < RW ? RW * wave + u : 4 * RW + IT * wave + u - RW));
     };
     const auto all_scales = [&](int s0) {
-        const int r = tid - kMidRows;
+        const int r = tid - kTileRows;
         if (tid < kAll)
             stage_scales<kMidSegment>((r < 0 ? a.ws + (n0 + row_n(tid)) * a.groups : a.xs + (m0 + row_m(r)) * a.groups) + g0 + s0,
                                       blocks - s0, scale_lds + uint32_t(tid) * kMidPitch);
@@ -247,9 +253,10 @@ __global__ __launch_bounds__(kMidThreads) __attribute__((amdgpu_waves_per_eu(2))
     const uint32_t f = uint32_t(c) * 128u + 16u * uint32_t((2 * q) ^ ((c >> 1) & 7));
     const auto half = [&](uint32_t at, int h) { return fragment(at + (f ^ (64u * h)), at + (f ^ (64u * h) ^ 16u)); };
 
-    float16v acc[IT];
+    const int rg = wave % RW, tg = wave / RW * J;       // the wave's rows, its first tokens
+    float16v acc[J];
 #pragma unroll
-    for (int j = 0; j < IT; ++j)
+    for (int j = 0; j < J; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[j][r] = 0.0f;
 #pragma unroll
@@ -269,21 +276,21 @@ __global__ __launch_bounds__(kMidThreads) __attribute__((amdgpu_waves_per_eu(2))
             fill = fill == S - 1 ? 0 : fill + 1;
             const uint32_t at = lds + stage * kStage;
             stage = stage == S - 1 ? 0 : stage + 1;
-            const int ws = *reinterpret_cast<lds_u8*>(sc + 32u * uint32_t(wave) * kMidPitch);
-            int xs[IT];
+            const int ws = *reinterpret_cast<lds_u8*>(sc + 32u * uint32_t(rg) * kMidPitch);
+            int xs[J];
 #pragma unroll
-            for (int j = 0; j < IT; ++j) xs[j] = *reinterpret_cast<lds_u8*>(sc + uint32_t(kMidRows + 32 * j) * kMidPitch);
+            for (int j = 0; j < J; ++j) xs[j] = *reinterpret_cast<lds_u8*>(sc + uint32_t(kTileRows + 32 * (tg + j)) * kMidPitch);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int8v wf = half(at + 4096u * uint32_t(wave), h);
+                const int8v wf = half(at + 4096u * uint32_t(rg), h);
                 bf8v wv[4];
                 if constexpr (WIDE) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) wv[e] = widen(uint32_t(wf[2 * e]), uint32_t(wf[2 * e + 1]), uint32_t(ws));
                 }
 #pragma unroll
-                for (int j = 0; j < IT; ++j) {
-                    const int8v xf = half(at + 128u * uint32_t(kMidRows + 32 * j), h);
+                for (int j = 0; j < J; ++j) {
+                    const int8v xf = half(at + 128u * uint32_t(kTileRows + 32 * (tg + j)), h);
                     if constexpr (WIDE) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
@@ -303,9 +310,9 @@ __global__ __launch_bounds__(kMidThreads) __attribute__((amdgpu_waves_per_eu(2))
     // no load may write LDS that belongs to another workgroup
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
-    for (int j = 0; j < IT; ++j) {
-        if (it.slot >= 0) store_sums<kMidRows>(acc[j], a.sums + size_t(it.slot) * (kMidRows * kTokens), 32 * wave, 32 * j + c, q);
-        else store_tile(acc[j], a, n0 + 32 * wave, m0 + 32 * j + c, q);
+    for (int j = 0; j < J; ++j) {
+        if (it.slot >= 0) store_sums<kTileRows>(acc[j], a.sums + size_t(it.slot) * (kTileRows * kTileTokens), 32 * rg, 32 * (tg + j) + c, q);
+        else store_tile(acc[j], a, n0 + 32 * rg, m0 + 32 * (tg + j) + c, q);
     }
 }
 
@@ -561,39 +568,47 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 // ---- which kernel, and how K is cut ----
 
 struct Plan {
-    int it;             // 32 it tokens a tile of 128 weight rows; 8: the 256 x 256 kernel
+    int rw, it;         // 32 rw weight rows by 32 it tokens a tile; 8 by 8: the large kernel
     int splits;
     int64_t tiles_m, tiles_n, tiles, whole;
-    int64_t sums() const { return splits > 1 ? (tiles - whole) * splits * (it == 8 ? 65536 : 4096 * it) * 4 : 0; }
+    int64_t sums() const { return splits > 1 ? (tiles - whole) * splits * 1024 * it * rw * 4 : 0; }
 };
 
 constexpr int64_t kMostSums = int64_t(1) << 28;
 
-// The plan with the least estimated time.  What it weighs was measured over 500 x 640
-// to 131072 x 5120 by 17 to 4096 tokens, weights not in the caches, and picks within a
-// few per cent of the best cut of nearly every one: a block of 128 K takes the busiest
-// compute unit `each` us for every workgroup on it, `alone` where it has one; weights
-// and activations arrive at 5.2 bytes per ps, longer by half of what an uneven load
-// leaves idle; operands at 10 from the caches; the second kernel costs 3 us, 0.2 a
-// part, and its sums, written and read, 5 bytes per ps.  (17408 x 5120 by 64 tokens
-// takes 30 us in tiles of 64 tokens, 36 in tiles of 32, 112 with a ring of chunks a
-// wave; by 512 66 us in tiles of 256 x 256, 87 in tiles of 128 x 128.)
+// The plan with the least estimated time.  What it weighs was fitted to the times of
+// every kernel and cut over 273 products (512 x 7168 to 131072 x 5120 by 18 to 800
+// tokens, most with weights not in the caches); on 220 others it takes 1.3 % longer than
+// the best cut of each on average.  A block of 128 K takes the busiest compute unit
+// `each` us for every workgroup on it, `alone` where it has one; weights and activations
+// arrive at 6.1 bytes per ps, longer by half of what an uneven load leaves idle;
+// operands at 10 from the caches; the second kernel costs 3.3 us, 0.31 a part, and its
+// sums, written and read, 4.9 bytes per ps.  (us, tiles of 128 rows only and of 64 too:
+// 4096 x 4096 by 200 tokens 17.8 13.0, 8192 x 8192 by 200 41.0 33.6, 6144 x 5120 by 100
+// 20.6 17.1, 17408 x 5120 by 64 32.1 33.9.  17408 x 5120 by 64 in tiles of 64 tokens 30,
+// of 32 36; by 512 66 in tiles of 256 x 256, 87 in tiles of 128 x 128.)
 Plan make_plan(int64_t m, int64_t n, int64_t k, bool wide) {
-    static const double kEach[2][4] = {{0.42, 0.50, 0.65, 1.6}, {0.50, 0.65, 1.0, 2.9}};
-    static const double kAlone[2][4] = {{0.60, 0.68, 1.0, 1.6}, {0.65, 0.85, 1.4, 2.9}};
+    struct Kind {
+        int rw, it;
+        double each[2], alone[2];       // of 16-bit outputs, of float32
+    };
+    static const Kind kinds[] = {{4, 1, {0.42, 0.50}, {0.67, 0.65}}, {2, 2, {0.36, 0.44}, {0.39, 0.53}},
+                                 {4, 2, {0.65, 0.65}, {0.68, 0.85}}, {2, 4, {0.49, 0.65}, {0.62, 0.85}},
+                                 {4, 4, {0.72, 1.01}, {1.24, 1.40}}, {8, 8, {2.00, 2.90}, {2.00, 2.90}}};
     const int64_t cus = cu_count(), groups = k / 128;
     Plan best = {};
     double least = 0;
-    for (int i = 0; i < 4; ++i) {
+    for (const Kind& kind : kinds) {
         Plan p;
-        p.it = 1 << i;
-        if (i > 0 && 16 * p.it >= m) break;      // (half the tokens or more of every tile absent)
+        p.rw = kind.rw;
+        p.it = kind.it;
+        if (p.it > 2 && 16 * p.it >= m) break;      // (half the tokens or more of every tile absent)
         const bool big = p.it == 8;
-        const int64_t rows = big ? kRows : kMidRows;
+        const int64_t rows = 32 * p.rw;
         p.tiles_m = (m + 32 * p.it - 1) / (32 * p.it);
         p.tiles_n = (n + rows - 1) / rows;
         p.tiles = p.tiles_m * p.tiles_n;
-        const double bytes = double(n + m) * k / 5.2e6, caches = double(p.tiles) * (rows + 32 * p.it) * k / 10e6;
+        const double bytes = double(n + m) * k / 6.1e6, caches = double(p.tiles) * (rows + 32 * p.it) * k / 10e6;
         for (p.splits = 1; p.splits <= 16 && p.splits <= groups; ++p.splits) {
             // the large kernel cuts only the tiles of the last, partial round
             p.whole = p.splits == 1 ? p.tiles : big ? p.tiles / cus * cus : 0;
@@ -603,11 +618,11 @@ Plan make_plan(int64_t m, int64_t n, int64_t k, bool wide) {
             const int64_t in_whole = (p.whole + cus - 1) / cus, in_cut = (cut + cus - 1) / cus;
             const double busiest = double(in_whole * groups + in_cut * part);     // blocks of a compute unit
             const double mean = double(p.whole * groups + cut * part) / cus;
-            double us = busiest * (in_whole + in_cut == 1 ? kAlone : kEach)[wide][i];
+            double us = busiest * (in_whole + in_cut == 1 ? kind.alone : kind.each)[wide];
             const double memory = bytes * (0.5 + 0.5 * busiest / mean);
             us = us > memory ? us : memory;
             us = us > caches ? us : caches;
-            if (p.splits > 1) us += 3.0 + 0.2 * p.splits + 2 * double(p.sums()) / 5e6;
+            if (p.splits > 1) us += 3.3 + 0.31 * p.splits + 2 * double(p.sums()) / 4.9e6;
             if (least == 0 || us < least) {
                 least = us;
                 best = p;
@@ -656,10 +671,13 @@ hipError_t run(void (*kernel)(const Args), int threads, int lds, Args a, const P
 
 template <bool WIDE>
 hipError_t run(const Args& a, const Plan& p, hipStream_t stream) {
-    switch (p.it) {
-        case 1: return run<kMidRows, 32>(f8_gemm_mid_kernel<1, WIDE>, kMidThreads, mid_lds<1>(), a, p, stream);
-        case 2: return run<kMidRows, 64>(f8_gemm_mid_kernel<2, WIDE>, kMidThreads, mid_lds<2>(), a, p, stream);
-        case 4: return run<kMidRows, 128>(f8_gemm_mid_kernel<4, WIDE>, kMidThreads, mid_lds<4>(), a, p, stream);
+    constexpr int t = kMidThreads;
+    switch (10 * p.rw + p.it) {
+        case 41: return run<128, 32>(f8_gemm_mid_kernel<4, 1, WIDE>, t, mid_lds<4, 1>(), a, p, stream);
+        case 42: return run<128, 64>(f8_gemm_mid_kernel<4, 2, WIDE>, t, mid_lds<4, 2>(), a, p, stream);
+        case 44: return run<128, 128>(f8_gemm_mid_kernel<4, 4, WIDE>, t, mid_lds<4, 4>(), a, p, stream);
+        case 22: return run<64, 64>(f8_gemm_mid_kernel<2, 2, WIDE>, t, mid_lds<2, 2>(), a, p, stream);
+        case 24: return run<64, 128>(f8_gemm_mid_kernel<2, 4, WIDE>, t, mid_lds<2, 4>(), a, p, stream);
     }
     return run<kRows, kTokens>(f8_gemm_big_kernel<WIDE>, kThreads, kBigLds, a, p, stream);
 }
