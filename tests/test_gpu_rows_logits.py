@@ -237,6 +237,18 @@ def test_logits_past_32_bits(gpu):
     assert not any(bool(x[i:i + 512].any()) for i in range(0, m, 512))
 
 
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+def test_logits_larger_than_the_caches(gpu, out):
+    """Rows that start at every alignment of the type."""
+    m, v = 530, 131075
+    x = (torch.arange(m * v, device=gpu, dtype=torch.int32) % 251).view(m, v).to(torch.bfloat16)
+    big = torch.full((m + 1, v), 7.0, dtype=TYPES[out], device=gpu)
+    ids = torch.stack([torch.arange(m, device=gpu), torch.full((m,), v - 1, device=gpu)], 1).int().contiguous()
+    tl.adjust_logits(x, bias_ids=ids, bias_values=torch.full((m, 2), 4.0, device=gpu), out_dtype=TYPES[out], out=big[:m])
+    want = x.float().scatter_add_(1, ids.long(), torch.full((m, 2), 4.0, device=gpu)).to(TYPES[out])
+    assert torch.equal(big[:m], want) and bool((big[m] == 7).all())
+
+
 def test_rows_past_one_launch(gpu):
     """More lanes of 8 values than a launch has."""
     m, n, k = 1 << 24, 1000, 1152

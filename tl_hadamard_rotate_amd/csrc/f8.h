@@ -23,7 +23,7 @@ __device__ __forceinline__ float scale_value(uint32_t b) {
     return __builtin_bit_cast(float, b == 255 ? 0x7FC00000u : b == 0 ? 0x00400000u : b << 23);
 }
 
-// the values of 8 codes; exact in fp32 (but below 2^-126)
+// the values of 8 codes, exact in fp32
 __device__ __forceinline__ void values8(uint2 c, float s, float (&v)[8]) {
     typedef float f2 __attribute__((ext_vector_type(2)));
     const uint32_t w[2] = {c.x, c.y};

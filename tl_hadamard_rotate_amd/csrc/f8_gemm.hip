@@ -118,12 +118,18 @@ __device__ __forceinline__ uint32_t pair(int type, float u, float v) {
     return type == TL_F16 ? f16_bits(u) | f16_bits(v) << 16 : bf16_pair(u, v);
 }
 
+// 16 bytes at any alignment of the type (of a copy of bytes the compiler makes stores
+// of 12 and 4 bytes, some shared with the row's end)
+typedef float float4_at4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
+
 // 8 weight rows of a token to y
 __device__ __forceinline__ void store8_rows(const Args& a, int64_t token, int64_t n, const float (&v)[8]) {
     if (a.y_dtype == TL_F32) {
         float* y = static_cast<float*>(a.y) + token * a.n + n;
         if (n + 8 <= a.n) {
-            __builtin_memcpy(y, v, 32);
+            reinterpret_cast<float4_at4*>(y)[0] = float4_at4{v[0], v[1], v[2], v[3]};
+            reinterpret_cast<float4_at4*>(y)[1] = float4_at4{v[4], v[5], v[6], v[7]};
         } else {
 #pragma unroll
             for (int r = 0; r < 8; ++r)
@@ -136,7 +142,7 @@ __device__ __forceinline__ void store8_rows(const Args& a, int64_t token, int64_
     for (int r = 0; r < 4; ++r) w[r] = pair(a.y_dtype, v[2 * r], v[2 * r + 1]);
     uint16_t* y = static_cast<uint16_t*>(a.y) + token * a.n + n;
     if (n + 8 <= a.n) {
-        __builtin_memcpy(y, w, 16);
+        *reinterpret_cast<u32x4_at2*>(y) = u32x4_at2{w[0], w[1], w[2], w[3]};
     } else {
 #pragma unroll
         for (int r = 0; r < 8; ++r)
@@ -556,7 +562,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
         if (token >= a.m) continue;
         uint16_t* y = static_cast<uint16_t*>(a.y) + token * a.n + n;
         if (n + 8 <= a.n) {
-            __builtin_memcpy(y, &v, 16);
+            *reinterpret_cast<u32x4_at2*>(y) = u32x4_at2{v[0], v[1], v[2], v[3]};
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)

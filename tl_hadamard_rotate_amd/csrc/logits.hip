@@ -31,6 +31,7 @@ struct Args {
     void* out;
     int64_t v, h, b, row0;       // row0: the launch's first row
     uint32_t slices;
+    bool stream;                 // stores past the caches' replacement order
 };
 
 // 4 elements, at any alignment of the type (rows of an odd vocabulary)
@@ -111,6 +112,19 @@ struct Table {
         }
     }
 };
+
+// 4 elements as one vector, aligned as an element is (of a copy of bytes the compiler
+// makes stores of 12 and 4 bytes, one of them shared with the row's end)
+template <typename U>
+using Vector = uint32_t __attribute__((ext_vector_type(U::kBytes), aligned(U::kBytes)));
+
+template <typename U>
+__device__ __forceinline__ Vector<U> as_vector(const Raw<U>& r) {
+    Vector<U> v;
+#pragma unroll
+    for (int j = 0; j < U::kBytes; ++j) v[j] = r.w[j];
+    return v;
+}
 
 template <typename T, typename U, int I, bool WIDE>
 __global__ __launch_bounds__(1024) void adjust_logits_kernel(const Args a) {
@@ -233,7 +247,14 @@ __global__ __launch_bounds__(1024) void adjust_logits_kernel(const Args a) {
         Raw<U> res;
         pack<U>(x, res);
         if (at + 4 <= v) {
-            __builtin_memcpy(out + at, &res, sizeof(res));
+            Vector<U>* const to = reinterpret_cast<Vector<U>*>(out + at);
+            if (a.stream) {     // (the empty statements keep the compiler from making one plain store of both)
+                asm volatile("");
+                __builtin_nontemporal_store(as_vector(res), to);
+                asm volatile("");
+            } else {
+                *to = as_vector(res);
+            }
         } else {
             Elem<U> e[4];
             __builtin_memcpy(e, &res, sizeof(res));
@@ -267,9 +288,11 @@ hipError_t launch(Args a, int64_t m, unsigned threads, hipStream_t stream) {
 // a graph, slices of 2048, 8192, 16384, 32768 tokens: 64 rows of 131072 bfloat16 to
 // float32 logits, 8192 ids, 300 biases 22.7 18.3 16.8 17.9; one row of float32, 2048
 // ids, 16 biases 4.6 5.3 7.2 10.7.  The first moves 52 MB: the reads overlap the ids
-// of the history, the stores (33 MB, 6 us) begin when those are done.  (Stores past the
-// caches' replacement order: 14.8, but a maximum over each row behind it takes 12 us
-// longer then.)
+// of the history, the stores (33 MB, 6 us) begin when those are done.
+// Outputs of half the 256 MB last-level cache and more are stored past the caches'
+// replacement order, us alone and with a maximum over each row behind: 512 rows of
+// 131072 float32 94 and 145 (99 and 153), 256 37 and 86 (49 and 93); 128 20 and 58 (22
+// and 47), 64 14.8 and 53 (17 and 41).
 template <typename T, typename U>
 hipError_t launch_sized(const Args& a, int64_t m, hipStream_t stream) {
     const int64_t cus = cu_count(), slots = m * ((a.v + 8191) / 8192);
@@ -294,7 +317,8 @@ hipError_t launch_adjust_logits(const void* logits, int64_t m, int64_t v, int dt
                                 void* out, int out_dtype, hipStream_t stream) {
     // (a history of no tokens, or biases of none, are as good as absent)
     const Args a = {logits, h ? history : nullptr, history_lens, prompt_lens, repetition, presence, frequency,
-                    b ? bias_ids : nullptr, bias_values, reinterpret_cast<const uint8_t*>(mask), out, v, h, b, 0, 0};
+                    b ? bias_ids : nullptr, bias_values, reinterpret_cast<const uint8_t*>(mask), out, v, h, b, 0, 0,
+                    m * v * (out_dtype == TL_F32 ? 4 : 2) >= int64_t(1) << 27};
     return dtype == TL_F32   ? launch_out<F32>(a, m, out_dtype, stream)
            : dtype == TL_F16 ? launch_out<F16>(a, m, out_dtype, stream)
                              : launch_out<BF16>(a, m, out_dtype, stream);
