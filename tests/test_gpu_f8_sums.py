@@ -1,0 +1,170 @@
+"""What the sums of the 8-bit floating point product hold: fp32 for every output
+type and size, and fewer bits only where the caller allows them (``approx``).
+
+Tolerances, u = 2^-24, as in test_gpu_f8: fp32 sums of exact products are within
+    2 u (K/32 + 56) * sum |x w|.
+On the 8-bit matrix instructions each of 8 neighbouring products is cut below 2^-13
+of the largest exponent's unit: an error of rms 2^-13 / sqrt(3) of the largest
+product for each of 8, so that one eight is off by at most 2^-13 sqrt(8 / 3) = 2.0e-4
+of its largest product and a sum, rms over many, by 2.0e-4 sqrt(sum x^2 w^2).  That
+ceiling has every product cut; a product of two codes has 8 bits, and only those 2^-6
+of the largest and smaller are cut at all.  The header states 1.5e-5 and 4.3e-5
+(outliers); 1e-4 is the bound here, half of the ceiling."""
+import functools
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import tl_hadamard_rotate_amd as tl
+from tests import test_gpu_f8 as f8
+from tests.test_gpu_f8 import TYPES, U, call, e4, e8, host, make
+
+pytestmark = pytest.mark.gpu
+
+# the kernel of few tokens, then every tile of the two others, whole, cut, and both
+SIZES = [(1, 300, 1280), (16, 515, 640), (17, 48, 2048), (64, 80, 4096), (128, 300, 5120), (32, 4096, 640),
+         (33, 2091, 128), (18, 17, 5248), (324, 5429, 128), (1094, 257, 3712), (17, 16444, 128), (17, 1259, 5760),
+         (33, 16585, 128), (35, 5893, 3712), (268, 19756, 128), (66, 11551, 5376), (391, 18909, 128),
+         (193, 17209, 3456), (944, 16478, 640), (66, 2833, 4992), (65, 8228, 128), (19, 5519, 3200),
+         (33, 5947, 5760), (65, 10910, 6400), (131, 16324, 128), (129, 11856, 7296), (1447, 10943, 640)]
+
+
+@pytest.mark.parametrize("m,n,k", SIZES)
+def test_16_bit_outputs_are_the_float32_ones_rounded(gpu, m, n, k):
+    g = torch.Generator(device=gpu).manual_seed(m)
+    x = torch.randn(m, k, generator=g, device=gpu)
+    x = torch.where(torch.rand(m, k, generator=g, device=gpu) < 0.01, 20 * x, x)
+    xq, wq = tl.f8_quantize(x), tl.f8_quantize(0.02 * torch.randn(n, k, generator=g, device=gpu))
+    full = tl.f8_gemm(*wq, *xq, out_dtype=torch.float32)
+    for dt in (torch.float16, torch.bfloat16):
+        assert torch.equal(tl.f8_gemm(*wq, *xq, out_dtype=dt), full.to(dt))
+
+
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("m,n,k", SIZES)
+def test_small_products_beside_large_ones(gpu, m, n, k, out):
+    """Pairs of eights hold 64 and -64, and 2^-9 beside each, under a sign for each
+    row and pair: the large ones cancel, the small ones are the sum.  At most 512 eights
+    are used, so that every partial sum is below 2^15 in steps of 2^-9: 24 bits."""
+    rng = np.random.default_rng(m + n + k)
+    eights = rng.permutation(k // 8)[:min(512, k // 8 // 2 * 2)]
+    pairs = len(eights) // 2
+    r, s = rng.choice([-1, 1], (m, pairs)), rng.choice([-1, 1], (n, pairs))
+    xv, wv = np.zeros((m, k), np.float32), np.zeros((n, k), np.float32)
+    for side, large in ((0, 64.0), (1, -64.0)):
+        at = 8 * eights[side::2][:pairs]
+        lead, small = rng.integers(0, 4, pairs), rng.integers(4, 8, pairs)
+        xv[:, at + lead], xv[:, at + small] = large * r, 2.0 ** -9 * r
+        wv[:, at + lead], wv[:, at + small] = s, s
+    want = 2.0 ** -8 * (torch.from_numpy(r).float() @ torch.from_numpy(s).float().T)    # at most 256 steps: exact in each type
+    one = lambda rows: torch.full((rows, k // 128), 127, dtype=torch.uint8, device=gpu).view(torch.float8_e8m0fnu)  # noqa: E731
+    codes = lambda v: torch.from_numpy(v).to(gpu).to(torch.float8_e4m3fn)  # noqa: E731
+    got = tl.f8_gemm(codes(wv), one(n), codes(xv), one(m), out_dtype=TYPES[out])
+    assert torch.equal(got.float().cpu(), want)
+
+
+def cancelling(m, n, k, outliers, gpu):
+    """Rows whose second half repeats the first, places exchanged within each block of
+    128 (so that other products meet in an eight), with the weights' signs turned: every
+    sum is 0, and what comes out is the error, too small for the output to round away."""
+    g = torch.Generator(device=gpu).manual_seed(m + n + k)
+    h = k // 2
+    x, w = torch.randn(m, h, generator=g, device=gpu), torch.randn(n, h, generator=g, device=gpu)
+    if outliers:
+        x = torch.where(torch.rand(m, h, generator=g, device=gpu) < 0.01, 20 * x, x)
+    p = torch.randperm(128, generator=g, device=gpu)
+    swap = lambda t: t.view(-1, h // 128, 128)[:, :, p].reshape(-1, h)  # noqa: E731
+    xq, wq = tl.f8_quantize(torch.cat([x, swap(x)], 1)), tl.f8_quantize(torch.cat([w, -swap(w)], 1))
+    a, b = (tl.f8_dequantize(*q, out_dtype=torch.float32) for q in (xq, wq))
+    return xq, wq, a.abs() @ b.abs().T, ((a * a) @ (b * b).T).sqrt()
+
+
+@pytest.mark.parametrize("outliers", [False, True])
+@pytest.mark.parametrize("m,n,k", [(40, 96, 2048), (100, 4100, 1280), (200, 1500, 5376), (300, 5200, 7168), (66, 2833, 4864),
+                                   (65, 10910, 6400), (129, 11856, 7424), (520, 700, 17408), (1100, 16700, 5120)])
+def test_the_error_of_a_sum(gpu, m, n, k, outliers):
+    xq, wq, total, size = cancelling(m, n, k, outliers, gpu)
+    for dt in (torch.float16, torch.bfloat16):
+        got = tl.f8_gemm(*wq, *xq, out_dtype=dt).float()
+        # (sum |x w| above is itself within 2^-10, the output adds half a step)
+        assert bool((got.abs() <= 1.01 * 2 * U * (k / 32 + 56) * total + 2.0 ** -25).all())
+        got = tl.f8_gemm(*wq, *xq, out_dtype=dt, approx=True).float()
+        assert float(got.square().mean().sqrt() / size.square().mean().sqrt()) <= 1e-4
+
+
+@pytest.mark.parametrize("m,n,k", [(40, 150, 7040), (66, 2833, 4992), (300, 5200, 7040), (1447, 10943, 640)])
+def test_approximate_sums_keep_14_bits(gpu, m, n, k):
+    """1, 2^-13 and -1: what lies 2^-13 below is kept."""
+    xv = torch.zeros(m, k, device=gpu)
+    xv[:, 130], xv[:, 133], xv[:, 250] = 64, 2.0 ** -7, -64
+    one = lambda rows: torch.full((rows, k // 128), 127, dtype=torch.uint8, device=gpu).view(torch.float8_e8m0fnu)  # noqa: E731
+    got = tl.f8_gemm(torch.ones(n, k, device=gpu).to(torch.float8_e4m3fn), one(n), xv.to(torch.float8_e4m3fn), one(m),
+                     out_dtype=torch.float16, approx=True)
+    assert bool((got == 2.0 ** -7).all())
+
+
+# ---------------------------------------------------------------- approx: the product's other tests
+
+@pytest.fixture
+def approx(monkeypatch):
+    monkeypatch.setattr(tl, "f8_gemm", functools.partial(tl.f8_gemm, approx=True))
+
+
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("m,n,k", [(1, 1000, 5120), (16, 515, 640), (64, 80, 4096), (65, 17, 5248), (129, 257, 640),
+                                   (200, 1, 896), (257, 259, 2176), (300, 1030, 1280), (20, 4200, 640), (33, 9000, 384),
+                                   (100, 2100, 896), (200, 1500, 5248), (66, 8371, 256)])
+def test_approximate_products(gpu, approx, m, n, k, out):
+    f8.test_many_tokens(gpu, m, n, k, out)
+
+
+@pytest.mark.parametrize("m,n,k", SIZES)
+def test_approximate_sums_of_whole_numbers(gpu, approx, m, n, k):
+    f8.test_long_sums_of_whole_numbers(gpu, m, n, k, "f16")
+
+
+@pytest.mark.parametrize("m", [20, 100, 300])
+@pytest.mark.parametrize("k", [1152, 5376])
+def test_approximate_products_scales_and_nan(gpu, approx, m, k):
+    f8.test_every_scale_reaches_its_block(gpu, m, "bf16", k)
+    f8.test_nan_and_zero_stay_in_their_rows(gpu, m, "f16", k)
+    f8.test_scales_far_from_one(gpu, m, "bf16", k)
+    f8.test_rows_cut_out_of_others(gpu, m, k)
+    f8.test_nothing_behind_the_rows_is_written(gpu, m, k)
+
+
+@pytest.mark.parametrize("m,n,k", [(40, 96, 6016), (100, 4100, 1280), (300, 520, 6016)])
+def test_approximate_products_repeat_and_replay(gpu, approx, m, n, k):
+    f8.test_same_bits_again_and_alone(gpu, m, n, k)
+    f8.test_captured_and_replayed(gpu, m, n, k, "f16")
+
+
+@pytest.mark.parametrize("m", [40, 1100])
+def test_approximate_weights_past_32_bits(gpu, approx, m):
+    f8.test_weights_past_32_bits(gpu, m)
+
+
+def test_approximate_products_change_nothing_else(gpu):
+    """Float32 outputs, few tokens and small products are the same bits."""
+    for m, n, k, out in ((300, 1030, 1280, "f32"), (16, 515, 6400, "bf16"), (17, 48, 2048, "f16"), (32, 4096, 5120, "f16")):
+        x, w = make(m, n, k, seed=m)
+        assert torch.equal(call(x, w, TYPES[out], gpu), call(x, w, TYPES[out], gpu, approx=True))
+    x, w = make(32, 4112, 5120, seed=1)         # a tile of weight rows more: the 8-bit instructions
+    assert not torch.equal(call(x, w, torch.float16, gpu), call(x, w, torch.float16, gpu, approx=True))
+
+
+def test_linear_allows_approximate_sums(gpu):
+    g = torch.Generator().manual_seed(6)
+    codes, scales = tl.f8_quantize(0.02 * torch.randn(300, 1280, generator=g).to(gpu))
+    x = torch.randn(300, 1280, generator=g).to(gpu)
+    for approx in (False, True):
+        got = tl.F8Linear(codes, scales, approx=approx)(x, out_dtype=torch.float16)
+        assert torch.equal(got, tl.f8_gemm(codes, scales, *tl.f8_quantize(x), out_dtype=torch.float16, approx=approx))
+    want = oracle.f8_values(f8.raw(codes), f8.raw(scales))
+    xv = oracle.f8_values(*(f8.raw(t) for t in tl.f8_quantize(x)))
+    full = xv @ want.T
+    got = host(tl.F8Linear(codes, scales)(x, out_dtype=torch.float16))
+    tol = 2 * U * (1280 / 32 + 56) * (np.abs(xv) @ np.abs(want).T) + 2.0 ** -11 * np.abs(full) + 2.0 ** -25
+    assert np.all(np.abs(got - full) <= tol)

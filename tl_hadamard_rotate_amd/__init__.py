@@ -82,6 +82,7 @@ def lib() -> ctypes.CDLL:
             "tl_f8_dequantize": (i32, [p, p, i64, i64, p, i32, p]),
             "tl_f8_gemm_workspace_bytes": (i64, [i64, i64, i64]),
             "tl_f8_gemm": (i32, [p, p, p, p, i64, i64, i64, p, i32, p, i64, p]),
+            "tl_f8_gemm_approx": (i32, [p, p, p, p, i64, i64, i64, p, i32, p, i64, p]),
             "tl_q4_rows": (i32, [p, p, i32, p, i64, i64, i64, f32, p, i32, p]),
             "tl_f8_rows": (i32, [p, p, p, i64, i64, i64, f32, p, i32, p]),
             "tl_adjust_logits": (i32, [p, i64, i64, i32, p, i64, p, p, p, p, p, p, p, i64, p, p, i32, p]),
@@ -672,7 +673,7 @@ def f8_dequantize(codes, scales, out_dtype=torch.float16, out=None) -> torch.Ten
 
 
 def f8_gemm_workspace_bytes(m: int, n: int, k: int) -> int:
-    """Device workspace bytes tl_f8_gemm needs (0: none)."""
+    """Device workspace bytes tl_f8_gemm and tl_f8_gemm_approx need (0: none)."""
     b = int(lib().tl_f8_gemm_workspace_bytes(m, n, k))
     if b < 0:
         raise TLError("tl_f8_gemm_workspace_bytes", 2)
@@ -686,11 +687,15 @@ def _f8_workspace(index: int, m: int, n: int, k: int) -> int:
         return f8_gemm_workspace_bytes(m, n, k)
 
 
-def f8_gemm(codes, scales, x, x_scales, out_dtype=torch.float32, out=None, workspace=None) -> torch.Tensor:
+def f8_gemm(codes, scales, x, x_scales, out_dtype=torch.float32, out=None, workspace=None,
+            approx=False) -> torch.Tensor:
     """y[M, N] = x . w^T with both in 8-bit floating point (``f8_quantize``):
     weights codes [N, K] and scales, activations x [M, K] and x_scales, one
-    token or a prompt.  ``workspace`` (uint8, at least
-    ``f8_gemm_workspace_bytes``) is taken from torch's allocator when not given."""
+    token or a prompt.  Products are exact and their sums fp32; ``approx``
+    allows float16 and bfloat16 outputs sums of 14 bits in every 8 products,
+    in about half the time for a prompt (tl_f8_gemm_approx).  ``workspace``
+    (uint8, at least ``f8_gemm_workspace_bytes``) is taken from torch's
+    allocator when not given."""
     n, k, index = _f8_shape(codes, scales)
     m, kx, at = _f8_shape(x, x_scales, "x")
     if kx != k or at != index:
@@ -712,20 +717,21 @@ def f8_gemm(codes, scales, x, x_scales, out_dtype=torch.float32, out=None, works
         if wb:
             workspace = torch.empty(wb, dtype=_U8, device=codes.device)
             wp = workspace.data_ptr()
-    _call("tl_f8_gemm", index, (codes.data_ptr(), scales.data_ptr(), x.data_ptr(), x_scales.data_ptr(), m, n, k,
-                                out.data_ptr(), yd, wp, wb))
+    _call("tl_f8_gemm_approx" if approx else "tl_f8_gemm", index,
+          (codes.data_ptr(), scales.data_ptr(), x.data_ptr(), x_scales.data_ptr(), m, n, k, out.data_ptr(), yd, wp, wb))
     return out
 
 
 class F8Linear:
     """A linear layer with weights in 8-bit floating point, for the matrices
-    beside the ternary ones; ``forward`` rounds its input rows to the same form."""
+    beside the ternary ones; ``forward`` rounds its input rows to the same form.
+    ``approx`` as for ``f8_gemm``."""
 
-    def __init__(self, codes, scales):
-        self.codes, self.scales = codes, scales
+    def __init__(self, codes, scales, approx=False):
+        self.codes, self.scales, self.approx = codes, scales, approx
 
     def forward(self, x: torch.Tensor, out_dtype=torch.float32) -> torch.Tensor:
-        return f8_gemm(self.codes, self.scales, *f8_quantize(x), out_dtype)
+        return f8_gemm(self.codes, self.scales, *f8_quantize(x), out_dtype, approx=self.approx)
 
     __call__ = forward
 

@@ -110,6 +110,26 @@ tl_status check_rows(const void* codes, int64_t code_bytes, const void* scales, 
     return TL_OK;
 }
 
+// tl_f8_gemm and tl_f8_gemm_approx
+tl_status f8_product(const uint8_t* codes, const uint8_t* scales, const uint8_t* x, const uint8_t* x_scales,
+                     int64_t M, int64_t N, int64_t K, void* y, int32_t y_dtype, bool approx, void* workspace,
+                     int64_t workspace_bytes, hipStream_t stream) {
+    if (!codes || !scales || !x || !x_scales || !y) return TL_ERR_NULL;
+    if (!q4_product_shape_ok(M, N, K)) return TL_ERR_SHAPE;
+    if (!real_dtype(y_dtype)) return TL_ERR_DTYPE;
+    if (!aligned16(codes) || !aligned16(x) || !aligned16(y)) return TL_ERR_ALIGN;
+    const int64_t cb = N * K, sb = N * (K / TL_GROUP), xb = M * K, xsb = M * (K / TL_GROUP);
+    const int64_t yb = M * N * dtype_bytes(y_dtype);
+    if (overlap(y, yb, codes, cb) || overlap(y, yb, scales, sb) || overlap(y, yb, x, xb) ||
+        overlap(y, yb, x_scales, xsb))
+        return TL_ERR_ALIAS;
+    const tl_status st =
+        check_workspace(tl::f8_gemm_workspace_bytes(M, N, K), workspace, workspace_bytes,
+                        {{codes, cb}, {scales, sb}, {x, xb}, {x_scales, xsb}, {y, yb}});
+    if (st != TL_OK) return st;
+    return launched(tl::launch_f8_gemm(codes, scales, x, x_scales, M, N, K, y, y_dtype, approx, workspace, stream));
+}
+
 // TL_DEBUG=1: count the packed bytes that are not valid encodings before a
 // call that decodes them; a device int per GPU holds the count
 bool debug_on() {
@@ -491,20 +511,13 @@ int64_t tl_f8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
 tl_status tl_f8_gemm(const uint8_t* codes, const uint8_t* scales, const uint8_t* x, const uint8_t* x_scales,
                      int64_t M, int64_t N, int64_t K, void* y, int32_t y_dtype, void* workspace,
                      int64_t workspace_bytes, hipStream_t stream) {
-    if (!codes || !scales || !x || !x_scales || !y) return TL_ERR_NULL;
-    if (!q4_product_shape_ok(M, N, K)) return TL_ERR_SHAPE;
-    if (!real_dtype(y_dtype)) return TL_ERR_DTYPE;
-    if (!aligned16(codes) || !aligned16(x) || !aligned16(y)) return TL_ERR_ALIGN;
-    const int64_t cb = N * K, sb = N * (K / TL_GROUP), xb = M * K, xsb = M * (K / TL_GROUP);
-    const int64_t yb = M * N * dtype_bytes(y_dtype);
-    if (overlap(y, yb, codes, cb) || overlap(y, yb, scales, sb) || overlap(y, yb, x, xb) ||
-        overlap(y, yb, x_scales, xsb))
-        return TL_ERR_ALIAS;
-    const tl_status st =
-        check_workspace(tl::f8_gemm_workspace_bytes(M, N, K), workspace, workspace_bytes,
-                        {{codes, cb}, {scales, sb}, {x, xb}, {x_scales, xsb}, {y, yb}});
-    if (st != TL_OK) return st;
-    return launched(tl::launch_f8_gemm(codes, scales, x, x_scales, M, N, K, y, y_dtype, workspace, stream));
+    return f8_product(codes, scales, x, x_scales, M, N, K, y, y_dtype, false, workspace, workspace_bytes, stream);
+}
+
+tl_status tl_f8_gemm_approx(const uint8_t* codes, const uint8_t* scales, const uint8_t* x, const uint8_t* x_scales,
+                            int64_t M, int64_t N, int64_t K, void* y, int32_t y_dtype, void* workspace,
+                            int64_t workspace_bytes, hipStream_t stream) {
+    return f8_product(codes, scales, x, x_scales, M, N, K, y, y_dtype, true, workspace, workspace_bytes, stream);
 }
 
 tl_status tl_q4_rows(const uint8_t* packed, const uint16_t* scales, int32_t group, const int32_t* ids,

@@ -151,7 +151,8 @@ hipError_t launch_q4_gemv(const uint8_t* packed, const uint16_t* scales, int gro
                           int y_dtype, void* ws, hipStream_t stream);
 
 // 8-bit floating point rows with block scales: rounding, values, and the
-// product of rows with weights (when f8_gemv_fits; any number)
+// product of rows with weights (when f8_gemv_fits; any number; approx: 16-bit
+// outputs may come from the 8-bit matrix instructions' sums)
 hipError_t launch_f8_quantize(const void* x, int64_t m, int64_t k, int x_dtype, uint8_t* codes, uint8_t* scales,
                               hipStream_t stream);
 hipError_t launch_f8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t n, int64_t k, void* w,
@@ -161,7 +162,8 @@ hipError_t launch_f8_gemv(const uint8_t* codes, const uint8_t* scales, const uin
                           int64_t m, int64_t n, int64_t k, void* y, int y_dtype, hipStream_t stream);
 int64_t f8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k);
 hipError_t launch_f8_gemm(const uint8_t* codes, const uint8_t* scales, const uint8_t* x, const uint8_t* x_scales,
-                          int64_t m, int64_t n, int64_t k, void* y, int y_dtype, void* ws, hipStream_t stream);
+                          int64_t m, int64_t n, int64_t k, void* y, int y_dtype, bool approx, void* ws,
+                          hipStream_t stream);
 // Embedding rows of both kinds of tables
 hipError_t launch_q4_rows(const uint8_t* packed, const uint16_t* scales, int group, const int32_t* ids, int64_t m,
                           int64_t n, int64_t k, float factor, void* out, int out_dtype, hipStream_t stream);
