@@ -613,14 +613,21 @@ class Q4Linear:
     __call__ = forward
 
 
-_F8, _E8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+# (torch has the scales' type from 2.7 on; the other calls do without)
+_F8, _E8 = getattr(torch, "float8_e4m3fn", None), getattr(torch, "float8_e8m0fnu", None)
 _I32 = torch.int32
+
+
+def _no_f8_types():
+    raise RuntimeError(f"torch {torch.__version__} lacks float8_e4m3fn or float8_e8m0fnu, the types of 8-bit rows")
 
 
 def f8_quantize(x, codes=None, scales=None):
     """Rows x [M, K] (float32, float16 or bfloat16; weights or activations) to
     8-bit floating point with a power-of-two scale per 128: returns (codes
     float8_e4m3fn [M, K], scales float8_e8m0fnu [M, K/128]); value = code * scale."""
+    if _E8 is None or _F8 is None:
+        _no_f8_types()
     dt, shape, index = _rows(x, "x")
     m, k = shape
     if k % GROUP:
@@ -645,6 +652,8 @@ def _f8_shape(codes, scales, what="codes"):
     if not (isinstance(codes, torch.Tensor) and isinstance(scales, torch.Tensor)):
         raise TypeError(f"{what} and their scales must be torch.Tensors")
     if codes.dtype is not _F8 or scales.dtype is not _E8:
+        if _E8 is None or _F8 is None:
+            _no_f8_types()
         raise TypeError(f"{what} must be float8_e4m3fn and their scales float8_e8m0fnu")
     index = codes.get_device()
     if index < 0 or scales.get_device() != index:
