@@ -448,8 +448,10 @@ TL_API tl_status tl_q4_gemv(const uint8_t* packed, const uint16_t* scales, int32
 TL_API tl_status tl_f8_quantize(const void* x, int64_t M, int64_t K, int32_t x_dtype, uint8_t* codes,
                                 uint8_t* scales, hipStream_t stream);
 
-/* The values of f8 rows, rounded to nearest even in out_dtype (exact in TL_F32,
- * and in TL_BF16 from 2^-126 up).  out: [M, K]; rules as tl_f8_quantize; out
+/* The values of f8 rows, rounded to nearest even in out_dtype: below 2^128 exact in
+ * TL_F32, and in TL_BF16 from 2^-126 up; infinity from 2^128 on, which only scales
+ * of 2^120 and more reach (of tl_f8_quantize's: x from 1.9375 * 2^127 on, whose
+ * nearest code stands for 2^128).  out: [M, K]; rules as tl_f8_quantize; out
  * overlaps neither input. */
 TL_API tl_status tl_f8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K, void* out,
                                   int32_t out_dtype, hipStream_t stream);
@@ -471,10 +473,10 @@ TL_API int64_t tl_f8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * nothing else.
  *   Products are exact, their sums fp32, for every type and size: a TL_F16 or
  * TL_BF16 output is the TL_F32 one rounded.
- *   code * scale must lie between 2^-126 and 2^127 (below, bits are lost; above,
- * infinity), products within fp32; a NaN code or scale gives NaN where it
- * enters.  A token's result does not depend on what the other tokens hold, and is
- * the same bits from call to call on one device. */
+ *   |code * scale| must be 0, or 2^-126 at least (below, bits are lost) and below
+ * 2^128 (from there on, infinity), products within fp32; a NaN code or scale gives
+ * NaN where it enters.  A token's result does not depend on what the other tokens
+ * hold, and is the same bits from call to call on one device. */
 TL_API tl_status tl_f8_gemm(const uint8_t* codes, const uint8_t* scales, const uint8_t* x,
                             const uint8_t* x_scales, int64_t M, int64_t N, int64_t K, void* y, int32_t y_dtype,
                             void* workspace, int64_t workspace_bytes, hipStream_t stream);
@@ -496,10 +498,11 @@ TL_API tl_status tl_f8_gemm_approx(const uint8_t* codes, const uint8_t* scales, 
 /* Embedding lookup in a q4 or an f8 table of N rows, times a factor:
  *   out[m, k] = w[ids[m], k] * factor
  * ids: int32 [M]; an id outside 0 .. N - 1 (padding) gives a row of zeros, any
- * may occur more than once.  The product is fp32, then rounded to nearest even
- * in out_dtype (TL_F32, TL_F16 or TL_BF16).  out: [M, K].  A q4 table must have
- * been rounded without the rotation.  Requires 1 <= M, N <= 2^24, 128 <= K <=
- * TL_MAX_K, K % 128 == 0, M * K and N * K <= 2^36; factor finite (TL_ERR_VALUE);
+ * may occur more than once.  w (of an f8 table infinity from 2^128 on) and the
+ * product are fp32, then rounded to nearest even in out_dtype (TL_F32, TL_F16 or
+ * TL_BF16).  out: [M, K].  A q4 table must have been rounded without the
+ * rotation.  Requires 1 <= M, N <= 2^24, 128 <= K <= TL_MAX_K, K % 128 == 0,
+ * M * K and N * K <= 2^36; factor finite (TL_ERR_VALUE);
  * group as tl_q4_quantize; every pointer 16-byte aligned, ids 4-byte, f8 scales
  * at any address; out overlaps nothing else. */
 TL_API tl_status tl_q4_rows(const uint8_t* packed, const uint16_t* scales, int32_t group, const int32_t* ids,
