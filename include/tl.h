@@ -27,8 +27,10 @@
  *     call returns TL_OK without synchronising.  A launch failure returns
  *     TL_ERR_LAUNCH and tl_last_error() gives the HIP error text (per thread).
  *   - The library keeps no state between calls apart from that per-thread
- *     error text and, per device, the compute-unit count and the kernels' LDS
- *     limits, looked up on first use; calls from several threads are safe.
+ *     error text, per thread the launch plans of tl_f8_gemm's last shapes (they
+ *     depend on nothing else) and, per device, the compute-unit count and the
+ *     kernels' LDS limits, looked up on first use; calls from several threads
+ *     are safe.
  *   - Debug checks: with the environment variable TL_DEBUG=1, tl_unpack,
  *     tl_gemv, tl_gemm, tl_gemm_bf16 and tl_linear first count the packed
  *     bytes that are not valid encodings (see Formats) on the device, wait
