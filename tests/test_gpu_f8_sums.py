@@ -23,9 +23,11 @@ from tests.test_gpu_f8 import TYPES, U, call, e4, e8, host, make
 
 pytestmark = pytest.mark.gpu
 
-# the kernel of few tokens, then every tile of the two others, whole, cut, and both
-SIZES = [(1, 300, 1280), (16, 515, 640), (17, 48, 2048), (64, 80, 4096), (128, 300, 5120), (32, 4096, 640),
-         (33, 2091, 128), (18, 17, 5248), (324, 5429, 128), (1094, 257, 3712), (17, 16444, 128), (17, 1259, 5760),
+# the kernel of few tokens, on both sides of where it ends, then every tile of the two
+# others, whole, cut, and both
+SIZES = [(1, 300, 1280), (16, 515, 640), (17, 48, 2048), (64, 80, 4096), (128, 300, 5120), (17, 1259, 5760),
+         (32, 4096, 640), (32, 4096, 8192), (33, 4096, 8192), (32, 4112, 8192), (32, 4096, 8320),
+         (33, 2091, 128), (18, 17, 8320), (324, 5429, 128), (1094, 257, 3712), (17, 16444, 128), (17, 4289, 1920),
          (33, 16585, 128), (35, 5893, 3712), (268, 19756, 128), (66, 11551, 5376), (391, 18909, 128),
          (193, 17209, 3456), (944, 16478, 640), (66, 2833, 4992), (65, 8228, 128), (19, 5519, 3200),
          (33, 5947, 5760), (65, 10910, 6400), (131, 16324, 128), (129, 11856, 7296), (1447, 10943, 640)]
@@ -94,7 +96,7 @@ def test_the_error_of_a_sum(gpu, m, n, k, outliers):
         assert float(got.square().mean().sqrt() / size.square().mean().sqrt()) <= 1e-4
 
 
-@pytest.mark.parametrize("m,n,k", [(40, 150, 7040), (66, 2833, 4992), (300, 5200, 7040), (1447, 10943, 640)])
+@pytest.mark.parametrize("m,n,k", [(40, 150, 8320), (66, 2833, 4992), (300, 5200, 7040), (1447, 10943, 640)])
 def test_approximate_sums_keep_14_bits(gpu, m, n, k):
     """1, 2^-13 and -1: what lies 2^-13 below is kept."""
     xv = torch.zeros(m, k, device=gpu)
@@ -105,6 +107,29 @@ def test_approximate_sums_keep_14_bits(gpu, m, n, k):
     assert bool((got == 2.0 ** -7).all())
 
 
+# ---------------------------------------------------------------- where the kernel of few tokens ends
+
+def test_small_products_need_no_workspace(gpu):
+    """Up to 256 workgroups of 16 weight rows by 32 tokens, K up to 8192."""
+    assert tl.f8_gemm_workspace_bytes(32, 1024, 8192) == 0 and tl.f8_gemm_workspace_bytes(128, 1024, 8192) == 0
+    assert tl.f8_gemm_workspace_bytes(32, 1024, 8320) > 0 and tl.f8_gemm_workspace_bytes(129, 1024, 8192) > 0
+    assert tl.f8_gemm_workspace_bytes(16, 1024, 1 << 20) == 0
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("m", [20, 100, 300])
+def test_tiles_of_a_long_k(gpu, m, out):
+    """The product's other tests, past the kernel of few tokens."""
+    f8.test_every_scale_reaches_its_block(gpu, m, out, 8320)
+    f8.test_nan_and_zero_stay_in_their_rows(gpu, m, out, 8320)
+    f8.test_scales_far_from_one(gpu, m, out, 8320)
+    f8.test_codes_count_and_none_is_missed(gpu, m, 270, 8320)
+    f8.test_rows_cut_out_of_others(gpu, m, 8320)
+    f8.test_nothing_behind_the_rows_is_written(gpu, m, 8320)
+    f8.test_same_bits_again_and_alone(gpu, m, 96, 8320)
+    f8.test_captured_and_replayed(gpu, m, 96, 8320, out)
+
+
 # ---------------------------------------------------------------- approx: the product's other tests
 
 @pytest.fixture
@@ -113,7 +138,7 @@ def approx(monkeypatch):
 
 
 @pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("m,n,k", [(1, 1000, 5120), (16, 515, 640), (64, 80, 4096), (65, 17, 5248), (129, 257, 640),
+@pytest.mark.parametrize("m,n,k", [(1, 1000, 5120), (16, 515, 640), (64, 80, 4096), (65, 17, 8320), (129, 257, 640),
                                    (200, 1, 896), (257, 259, 2176), (300, 1030, 1280), (20, 4200, 640), (33, 9000, 384),
                                    (100, 2100, 896), (200, 1500, 5248), (66, 8371, 256)])
 def test_approximate_products(gpu, approx, m, n, k, out):
@@ -126,7 +151,7 @@ def test_approximate_sums_of_whole_numbers(gpu, approx, m, n, k):
 
 
 @pytest.mark.parametrize("m", [20, 100, 300])
-@pytest.mark.parametrize("k", [1152, 5376])
+@pytest.mark.parametrize("k", [1152, 8320])
 def test_approximate_products_scales_and_nan(gpu, approx, m, k):
     f8.test_every_scale_reaches_its_block(gpu, m, "bf16", k)
     f8.test_nan_and_zero_stay_in_their_rows(gpu, m, "f16", k)
@@ -135,7 +160,7 @@ def test_approximate_products_scales_and_nan(gpu, approx, m, k):
     f8.test_nothing_behind_the_rows_is_written(gpu, m, k)
 
 
-@pytest.mark.parametrize("m,n,k", [(40, 96, 6016), (100, 4100, 1280), (300, 520, 6016)])
+@pytest.mark.parametrize("m,n,k", [(40, 96, 8448), (100, 4100, 1280), (300, 520, 6016)])
 def test_approximate_products_repeat_and_replay(gpu, approx, m, n, k):
     f8.test_same_bits_again_and_alone(gpu, m, n, k)
     f8.test_captured_and_replayed(gpu, m, n, k, "f16")

@@ -592,10 +592,14 @@ constexpr int64_t kMostSums = int64_t(1) << 28;
 // `each` us for every workgroup on it, `alone` where it has one; weights and activations
 // arrive at 6.1 bytes per ps, longer by half of what an uneven load leaves idle;
 // operands at 10 from the caches; the second kernel costs 3.3 us, 0.31 a part, and its
-// sums, written and read, 4.9 bytes per ps.  (us, tiles of 128 rows only and of 64 too:
-// 4096 x 4096 by 200 tokens 17.8 13.0, 8192 x 8192 by 200 41.0 33.6, 6144 x 5120 by 100
-// 20.6 17.1, 17408 x 5120 by 64 32.1 33.9.  17408 x 5120 by 64 in tiles of 64 tokens 30,
-// of 32 36; by 512 66 in tiles of 256 x 256, 87 in tiles of 128 x 128.)
+// sums, written and read, 4.9 bytes per ps.  us in a graph with fp32 sums, the plan's
+// choice and the next kind of tile: 17408 x 5120 by 64 tokens 31.8 (128 x 64 in 3 parts)
+// 36.2 (64 x 64), by 256 64.0 (256 x 256 in 3 parts) 70.7 (128 x 64), by 512 102.6 (256 x
+// 256) 112.9 (128 x 64); 4096 x 4096 by 200 17.5 (64 x 64) 18.4 (128 x 32); 32003 x 5120
+// by 320 126 (256 x 256) 131 (128 x 64).  With the 8-bit instructions' sums: 17408 x 5120
+// by 64 30.9 (128 x 64) 33.9 (64 x 64), by 512 68 (256 x 256) 88 (64 x 128).  Where it is
+// furthest off: 6144 x 5120 by 200 with fp32 sums 32.3 (128 x 128 in 5 parts), 27.5 (64 x
+// 64 whole).
 Plan make_plan(int64_t m, int64_t n, int64_t k, bool wide) {
     struct Kind {
         int rw, it;

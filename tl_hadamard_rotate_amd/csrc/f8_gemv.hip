@@ -218,13 +218,19 @@ hipError_t launch(Args a, int64_t waves, hipStream_t stream) {
 }  // namespace
 
 // More than 16 tokens come in blocks of 32 where the product is so small that the other
-// kernels would cut K and add the parts in a second launch (us in a graph, here and
-// there: 2048 x 2048 by 17, 64, 128 tokens 6.3 7.8, 6.9 8.6, 8.9 9.5; 1024 x 5120 by 17,
-// 32, 64, 128 8.2 8.5, 9.7 8.7, 9.8 9.6, 9.8 10.5; called one by one, with that launch
-// and its workspace, 16 x 2560 by 18 6.4 11.4).  Past 40 chunks, ten a wave, cutting K
-// further wins: 512 x 7168 by 32 tokens 10.4 8.5.
+// kernels would cut K and add the parts in a second launch: up to one workgroup a compute
+// unit and 64 chunks, eight a wave.  us in a graph, weights not in the caches, here and in
+// the others' tiles with fp32 sums: 2048 x 2048 by 17, 64 tokens 6.1 8.2, 6.8 9.1;
+// 1024 x 5120 by 17, 32, 64, 128 8.3 9.4, 9.6 9.7, 9.4 10.2, 9.5 10.9; 1024 x 7168 by 32,
+// 128 10.5 11.5, 10.4 13.1; 2048 x 8192 by 32, 64 11.6 12.5, 11.4 13.6.  The others are
+// ahead with 32 tokens and few rows (256 x 7168 10.2 9.9, 512 x 5120 9.3 8.4) and where
+// little K needs no cut (512 x 512 4.7 4.5, 4096 x 640 by 32 6.0 5.6); of more workgroups
+// (1024 x 7168 by 160 16.5 12.9, 1536 x 5120 by 80 13.0 11.2) and of longer rows (1024 x
+// 10240 by 32, 64 14.3 11.6, 14.2 12.3).  Called one by one, with that second launch and
+// its workspace, 16 x 2560 by 18 takes 11.4 there and 6.4 here.  The 8-bit instructions'
+// sums would gain little on it: 1024 x 5120 by 32, 64 9.2, 10.1.
 bool f8_gemv_fits(int64_t m, int64_t n, int64_t k) {
-    return m <= 16 || (k <= 5120 && ((n + 15) / 16) * ((m + 31) / 32) <= 256);
+    return m <= 16 || (k <= 8192 && ((n + 15) / 16) * ((m + 31) / 32) <= 256);
 }
 
 // Waves share a tile until there are about 1024 (512 where each brings 16 tokens'
