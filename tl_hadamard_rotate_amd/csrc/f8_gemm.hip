@@ -17,7 +17,7 @@
 //
 // Operands go from memory straight into LDS (global_load_lds), 128 bytes of each of
 // 8 rows a load: whole cache lines (half lines cost the address path twice the time,
-// 8192 x 8192 x 8192 438 us against 399).  A row's 128 bytes of a block lie together,
+// 8192 x 8192 x 8192 on the 8-bit instructions 438 us against 399).  A row's 128 bytes of a block lie together,
 // its 16-byte pieces exchanged by bits 1 .. 3 of the row, so that 16 rows read at one
 // piece meet all banks.  Waits and barriers are written out: the compiler would make
 // every LDS read wait for every load in flight.  Scales come as they lie in memory,
@@ -25,10 +25,13 @@
 //
 // Two kernels:
 //  - some tokens: 64 or 128 weight rows by 32, 64 or 128 tokens, 4 waves, two
-//    workgroups on a compute unit.  Bound by the weights' bytes.
+//    workgroups on a compute unit.  Up to some 64 tokens bound by the weights' bytes
+//    (17408 x 5120 by 64 24 us traced and 4 of joining, 93 MB), then by matrix
+//    instructions and by the sums of what is cut (by 256 52 and 11 us, 53 MB of sums).
 //  - many: 256 by 256, 8 waves, one workgroup.  Bound by the matrix cores' power: with
-//    zeros for data 8192 x 8192 x 8192 takes 295 us at 2.4 GHz, with random data 405 us
-//    at 1.7 GHz, 72 % of the cycles issuing matrix instructions.
+//    zeros for data 8192 x 8192 x 8192 takes 568 us, with random data 750 (on the 8-bit
+//    instructions 281 and 391); 4096 x 17408 x 5120 532 us (292), matrix instructions
+//    issuing in 75 % of the cycles (69 %) at about 1.75 GHz of 2.4.
 // Either is cut along K where tiles are few, into parts whose sums a second kernel
 // adds in order.
 #include "elem.h"
@@ -335,7 +338,7 @@ __global__ __launch_bounds__(kMidThreads) __attribute__((amdgpu_waves_per_eu(2))
 // are single: what a half of the block no longer needs is read for its next use, half
 // a phase ahead, so that matrix instructions wait for no LDS latency.  (Four waves of
 // 128 x 128 read a third less from LDS and take as long; 16 x 16 x 128 instructions
-// draw less power and take as long too.)
+// draw less power and take as long too: both on the 8-bit instructions.)
 
 constexpr int kThreads = 512, kRows = 256, kTokens = 256;
 constexpr int kSegment = 48, kPitch = 52;       // groups of scales in LDS, and their bytes a row
@@ -539,7 +542,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     // through LDS, 128 tokens by 64 weight rows a wave, so that a store writes whole cache
     // lines: piece e of 8 weight rows of a token in place e ^ (token / 2) % 8.  Straight
     // from the registers, 32 bytes of a token a store, 4096 x 17408 x 5120 takes 328 us
-    // instead of 309.  (Stores past the caches' replacement order: the same time here,
+    // instead of 309 on the 8-bit instructions.  (Stores past the caches' replacement order: the same time here,
     // and 1 to 3 us more for what reads y next.)
     asm volatile("s_barrier" ::: "memory");
     const auto place = [&](int token, int e) { return uint32_t(token) * 128u + 16u * uint32_t(e ^ ((token >> 1) & 7)); };

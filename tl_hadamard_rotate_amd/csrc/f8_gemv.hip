@@ -219,7 +219,7 @@ hipError_t launch(Args a, int64_t waves, hipStream_t stream) {
 
 // More than 16 tokens come in blocks of 32 where the product is so small that the other
 // kernels would cut K and add the parts in a second launch: up to one workgroup a compute
-// unit and 64 chunks, eight a wave.  us in a graph, weights not in the caches, here and in
+// unit and 64 chunks, sixteen a wave.  us in a graph, weights not in the caches, here and in
 // the others' tiles with fp32 sums: 2048 x 2048 by 17, 64 tokens 6.1 8.2, 6.8 9.1;
 // 1024 x 5120 by 17, 32, 64, 128 8.3 9.4, 9.6 9.7, 9.4 10.2, 9.5 10.9; 1024 x 7168 by 32,
 // 128 10.5 11.5, 10.4 13.1; 2048 x 8192 by 32, 64 11.6 12.5, 11.4 13.6.  The others are
